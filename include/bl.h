@@ -36,8 +36,9 @@ typedef struct CUstream_st *bl_stream_t;
 
 typedef enum { BL_LOWER = 0, BL_UPPER = 1 } bl_uplo;
 
-/* f32 = float, f64 = double, c64 = complex<float>, c128 = complex<double>. */
-typedef enum { BL_F32 = 0, BL_F64 = 1, BL_C64 = 2, BL_C128 = 3 } bl_dtype;
+/* f32 = float, f64 = double, c64 = complex<float>, c128 = complex<double>: the matrices'
+ * types. bf16 and f16 exist for the training operators (bl_xent*, bl_gnorm, bl_gclip) only. */
+typedef enum { BL_F32 = 0, BL_F64 = 1, BL_C64 = 2, BL_C128 = 3, BL_BF16 = 4, BL_F16 = 5 } bl_dtype;
 
 typedef enum {
     BL_SUCCESS = 0,
@@ -96,6 +97,98 @@ bl_status bl_posv(bl_uplo uplo, bl_dtype dtype, int64_t n, int64_t nrhs, int64_t
 bl_status bl_potrs(bl_uplo uplo, bl_dtype dtype, int64_t n, int64_t nrhs, int64_t batch,
                    const void *A, int64_t lda, int64_t stride_a, void *B, int64_t ldb,
                    int64_t stride_b, bl_stream_t stream);
+
+/*
+ * Training operators: what a block-preconditioned training step needs on either side of the
+ * solves. bl_xent and bl_xent_grad give the loss and the gradients, bl_posv preconditions them
+ * block by block, bl_gclip bounds the step.
+ */
+
+/*
+ * bl_gnorm -- the global norm sqrt(sum_i sum_j x_ij^2) of `count` tensors.
+ *
+ *   count     number of tensors, 0 <= count <= 2^24 (none: the norm is 0).
+ *   dtypes    HOST array: each tensor's type, BL_F32, BL_F64, BL_BF16 or BL_F16, in any mix.
+ *   x         HOST array of device pointers, each aligned to its element size.
+ *   sizes     HOST array: each tensor's number of elements, stored back to back; 0 is allowed
+ *             (its pointer is not looked at). 2^44 bytes in all at most.
+ *   norm      device float; receives the norm (NaN or infinity where the tensors hold any).
+ *             Squares are added in f32 over at most 32 values and in f64 from there on, and
+ *             nothing overflows or underflows on the way for f32, bf16 and f16 tensors; f64
+ *             tensors are squared in f64. The same call gives the same bits every time.
+ *   workspace device memory of at least bl_gnorm_workspace(count) bytes, 8-byte aligned, free
+ *             again once the call's work has completed on the stream.
+ * The host arrays are read before the call returns.
+ */
+bl_status bl_gnorm(int64_t count, const int32_t *dtypes, const void *const *x, const int64_t *sizes,
+                   float *norm, void *workspace, int64_t workspace_bytes, bl_stream_t stream);
+
+/*
+ * bl_gclip -- scale `count` tensors so that their global norm is at most max_norm:
+ * y_ij = c * x_ij with c = max_norm / norm where norm > max_norm, else 1. Where the norm is not
+ * finite c is 1 as well: the caller sees it in `norm` and skips the step.
+ *
+ *   y         HOST array of device pointers to the results, of x's types and sizes. y[i] may be
+ *             x[i] (in place; left untouched where c = 1) but overlaps no other input or output.
+ *   max_norm  >= 0, infinity allowed (copies).
+ *   norm      receives the norm BEFORE scaling. c is computed in f64 and rounded to f32 for f32,
+ *             bf16 and f16 tensors, whose products are rounded once to their type.
+ * Other arguments as bl_gnorm.
+ */
+bl_status bl_gclip(int64_t count, const int32_t *dtypes, const void *const *x, void *const *y,
+                   const int64_t *sizes, double max_norm, float *norm, void *workspace,
+                   int64_t workspace_bytes, bl_stream_t stream);
+
+/* Bytes of workspace that bl_gnorm and bl_gclip need for `count` tensors (-1: count is invalid). */
+int64_t bl_gnorm_workspace(int64_t count);
+
+/*
+ * bl_xent -- softmax cross entropy of `rows` tokens over a vocabulary, from the hidden vectors:
+ *     s_rv = sum_k H_rk W_vk,   lse_r = log sum_v exp(s_rv),   loss_r = lse_r - s_r,target(r)
+ * The logits s are never stored.
+ *
+ *   dtype     BL_BF16 or BL_F32, of H and W (and of the gradients). Products of bf16 values are
+ *             added in f32; f32 values are multiplied to f32 accuracy (three bf16 parts each).
+ *   rows      1 .. 2^22.    dim  1 .. 2^16.    vocab  1 .. 2^24.
+ *   H         one column per token: element k of token r at H + r*ldh + k, ldh >= dim.
+ *   W         one column per vocabulary entry: W + v*ldw + k, ldw >= dim. bf16 is read in place
+ *             where W and its columns start on 16-byte boundaries, and copied otherwise.
+ *   target    device int64[rows]. A target outside [0, vocab) marks a row that does not count: its
+ *             loss and lse are 0 and its column of H, whatever it holds, reaches no result.
+ *   loss, lse device float[rows].
+ *   workspace device memory of at least bl_xent_workspace(..., grad = 0) bytes, 256-byte aligned,
+ *             free again once the call's work has completed on the stream.
+ * The same call gives the same bits every time. A kernel that gave up waiting for an asynchronous
+ * copy or product (a device fault, not a numerical result) makes every loss NaN.
+ */
+bl_status bl_xent(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
+                  const void *W, int64_t ldw, const int64_t *target, float *loss, float *lse,
+                  void *workspace, int64_t workspace_bytes, bl_stream_t stream);
+
+/*
+ * bl_xent_grad -- its gradients: with P_rv = g_r (exp(s_rv - lse_r) - [v = target(r)]), and P_r = 0
+ * for a row that does not count,   dH = P W,   dW = P^T H.
+ *
+ *   lse       device float[rows], as bl_xent gave it for the same H, W and target.
+ *   g         device float[rows]: the gradient of what is minimised with respect to each row's
+ *             loss (1/rows for a mean). Not looked at where a row does not count.
+ *   dH, dW    the gradients, laid out as H and W (lddh, lddw >= dim), overwritten. Either may be
+ *             NULL: that product is skipped. They overlap no input.
+ *   workspace at least bl_xent_workspace(..., grad = 1) bytes.
+ * P is formed piece by piece of the vocabulary and rounded to bf16 for bf16 operands (relative
+ * 2^-9 an element, what the gradients themselves are rounded to); f32 operands keep it in f32.
+ * A kernel that gave up waiting makes dH NaN. Other arguments as bl_xent.
+ */
+bl_status bl_xent_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
+                       const void *W, int64_t ldw, const int64_t *target, const float *lse, const float *g,
+                       void *dH, int64_t lddh, void *dW, int64_t lddw, void *workspace,
+                       int64_t workspace_bytes, bl_stream_t stream);
+
+/* Bytes of workspace that bl_xent (grad = 0) or bl_xent_grad (grad = 1) needs on the current
+ * device for these arguments; -1 if they are invalid (see bl_last_error()). Of W only the
+ * address is looked at. */
+int64_t bl_xent_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw,
+                          int grad);
 
 /* Static, human-readable name of a status code. */
 const char *bl_status_string(bl_status status);

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdarg>
@@ -28,22 +29,16 @@
 #include <tuple>
 #include <vector>
 
+#include "host.h"
 #include "registry.h"
 
 #include "_tuned_tables.inc"  // kTunedTables[]: {name, text}, generated from tuned/*.txt
 
 namespace {
-
-using bl::KernelEntry;
-
-constexpr int64_t kMaxN = int64_t(1) << 20;
-constexpr int64_t kMaxBatch = (int64_t(1) << 31) - 1;
-
 thread_local std::string t_error;
-thread_local std::string t_choice;
-thread_local std::map<std::string, std::string> t_pins;  // op -> spelling ("" = none)
+}  // namespace
 
-bl_status fail(bl_status st, const char *fmt, ...) {
+bl_status bl::fail(bl_status st, const char *fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -52,6 +47,29 @@ bl_status fail(bl_status st, const char *fmt, ...) {
     t_error = buf;
     return st;
 }
+
+void bl::clear_error() { t_error.clear(); }
+
+int bl::sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (v = known[dev].load()) > 0) return v;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(v);
+    return v;
+}
+
+namespace {
+
+using bl::fail;
+using bl::KernelEntry;
+
+constexpr int64_t kMaxN = int64_t(1) << 20;
+constexpr int64_t kMaxBatch = (int64_t(1) << 31) - 1;
+
+thread_local std::string t_choice;
+thread_local std::map<std::string, std::string> t_pins;  // op -> spelling ("" = none)
 
 const char *dtype_name(int d) {
     static const char *names[] = {"f32", "f64", "c64", "c128"};

@@ -1,0 +1,390 @@
+// Global gradient norm over many tensors, and clipping to a norm.
+//
+//   norm = sqrt(sum_i sum_j x_ij^2),   y_ij = c * x_ij,   c = norm > max_norm ? max_norm / norm : 1
+//
+// (c = 1 too where the norm is not finite.) The norm reads every element once and does one
+// multiply-add each, so HBM bandwidth bounds it; clipping reads every element twice and writes it
+// once. Two launches whatever the number of tensors (up to kMany per launch): the sum kernel
+// leaves one f64 partial sum per CTA, and every CTA of the second kernel adds those partials in
+// the same order, so no atomics are needed and the result does not depend on the schedule.
+//
+// The tensors' pointers and sizes travel in the kernel's parameters (no host-to-device copy, and
+// the call can be captured in a graph). Each tensor is cut into 16 KB chunks that start on a
+// 16-byte boundary of memory, wherever the tensor itself starts; a CTA takes a contiguous run of
+// chunks, finds its first tensor by bisection and then walks.
+//
+// Squares are summed in f32 over the 16 or 32 values that a thread holds of one chunk and in f64
+// from there on. Where that f32 sum leaves [1e-20, 1e30] (squares that overflow, or underflow to
+// nothing) the thread adds the same values again in f64: the range of f32 and bf16 is safe, at no
+// cost to ordinary data.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "host.h"
+
+namespace bl {
+namespace grads {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;                                    // 16-byte loads a thread has in flight
+constexpr int kChunk = kThreads * kVecs * 16;               // 16 KB
+constexpr int kCtasPerSm = 4;
+constexpr int kFew = 64, kMany = 1000;                      // tensors per launch: two sizes of the parameter block
+constexpr int kMaxPartials = 4096;                          // CTAs of one sum launch, at most
+
+template <int MAXT>
+struct Tensors {
+    const void *x[MAXT];
+    void *y[MAXT];
+    int64_t n[MAXT];
+    int first[MAXT + 1];      // first chunk of each tensor; first[count] = all chunks
+    uint8_t dtype[MAXT];
+    int count;
+};
+
+// One 16-byte vector's values as floats (f64: as doubles).
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+    using Wide = float;
+    __device__ static float up(float v) { return v; }
+    __device__ static float down(float v) { return v; }
+};
+template <> struct Elem<double> {
+    using Wide = double;
+    __device__ static double up(double v) { return v; }
+    __device__ static double down(double v) { return v; }
+};
+template <> struct Elem<__nv_bfloat16> {
+    using Wide = float;
+    __device__ static float up(__nv_bfloat16 v) { return __bfloat162float(v); }
+    __device__ static __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Elem<__half> {
+    using Wide = float;
+    __device__ static float up(__half v) { return __half2float(v); }
+    __device__ static __half down(float v) { return __float2half_rn(v); }
+};
+
+template <typename T>
+union Vec {
+    static constexpr int N = 16 / sizeof(T);
+    uint4 q;
+    T e[N];
+    __device__ Vec() {}
+};
+
+// The part of a tensor that one chunk covers: bytes [lo, hi) of memory, `base` 16-byte aligned.
+struct Span {
+    uintptr_t base, lo, hi;
+};
+__device__ __forceinline__ Span span_of(const void *x, int64_t bytes, int64_t k) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(x), a = p & ~uintptr_t(15);
+    Span s;
+    s.base = a + static_cast<uintptr_t>(k) * kChunk;
+    s.lo = s.base > p ? s.base : p;
+    const uintptr_t end = p + static_cast<uintptr_t>(bytes), stop = s.base + kChunk;
+    s.hi = stop < end ? stop : end;
+    return s;
+}
+
+// Load the vector at byte address a; elements outside [lo, hi) read as zero and touch no memory.
+template <typename T>
+__device__ __forceinline__ void load(Vec<T> &v, uintptr_t a, const Span &s) {
+    if (a >= s.lo && a + 16 <= s.hi) {
+        v.q = *reinterpret_cast<const uint4 *>(a);
+    } else {
+        v.q = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i) {
+            const uintptr_t b = a + i * sizeof(T);
+            if (b >= s.lo && b < s.hi) v.e[i] = *reinterpret_cast<const T *>(b);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_sum(const Span &s) {
+    Vec<T> v[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) load(v[u], s.base + (u * kThreads + threadIdx.x) * 16, s);
+    typename Elem<T>::Wide acc = 0;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i) {
+            const typename Elem<T>::Wide w = Elem<T>::up(v[u].e[i]);
+            acc += w * w;
+        }
+    if constexpr (sizeof(typename Elem<T>::Wide) == 4) {
+        if (!(acc >= 1e-20f && acc <= 1e30f)) {       // also taken by all-zero and NaN values
+            uint32_t any = 0;
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u) any |= v[u].q.x | v[u].q.y | v[u].q.z | v[u].q.w;
+            if (any == 0) return 0.0;
+            double d = 0.0;
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+                for (int i = 0; i < Vec<T>::N; ++i) {
+                    const double w = static_cast<double>(Elem<T>::up(v[u].e[i]));
+                    d = fma(w, w, d);
+                }
+            return d;
+        }
+    }
+    return static_cast<double>(acc);
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const Span &s, const void *x, void *y, double c) {
+    const typename Elem<T>::Wide cw = static_cast<typename Elem<T>::Wide>(c);
+    const intptr_t shift = reinterpret_cast<intptr_t>(y) - reinterpret_cast<intptr_t>(x);
+    const bool together = (shift & 15) == 0;
+    Vec<T> v[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) load(v[u], s.base + (u * kThreads + threadIdx.x) * 16, s);
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+        const uintptr_t a = s.base + (u * kThreads + threadIdx.x) * 16;
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i) v[u].e[i] = Elem<T>::down(Elem<T>::up(v[u].e[i]) * cw);
+        if (together && a >= s.lo && a + 16 <= s.hi) {
+            *reinterpret_cast<uint4 *>(a + shift) = v[u].q;
+        } else {
+#pragma unroll
+            for (int i = 0; i < Vec<T>::N; ++i) {
+                const uintptr_t b = a + i * sizeof(T);
+                if (b >= s.lo && b < s.hi) *reinterpret_cast<T *>(b + shift) = v[u].e[i];
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ double block_sum(double v, double *slots) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) t += slots[w];
+    __syncthreads();
+    return t;
+}
+
+__device__ __forceinline__ int64_t elem_bytes(int dtype) {
+    return dtype == BL_F64 ? 8 : dtype == BL_F32 ? 4 : 2;
+}
+
+// The tensor that chunk k belongs to: the last one whose first chunk is <= k.
+template <int MAXT>
+__device__ __forceinline__ int tensor_of(const Tensors<MAXT> &t, int k) {
+    int lo = 0, hi = t.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.first[mid] <= k) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+template <int MAXT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    grads_sum_kernel(const __grid_constant__ Tensors<MAXT> t, double *partials) {
+    __shared__ double slots[kThreads / 32];
+    const int64_t chunks = t.first[t.count];
+    const int k0 = static_cast<int>(chunks * blockIdx.x / gridDim.x);
+    const int k1 = static_cast<int>(chunks * (blockIdx.x + 1) / gridDim.x);
+    double acc = 0.0;
+    int i = k0 < k1 ? tensor_of(t, k0) : 0;
+    for (int k = k0; k < k1; ++k) {
+        while (k >= t.first[i + 1]) ++i;
+        const int dt = t.dtype[i];
+        const Span s = span_of(t.x[i], t.n[i] * elem_bytes(dt), k - t.first[i]);
+        if (dt == BL_F32) acc += chunk_sum<float>(s);
+        else if (dt == BL_BF16) acc += chunk_sum<__nv_bfloat16>(s);
+        else if (dt == BL_F16) acc += chunk_sum<__half>(s);
+        else acc += chunk_sum<double>(s);
+    }
+    acc = block_sum(acc, slots);
+    if (threadIdx.x == 0) partials[blockIdx.x] = acc;
+}
+
+__device__ __forceinline__ double total_of(const double *partials, int count, double *slots) {
+    double acc = 0.0;
+    for (int i = threadIdx.x; i < count; i += kThreads) acc += partials[i];
+    return block_sum(acc, slots);
+}
+
+__global__ void __launch_bounds__(kThreads) grads_norm_kernel(const double *partials, int count, float *norm) {
+    __shared__ double slots[kThreads / 32];
+    const double sum = total_of(partials, count, slots);
+    if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(sum));
+}
+
+template <int MAXT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    grads_scale_kernel(const __grid_constant__ Tensors<MAXT> t, const double *partials, int count, double max_norm,
+                       float *norm) {
+    __shared__ double slots[kThreads / 32];
+    const double all = sqrt(total_of(partials, count, slots));
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(all);
+    const double c = (all > max_norm && isfinite(all)) ? max_norm / all : 1.0;
+    const int64_t chunks = t.first[t.count];
+    const int k0 = static_cast<int>(chunks * blockIdx.x / gridDim.x);
+    const int k1 = static_cast<int>(chunks * (blockIdx.x + 1) / gridDim.x);
+    int i = k0 < k1 ? tensor_of(t, k1 - 1) : 0;
+    // backwards: what the sum kernel read last is what L2 still holds
+    for (int k = k1 - 1; k >= k0; --k) {
+        while (k < t.first[i]) --i;
+        if (c == 1.0 && t.x[i] == t.y[i]) continue;        // in place and nothing to change
+        const int dt = t.dtype[i];
+        const Span s = span_of(t.x[i], t.n[i] * elem_bytes(dt), k - t.first[i]);
+        if (dt == BL_F32) chunk_scale<float>(s, t.x[i], t.y[i], c);
+        else if (dt == BL_BF16) chunk_scale<__nv_bfloat16>(s, t.x[i], t.y[i], c);
+        else if (dt == BL_F16) chunk_scale<__half>(s, t.x[i], t.y[i], c);
+        else chunk_scale<double>(s, t.x[i], t.y[i], c);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+int64_t host_bytes(int dtype) { return dtype == BL_F64 ? 8 : dtype == BL_F32 ? 4 : 2; }
+
+int64_t chunks_of(const void *x, int64_t n, int dtype) {
+    const int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(x) & 15);
+    return n == 0 ? 0 : (off + n * host_bytes(dtype) + kChunk - 1) / kChunk;
+}
+
+bl_status check(const char *op, int64_t count, const int32_t *dtypes, const void *const *x, void *const *y, bool clip,
+                const int64_t *sizes, double max_norm, const float *norm, const void *ws, int64_t ws_bytes) {
+    if (count < 0 || count > (int64_t(1) << 24))
+        return fail(BL_ERR_INVALID_ARGUMENT, "%s: count=%lld outside [0, 2^24]", op, (long long)count);
+    if (count > 0 && (!dtypes || !x || !sizes || (clip && !y)))
+        return fail(BL_ERR_INVALID_ARGUMENT, "%s: a list is NULL", op);
+    if (!norm || reinterpret_cast<uintptr_t>(norm) % 4 != 0)
+        return fail(BL_ERR_INVALID_ARGUMENT, "%s: norm is NULL or not 4-byte aligned", op);
+    const int64_t need = bl_gnorm_workspace(count);
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 8 != 0 || ws_bytes < need)
+        return fail(BL_ERR_INVALID_ARGUMENT, "%s: workspace is NULL, not 8-byte aligned or smaller than %lld bytes", op,
+                    (long long)need);
+    if (clip && !(max_norm >= 0.0)) return fail(BL_ERR_INVALID_ARGUMENT, "%s: max_norm=%g is not >= 0", op, max_norm);
+    int64_t all = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const int d = dtypes[i];
+        if (d != BL_F32 && d != BL_F64 && d != BL_BF16 && d != BL_F16)
+            return fail(BL_ERR_INVALID_ARGUMENT, "%s: tensor %lld has dtype %d, not f32, f64, bf16 or f16", op, (long long)i, d);
+        if (sizes[i] < 0 || sizes[i] > (int64_t(1) << 40))
+            return fail(BL_ERR_INVALID_ARGUMENT, "%s: tensor %lld has %lld elements", op, (long long)i, (long long)sizes[i]);
+        if (sizes[i] == 0) continue;
+        if ((all += sizes[i] * host_bytes(d)) > (int64_t(1) << 44))
+            return fail(BL_ERR_INVALID_ARGUMENT, "%s: the tensors hold more than 2^44 bytes", op);
+        const uintptr_t es = static_cast<uintptr_t>(host_bytes(d));
+        if (!x[i] || reinterpret_cast<uintptr_t>(x[i]) % es != 0)
+            return fail(BL_ERR_INVALID_ARGUMENT, "%s: tensor %lld is NULL or not aligned to its element", op, (long long)i);
+        if (clip && (!y[i] || reinterpret_cast<uintptr_t>(y[i]) % es != 0))
+            return fail(BL_ERR_INVALID_ARGUMENT, "%s: output %lld is NULL or not aligned to its element", op, (long long)i);
+        if (clip && x[i] != y[i]) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(x[i]), b = reinterpret_cast<uintptr_t>(y[i]);
+            const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * es;
+            if (a < b + bytes && b < a + bytes)
+                return fail(BL_ERR_INVALID_ARGUMENT, "%s: output %lld overlaps its input without being it", op, (long long)i);
+        }
+    }
+    return BL_SUCCESS;
+}
+
+// Fill the parameter block with tensors [from, ...): as many as fit, none that is empty. Returns
+// the first tensor that was not taken. (2^44 bytes are 2^30 chunks: an int holds them.)
+template <int MAXT>
+int64_t fill(Tensors<MAXT> &t, int64_t from, int64_t count, const int32_t *dtypes, const void *const *x,
+             void *const *y, const int64_t *sizes) {
+    t.count = 0;
+    t.first[0] = 0;
+    int64_t i = from;
+    for (; i < count && t.count < MAXT; ++i) {
+        if (sizes[i] == 0) continue;
+        t.x[t.count] = x[i];
+        t.y[t.count] = y ? y[i] : nullptr;
+        t.n[t.count] = sizes[i];
+        t.dtype[t.count] = static_cast<uint8_t>(dtypes[i]);
+        t.first[t.count + 1] = t.first[t.count] + static_cast<int>(chunks_of(x[i], sizes[i], dtypes[i]));
+        ++t.count;
+    }
+    return i;
+}
+
+template <int MAXT>
+cudaError_t run(int64_t count, const int32_t *dtypes, const void *const *x, void *const *y, const int64_t *sizes,
+                double max_norm, float *norm, double *partials, int sms, cudaStream_t s) {
+    Tensors<MAXT> t;
+    int done = 0;
+    bool one = false;
+    for (int64_t i = 0; i < count;) {
+        const int64_t from = i;
+        i = fill(t, i, count, dtypes, x, y, sizes);
+        one = from == 0 && i == count;
+        if (t.count == 0) continue;
+        const int grid = static_cast<int>(std::min<int64_t>(std::min(sms * kCtasPerSm, kMaxPartials), t.first[t.count]));
+        grads_sum_kernel<MAXT><<<grid, kThreads, 0, s>>>(t, partials + done);
+        done += grid;
+    }
+    if (!y || done == 0) {
+        grads_norm_kernel<<<1, kThreads, 0, s>>>(partials, done, norm);
+        return cudaGetLastError();
+    }
+    bool first = true;
+    for (int64_t i = 0; i < count;) {
+        if (!one) i = fill(t, i, count, dtypes, x, y, sizes);
+        else i = count;                                  // the block is filled already
+        if (t.count == 0) continue;
+        const int grid = static_cast<int>(std::min<int64_t>(sms * kCtasPerSm, t.first[t.count]));
+        grads_scale_kernel<MAXT><<<grid, kThreads, 0, s>>>(t, partials, done, max_norm, first ? norm : nullptr);
+        first = false;
+    }
+    return cudaGetLastError();
+}
+
+bl_status entry(const char *op, int64_t count, const int32_t *dtypes, const void *const *x, void *const *y, bool clip,
+                const int64_t *sizes, double max_norm, float *norm, void *ws, int64_t ws_bytes, bl_stream_t stream) {
+    clear_error();
+    const bl_status st = check(op, count, dtypes, x, y, clip, sizes, max_norm, norm, ws, ws_bytes);
+    if (st != BL_SUCCESS) return st;
+    const int sms = sm_count();
+    if (sms <= 0) return fail(BL_ERR_CUDA, "%s: cannot query the current CUDA device", op);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    double *partials = static_cast<double *>(ws);
+    const cudaError_t e = count <= kFew ? run<kFew>(count, dtypes, x, clip ? y : nullptr, sizes, max_norm, norm, partials, sms, s)
+                                        : run<kMany>(count, dtypes, x, clip ? y : nullptr, sizes, max_norm, norm, partials, sms, s);
+    if (e != cudaSuccess) return fail(BL_ERR_CUDA, "%s launch failed: %s", op, cudaGetErrorString(e));
+    return BL_SUCCESS;
+}
+
+}  // namespace grads
+}  // namespace bl
+
+extern "C" {
+
+int64_t bl_gnorm_workspace(int64_t count) {
+    using namespace bl::grads;
+    if (count < 0 || count > (int64_t(1) << 24)) return -1;
+    // one launch's partial sums, for each launch that the list takes
+    return 8 * static_cast<int64_t>(kMaxPartials) * (1 + count / kMany);
+}
+
+bl_status bl_gnorm(int64_t count, const int32_t *dtypes, const void *const *x, const int64_t *sizes, float *norm,
+                   void *workspace, int64_t workspace_bytes, bl_stream_t stream) {
+    return bl::grads::entry("gnorm", count, dtypes, x, nullptr, false, sizes, 0.0, norm, workspace, workspace_bytes, stream);
+}
+
+bl_status bl_gclip(int64_t count, const int32_t *dtypes, const void *const *x, void *const *y, const int64_t *sizes,
+                   double max_norm, float *norm, void *workspace, int64_t workspace_bytes, bl_stream_t stream) {
+    return bl::grads::entry("gclip", count, dtypes, x, y, true, sizes, max_norm, norm, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

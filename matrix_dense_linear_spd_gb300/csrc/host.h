@@ -1,0 +1,15 @@
+// Host-side helpers shared by the C entry points.
+#pragma once
+
+#include "../../include/bl.h"
+
+namespace bl {
+
+// Record a printf-style message for bl_last_error and return `st`.
+bl_status fail(bl_status st, const char *fmt, ...);
+// Forget the previous call's message (every entry point starts with it).
+void clear_error();
+// SMs of the current device (cached per device); 0 if it cannot be queried.
+int sm_count();
+
+}  // namespace bl
