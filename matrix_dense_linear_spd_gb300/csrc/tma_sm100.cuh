@@ -31,6 +31,17 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(mbar)) : "memory");
 }
 
+// Move registers between the block's warpgroups (every warp of a group executes it; the groups'
+// shares together must not exceed what the block was launched with).
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 // Shared-memory matrix descriptor of an MN-major tile: consecutive groups of 8 k lie 1024 bytes
 // apart (stride offset), consecutive groups of 64 M or N values `group` bytes apart (leading
 // offset); version and swizzle bits as in sdesc_sw128.

@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ plan
 
+// K is added in tensor memory over so many 64-deep steps at a time where the result is f32
+constexpr int kChunkF32 = 4, kChunkLoss = 8, kWhole = 1 << 30;
 constexpr int64_t kPieceBytes = int64_t(512) << 20;     // of P, and of a piece's copy of W
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -129,7 +131,7 @@ struct Plan {
     int64_t rows, dim, vocab;
     int64_t ldp;              // row length of the copies of H and W
     int64_t piece, pieces;    // vocabulary entries per piece
-    int64_t tiles_v;          // 256-wide tiles of the whole vocabulary
+    int64_t part_ld;          // partial maxima and sums of a row: two per tile
     int splits;
     int64_t kb_per_split;     // 64-deep steps of one part of dH
     int64_t ldo;              // row length of dH's partial sums
@@ -155,7 +157,7 @@ Plan plan_for(int dtype, int64_t rows, int64_t dim, int64_t vocab, const void *W
     q.pieces = cdiv(vocab, most);
     q.piece = up(cdiv(vocab, q.pieces), kTileN);
     q.pieces = cdiv(vocab, q.piece);
-    q.tiles_v = cdiv(vocab, kTileN);
+    q.part_ld = 2 * cdiv(vocab, kTileN);
     // dH has few tiles and a long K axis (the piece): cut K until there is work for every SM
     const int64_t tiles = cdiv(rows, kTileM) * cdiv(dim, kTileN), kb = cdiv(std::min(q.piece, vocab), kTileK);
     const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(sms / tiles, kb / 4));
@@ -172,7 +174,7 @@ Plan plan_for(int dtype, int64_t rows, int64_t dim, int64_t vocab, const void *W
     q.h = take(q.planes * rows * q.ldp * 2);
     if (q.copy_w) q.w = take(q.planes * std::min(q.piece, vocab) * q.ldp * 2);
     if (!grad) {
-        q.part = take(rows * q.tiles_v * 8);
+        q.part = take(rows * q.part_ld * 8);
         q.picked = take(rows * 4);
     } else {
         q.p = take(q.planes * rows * q.piece * 2);
@@ -284,6 +286,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     base.target = c.target;
     base.vocab = c.vocab;
     base.splits = 1;
+    base.chunk = PLANES == 3 ? kChunkF32 : kWhole;
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t v0 = i * q.piece, n = std::min(q.piece, c.vocab - v0);
         const char *const w_at = static_cast<const char *>(c.W) + v0 * c.ldw * static_cast<int64_t>(sizeof(T));
@@ -306,8 +309,9 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         a.tiles_n = static_cast<int>(cdiv(n, kTileN));
         a.v0 = static_cast<int>(v0);
         if (!q.grad) {
-            a.part = reinterpret_cast<float2 *>(c.ws + q.part) + v0 / kTileN;
-            a.part_ld = q.tiles_v;
+            if (PLANES == 1) a.chunk = kChunkLoss;
+            a.part = reinterpret_cast<float2 *>(c.ws + q.part) + 2 * (v0 / kTileN);
+            a.part_ld = q.part_ld;
             a.picked = reinterpret_cast<float *>(c.ws + q.picked);
             BL_TRY((launch_gemm<LOGITS, PLANES>(h_k, w_k, a, c.sms, c.s)));
             continue;
@@ -356,7 +360,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     }
     if (!q.grad) {
         loss_kernel<<<static_cast<unsigned>(cdiv(c.rows, 8)), 256, 0, c.s>>>(
-            reinterpret_cast<const float2 *>(c.ws + q.part), q.tiles_v, reinterpret_cast<const float *>(c.ws + q.picked),
+            reinterpret_cast<const float2 *>(c.ws + q.part), q.part_ld, reinterpret_cast<const float *>(c.ws + q.picked),
             c.target, c.vocab, static_cast<int>(c.rows), status, c.loss, c.lse);
         BL_TRY(cudaGetLastError());
     } else if (c.dH) {

@@ -7,12 +7,17 @@
 //
 // A CTA computes 128 x 256 tiles. One thread streams 64-deep operand tiles into a ring of shared
 // memory by TMA, one thread issues tcgen05.mma (bf16 operands, f32 accumulators in tensor
-// memory), and four warps turn finished accumulators into the mode's output while the next tile's
+// memory), and eight warps turn finished accumulators into the mode's output while the next tile's
 // products already run: tensor memory holds two accumulators of 256 columns.
 //
 // f32 operands are three bf16 planes each, x = x0 + x1 + x2 (8 bits of the 24-bit mantissa in
 // each), and six of the nine plane products are added, the ones above 2^-25 of the result,
 // smallest first. That costs as much tensor time as three tf32 products and is closer to f32.
+//
+// The tensor cores' f32 accumulation cuts where f32 would round, so a long chain of products is
+// biased towards zero, by about 2^-25 of the sum a step. Where the result is f32 (the loss; every
+// product of f32 operands) the chain is cut into chunks of K, whose sums are added in registers.
+// Measured at rows 1024, dim 1024, vocabulary 32000, f32: dH 9.6e-6 off without chunks.
 //
 // Every wait is bounded: a role that gives up marks *status, waits (bounded) for its own copies
 // and products in flight, and leaves; the others then run out of time too.
@@ -21,6 +26,7 @@
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "tma_sm100.cuh"
 
@@ -32,10 +38,15 @@ enum Mode : int { LOGITS = 0, PROBS = 1, DH = 2, DW = 3 };
 constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
 constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2;
 constexpr int kStages = 4;
-constexpr int kStageRow = 33;                                   // f32 words per row of the store staging
-constexpr int kStagingBytes = 4 * 32 * kStageRow * 4;
+constexpr int kEpilogueWarps = 8, kHalf = kTileN / 2;           // two warps share 32 rows: 128 columns each
+constexpr int kStageRow = 17;                                   // f32 words per row of the store staging
+constexpr int kStagingBytes = kEpilogueWarps * 32 * kStageRow * 4;
 constexpr int kSmem = kStages * (kBytesA + kBytesB) + kStagingBytes + 1024;
-constexpr int kThreads = 192;                                   // producer, issuer, four epilogue warps
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;             // producer, issuer (and two idle warps), epilogue
+// 384 threads start with 168 registers each; the first four warps give most of theirs to the
+// epilogue, whose rows hold 128 sums: 128 * 40 + 256 * 232 = 384 * 168.
+constexpr int kRegsLaunch = 168, kRegsFew = 40, kRegsMany = 232;
+static_assert(128 * kRegsFew + 32 * kEpilogueWarps * kRegsMany <= kThreads * kRegsLaunch, "more registers than the block has");
 constexpr uint32_t kPolls = 1u << 22;
 constexpr int kGroupM = 16;                                     // row tiles that share a column of B tiles
 constexpr float kLog2e = 1.4426950408889634f;
@@ -43,6 +54,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct GemmArgs {
     int m, n;                  // rows and columns of the product
     int kblocks;               // 64-deep steps of one pair of planes
+    int chunk;                 // of them, how many are added in tensor memory before registers take over
     int tiles_m, tiles_n;
     int splits, kb_per_split;  // DH: the K axis is cut and every part has its own partial sums
     int pairs;                 // pairs of planes multiplied, 1 or 6
@@ -113,146 +125,156 @@ __device__ __forceinline__ void split3(float x, float &x0, float &x1, float &x2)
     x2 = fine ? __bfloat162float(__float2bfloat16_rn(r - x1)) : 0.f;
 }
 
-// ---- epilogues: the warp's 32 rows (one per lane), 32 columns per tensor-memory read
+// ---- epilogues. A warp owns 32 rows (a lane each) and 128 columns, in blocks of 32 columns.
 
-__device__ __forceinline__ void epilogue_logits(const GemmArgs &a, const Work &w, uint32_t acc, int row) {
-    const int n0 = w.tn * kTileN, left = a.n - n0;
-    const int64_t t = row < a.m ? a.target[row] : -1;
-    const int64_t at64 = t - a.v0 - n0;
-    const int at = (t >= 0 && t < a.vocab && at64 >= 0 && at64 < min(left, kTileN)) ? static_cast<int>(at64) : -1;
-    float top = -INFINITY, sum = 0.f, picked = 0.f;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kTileN && c0 < left; c0 += 32) {
-        float v[32];
-        __syncwarp();
-        tc::tmem_ld32(acc + c0, v);
-        if (left - c0 < 32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = i < left - c0 ? v[i] : -INFINITY;
+struct Row {              // what an epilogue keeps of its row
+    int row, at;          // row of the product; the target's column within this tile or -1
+    bool counted;
+    float top, sum, picked;    // LOGITS
+    float lse, ref, g;         // PROBS
+};
+
+template <int MODE>
+__device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Work &w, int row) {
+    r.row = row;
+    if constexpr (MODE == LOGITS || MODE == PROBS) {
+        const int n0 = w.tn * kTileN;
+        const int64_t t = row < a.m ? a.target[row] : -1, at = t - a.v0 - n0;
+        r.counted = t >= 0 && t < a.vocab;
+        r.at = r.counted && at >= 0 && at < min(a.n - n0, kTileN) ? static_cast<int>(at) : -1;
+        r.top = -INFINITY;
+        r.sum = r.picked = 0.f;
+        if constexpr (MODE == PROBS) {
+            r.lse = r.counted ? a.lse[row] : 0.f;
+            r.g = r.counted ? a.g[row] : 0.f;
+            r.ref = r.lse * kLog2e;
         }
-        const uint32_t hit = at >= c0 && at < c0 + 32 ? 1u << (at - c0) : 0u;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (hit >> i & 1) picked = v[i];
-        float m = v[0];
-#pragma unroll
-        for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
-        m = fmaxf(m, top);
-        const float ref = m == -INFINITY ? 0.f : m * kLog2e;      // a row of -inf: every term is 0
-        sum *= exp2f(fmaf(top, kLog2e, -ref));
-#pragma unroll
-        for (int i = 0; i < 32; ++i) sum += exp2f(fmaf(v[i], kLog2e, -ref));
-        top = m;
     }
-    if (row < a.m) {
-        a.part[row * a.part_ld + w.tn] = make_float2(top, sum);
-        if (at >= 0) a.picked[row] = picked;
+}
+
+// Columns c0 .. c0 + 31 of the tile; those past the product's edge hold anything.
+__device__ __forceinline__ void block_logits(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
+    const int left = a.n - w.tn * kTileN - c0;
+    if (left < 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i < left ? v[i] : -INFINITY;
     }
+    const uint32_t hit = r.at >= c0 && r.at < c0 + 32 ? 1u << (r.at - c0) : 0u;
+    float m = r.top;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (hit >> i & 1) r.picked = v[i];
+        m = fmaxf(m, v[i]);
+    }
+    const float ref = m == -INFINITY ? 0.f : m * kLog2e;      // a row of -inf: every term is 0
+    r.sum *= exp2f(fmaf(r.top, kLog2e, -ref));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r.sum += exp2f(fmaf(v[i], kLog2e, -ref));
+    r.top = m;
 }
 
 template <int PLANES>
-__device__ __forceinline__ void epilogue_probs(const GemmArgs &a, const Work &w, uint32_t acc, int row) {
-    const int n0 = w.tn * kTileN;
-    const bool in = row < a.m;
-    const int64_t t = in ? a.target[row] : -1;
-    const bool counted = t >= 0 && t < a.vocab;
-    const int64_t at64 = t - a.v0 - n0;
-    const int at = (counted && at64 >= 0 && at64 < kTileN) ? static_cast<int>(at64) : -1;
-    const float lse = counted ? a.lse[row] : 0.f, g = counted ? a.g[row] : 0.f;
-    const float ref = lse * kLog2e;
-    __nv_bfloat16 *const dst = a.p + static_cast<int64_t>(row) * a.ldp + n0;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kTileN && n0 + c0 < a.n; c0 += 32) {
-        float v[32];
-        __syncwarp();
-        tc::tmem_ld32(acc + c0, v);
+__device__ __forceinline__ void block_probs(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            // the f32 form keeps s - lse exact where it can; the bf16 form rounds the result to 8
-            // bits anyway
-            float e = PLANES == 1 ? exp2f(fmaf(v[i], kLog2e, -ref)) : expf(v[i] - lse);
-            if (i == at - c0) e -= 1.f;
-            v[i] = counted ? g * e : 0.f;
-        }
-        if (!in) {
-        } else if constexpr (PLANES == 1) {
-            uint4 *const q = reinterpret_cast<uint4 *>(dst + c0);
+    for (int i = 0; i < 32; ++i) {
+        // the f32 form keeps s - lse exact where it can; the bf16 form rounds the result to 8
+        // bits anyway
+        float e = PLANES == 1 ? exp2f(fmaf(v[i], kLog2e, -r.ref)) : expf(v[i] - r.lse);
+        if (i == r.at - c0) e -= 1.f;
+        v[i] = r.counted ? r.g * e : 0.f;
+    }
+    if (r.row >= a.m) return;
+    __nv_bfloat16 *const dst = a.p + static_cast<int64_t>(r.row) * a.ldp + w.tn * kTileN + c0;
+    if constexpr (PLANES == 1) {
+        uint4 *const q = reinterpret_cast<uint4 *>(dst);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                q[j] = make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                  bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
-        } else {
+        for (int j = 0; j < 4; ++j)
+            q[j] = make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                              bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float x[3][8];
+        for (int j = 0; j < 4; ++j) {
+            float x[3][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split3(v[8 * j + i], x[0][i], x[1][i], x[2][i]);
+            for (int i = 0; i < 8; ++i) split3(v[8 * j + i], x[0][i], x[1][i], x[2][i]);
 #pragma unroll
-                for (int pl = 0; pl < 3; ++pl)
-                    *reinterpret_cast<uint4 *>(dst + pl * a.p_plane + c0 + 8 * j) =
-                        make_uint4(bf16x2(x[pl][0], x[pl][1]), bf16x2(x[pl][2], x[pl][3]),
-                                   bf16x2(x[pl][4], x[pl][5]), bf16x2(x[pl][6], x[pl][7]));
-            }
+            for (int pl = 0; pl < 3; ++pl)
+                *reinterpret_cast<uint4 *>(dst + pl * a.p_plane + 8 * j) =
+                    make_uint4(bf16x2(x[pl][0], x[pl][1]), bf16x2(x[pl][2], x[pl][3]),
+                               bf16x2(x[pl][4], x[pl][5]), bf16x2(x[pl][6], x[pl][7]));
         }
     }
 }
 
-__device__ __forceinline__ void epilogue_dh(const GemmArgs &a, const Work &w, uint32_t acc, int row) {
-    const int n0 = w.tn * kTileN;
-    float *const dst = static_cast<float *>(a.out) + (static_cast<int64_t>(w.split) * a.m + row) * a.ldo + n0;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kTileN && n0 + c0 < a.n; c0 += 32) {      // ldo is a multiple of 32
-        float v[32];
-        __syncwarp();
-        tc::tmem_ld32(acc + c0, v);
-        if (row < a.m) {
-            float4 *const q = reinterpret_cast<float4 *>(dst + c0);
-            if (a.accumulate) {
+__device__ __forceinline__ void block_dh(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
+    if (r.row >= a.m) return;
+    float4 *const q = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
+                                                 (static_cast<int64_t>(w.split) * a.m + r.row) * a.ldo + w.tn * kTileN + c0);
+    if (a.accumulate) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 o = q[j];
-                    v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        for (int j = 0; j < 8; ++j) {
+            const float4 o = q[j];
+            v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
         }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
+// A row that starts on a 16-byte boundary and has all 32 columns.
 template <typename T>
-__device__ __forceinline__ void epilogue_dw(const GemmArgs &a, const Work &w, uint32_t acc, int row0, float *staging) {
-    const int n0 = w.tn * kTileN, lane = threadIdx.x & 31, row = row0 + lane;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kTileN && n0 + c0 < a.n; c0 += 32) {
-        float v[32];
+__device__ __forceinline__ void block_dw(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
+    if (r.row >= a.m) return;
+    T *const dst = static_cast<T *>(a.out) + r.row * a.ldo + w.tn * kTileN + c0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            reinterpret_cast<float4 *>(dst)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            reinterpret_cast<uint4 *>(dst)[j] =
+                make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                           bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    }
+}
+
+// Rows that start anywhere, or end within the block: through shared memory, 16 columns at a time,
+// so that a warp stores along its rows.
+template <typename T>
+__device__ __forceinline__ void block_dw_any(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32],
+                                             float *staging) {
+    const int left = a.n - w.tn * kTileN - c0, lane = threadIdx.x & 31, rows = a.m - (r.row - lane);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
         __syncwarp();
-        tc::tmem_ld32(acc + c0, v);
-        if (a.out_vec && n0 + c0 + 32 <= a.n) {
-            if (row < a.m) {
-                T *const dst = static_cast<T *>(a.out) + row * a.ldo + n0 + c0;
-                if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        reinterpret_cast<float4 *>(dst)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        reinterpret_cast<uint4 *>(dst)[j] =
-                            make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                       bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
-                }
-            }
-        } else {
-            // rows that start anywhere: through shared memory, so that a warp stores along a row
-#pragma unroll
-            for (int i = 0; i < 32; ++i) staging[lane * kStageRow + i] = v[i];
-            __syncwarp();
-            const int col = n0 + c0 + lane;
-            if (col < a.n)
-                for (int r = 0; r < 32 && row0 + r < a.m; ++r)
-                    put(static_cast<T *>(a.out) + (row0 + r) * a.ldo + col, staging[r * kStageRow + lane]);
-            __syncwarp();
+        for (int i = 0; i < 16; ++i) staging[lane * kStageRow + i] = v[16 * h + i];
+        __syncwarp();
+        const int col = 16 * h + (lane & 15);
+        T *p = static_cast<T *>(a.out) + (r.row - lane + (lane >> 4)) * a.ldo + w.tn * kTileN + c0 + col;
+#pragma unroll 1
+        for (int q = lane >> 4; q < 32 && q < rows && col < left; q += 2, p += 2 * a.ldo)
+            put(p, staging[q * kStageRow + (lane & 15)]);
+    }
+}
+
+template <int MODE, int PLANES, bool ANY>
+__device__ __forceinline__ void block(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32], float *staging) {
+    using T = std::conditional_t<PLANES == 1, __nv_bfloat16, float>;
+    if constexpr (MODE == LOGITS) block_logits(r, a, w, c0, v);
+    else if constexpr (MODE == PROBS) block_probs<PLANES>(r, a, w, c0, v);
+    else if constexpr (MODE == DH) block_dh(r, a, w, c0, v);
+    else if constexpr (ANY) block_dw_any<T>(r, a, w, c0, v, staging);
+    else block_dw<T>(r, a, w, c0, v);
+}
+
+template <int MODE>
+__device__ __forceinline__ void end(const Row &r, const GemmArgs &a, const Work &w, int half) {
+    if constexpr (MODE == LOGITS) {
+        if (r.row < a.m) {
+            a.part[r.row * a.part_ld + 2 * w.tn + half] = make_float2(r.top, r.sum);
+            if (r.at >= half * kHalf && r.at < (half + 1) * kHalf) a.picked[r.row] = r.picked;
         }
     }
 }
@@ -262,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ GemmArgs a) {
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DH || MODE == DW;
+    constexpr bool SUMS = MODE == LOGITS || PLANES == 3;      // chunks are added in registers
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kBytesA;
@@ -281,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&acc_full[s], 1);
-            tc::mbar_init(&acc_empty[s], 128);
+            tc::mbar_init(&acc_empty[s], 32 * kEpilogueWarps);
         }
         tc::mbar_init(&drained, 1);
         tc::mbar_fence_init();
@@ -294,7 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_slot;
     const int total = a.tiles_m * a.tiles_n * a.splits;
 
-    if (warp == 0) {
+    if (warp < 4) {
+      tc::regs_dec<kRegsFew>();
+      if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
@@ -304,10 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kb0 = k.split * a.kb_per_split, kb1 = min(a.kblocks, kb0 + a.kb_per_split);
                 const int groups_b = (cols_of(k.tn, a) + 63) >> 6;
                 const uint32_t bytes = kBytesA + (B_MN ? groups_b * (kTileK * 128) : kBytesB);
+                for (int c = kb0; ok && c < kb1; c += a.chunk)
                 for (int pr = 0; ok && pr < a.pairs; ++pr) {
                     int pa, pb;
                     pair_of(pr, a.pairs, pa, pb);
-                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    for (int kb = c; kb < min(c + a.chunk, kb1); ++kb, ++it) {
                         const uint32_t s = it % kStages;
                         if (!tc::mbar_wait(&empty[s], (it / kStages & 1) ^ 1, kPolls)) {
                             ok = false;
@@ -336,38 +362,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::mbar_wait(&full[i % kStages], i / kStages & 1, kPolls);
             }
         }
-    } else if (warp == 1) {
+      } else if (warp == 1) {
         if (lane == 0) {
             uint32_t it = 0, done = 0;
             bool ok = true;
-            for (int w = blockIdx.x; ok && w < total; w += gridDim.x, ++done) {
+            for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
                 const Work k = work_of(w, a);
                 const int kb0 = k.split * a.kb_per_split, kb1 = min(a.kblocks, kb0 + a.kb_per_split);
                 const uint32_t idesc = tc::idesc_bf16(kTileM, cols_of(k.tn, a), A_MN, B_MN);
-                const uint32_t acc = tmem + (done & 1) * kTileN;
-                if (!tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls)) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after_sync();
-                const int steps = (kb1 - kb0) * a.pairs;
-                for (int i = 0; i < steps; ++i, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!tc::mbar_wait(&full[s], it / kStages & 1, kPolls)) {
+                for (int c = kb0; ok && c < kb1; c += a.chunk, ++done) {
+                    const uint32_t acc = tmem + (done & 1) * kTileN;
+                    if (!tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint32_t sa = tc::smem_u32(tiles_a + s * kBytesA), sb = tc::smem_u32(tiles_b + s * kBytesB);
-                    const uint64_t da = A_MN ? tc::sdesc_mn_sw128(sa, kTileK * 128) : tc::sdesc_sw128(sa);
-                    const uint64_t db = B_MN ? tc::sdesc_mn_sw128(sb, kTileK * 128) : tc::sdesc_sw128(sb);
+                    const int steps = (min(c + a.chunk, kb1) - c) * a.pairs;
+                    for (int i = 0; i < steps; ++i, ++it) {
+                        const uint32_t s = it % kStages;
+                        if (!tc::mbar_wait(&full[s], it / kStages & 1, kPolls)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint32_t sa = tc::smem_u32(tiles_a + s * kBytesA), sb = tc::smem_u32(tiles_b + s * kBytesB);
+                        const uint64_t da = A_MN ? tc::sdesc_mn_sw128(sa, kTileK * 128) : tc::sdesc_sw128(sa);
+                        const uint64_t db = B_MN ? tc::sdesc_mn_sw128(sb, kTileK * 128) : tc::sdesc_sw128(sb);
 #pragma unroll
-                    for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
-                        tc::mma_f16(acc, da + j * (A_MN ? 2048 / 16 : 2), db + j * (B_MN ? 2048 / 16 : 2), idesc,
-                                    i > 0 || j > 0);
-                    tc::mma_commit(&empty[s]);
+                        for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
+                            tc::mma_f16(acc, da + j * (A_MN ? 2048 / 16 : 2), db + j * (B_MN ? 2048 / 16 : 2), idesc,
+                                        i > 0 || j > 0);
+                        tc::mma_commit(&empty[s]);
+                    }
+                    if (ok) tc::mma_commit(&acc_full[done & 1]);
                 }
-                if (ok) tc::mma_commit(&acc_full[done & 1]);
             }
             if (!ok) {
                 atomicExch(a.status, 2);
@@ -375,26 +403,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mbar_wait(&drained, 0, kPolls);
             }
         }
+      }
     } else {
-        const int quad = warp & 3;                          // the tensor-memory lanes a warp may read
+        tc::regs_inc<kRegsMany>();
+        const int quad = warp & 3, half = (warp - 4) >> 2;  // a warp may read its quarter of the lanes
+        float *const stage = staging + (warp - 4) * 32 * kStageRow;
         uint32_t done = 0;
-        for (int w = blockIdx.x; w < total; w += gridDim.x, ++done) {
+        bool ok = true;
+        for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
             const Work k = work_of(w, a);
-            const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
-            const int row0 = k.tm * kTileM + quad * 32;
-            const bool ok = tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls);
-            if (!__all_sync(0xffffffffu, ok)) {
+            const int cols = min(a.n - k.tn * kTileN, (half + 1) * kHalf);     // this warp's columns end there
+            const int kb0 = k.split * a.kb_per_split, kb1 = min(a.kblocks, kb0 + a.kb_per_split);
+            const bool any = MODE == DW && !(a.out_vec && cols == (half + 1) * kHalf);
+            Row r;
+            begin<MODE>(r, a, k, k.tm * kTileM + quad * 32 + lane);
+            float v[SUMS ? kHalf / 32 : 1][32];
+            if constexpr (SUMS) {
+#pragma unroll
+                for (int b = 0; b < kHalf / 32; ++b)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[b][i] = 0.f;
+            }
+#pragma unroll 1
+            for (int c = kb0; c < kb1; c += a.chunk, ++done) {
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
+                if constexpr (SUMS) {
+#pragma unroll
+                    for (int b = 0; b < kHalf / 32; ++b) {
+                        const int c0 = half * kHalf + 32 * b;
+                        if (c0 < cols) {
+                            float x[32];
+                            tc::tmem_ld32(acc + c0, x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[b][i] += x[i];
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
+                        __syncwarp();
+                        tc::tmem_ld32(acc + c0, v[0]);
+                        if (any) block<MODE, PLANES, true>(r, a, k, c0, v[0], stage);
+                        else block<MODE, PLANES, false>(r, a, k, c0, v[0], stage);
+                    }
+                }
+                __syncwarp();
+                tc::fence_before_sync();
+                tc::mbar_arrive(&acc_empty[done & 1]);
+            }
+            if (!ok) {
                 if (lane == 0) atomicExch(a.status, 2);
                 break;
             }
-            tc::fence_after_sync();
-            if constexpr (MODE == LOGITS) epilogue_logits(a, k, acc, row0 + lane);
-            else if constexpr (MODE == PROBS) epilogue_probs<PLANES>(a, k, acc, row0 + lane);
-            else if constexpr (MODE == DH) epilogue_dh(a, k, acc, row0 + lane);
-            else if constexpr (PLANES == 1) epilogue_dw<__nv_bfloat16>(a, k, acc, row0, staging + quad * 32 * kStageRow);
-            else epilogue_dw<float>(a, k, acc, row0, staging + quad * 32 * kStageRow);
-            tc::fence_before_sync();
-            tc::mbar_arrive(&acc_empty[done & 1]);
+            if constexpr (SUMS) {
+                if (any) {
+#pragma unroll
+                    for (int b = 0; b < kHalf / 32; ++b)
+                        if (half * kHalf + 32 * b < cols) block<MODE, PLANES, true>(r, a, k, half * kHalf + 32 * b, v[b], stage);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < kHalf / 32; ++b)
+                        if (half * kHalf + 32 * b < cols) block<MODE, PLANES, false>(r, a, k, half * kHalf + 32 * b, v[b], stage);
+                }
+                __syncwarp();
+            }
+            end<MODE>(r, a, k, half);
         }
     }
     __syncwarp();
