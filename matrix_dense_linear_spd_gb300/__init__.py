@@ -11,7 +11,6 @@ Right-hand sides are (batch, n, nrhs), also with ``stride(-2) == 1``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -240,176 +239,53 @@ def potrs(A, B, uplo="L", stream=None):
 
 
 # ------------------------------------------------------------------ training operators
+#
+# Checks, allocation and the C call are in csrc/binding/torch_binding.cpp: these operators take
+# lists of hundreds of tensors and run for microseconds, where ctypes costs more than the GPU does.
 
-def _on(stream, device):
-    """Context in which allocations belong to `stream` (a raw handle): memory taken for work on
-    another stream than the current one has to come from, and go back to, that stream's order."""
-    torch = _torch()
-    if stream == torch.cuda.current_stream(device).cuda_stream:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
+_binding = None
 
 
-def _stream_on(stream, device):
-    return _torch().cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+def _training():
+    """The compiled binding of the training operators (loaded on first use)."""
+    global _binding
+    if _binding is None:
+        _torch()
+        try:
+            from . import _torch_binding as m
+        except ImportError as e:
+            raise ImportError("the training operators' binding is missing: build it with "
+                              "`python -m matrix_dense_linear_spd_gb300.build` (there is no CPU fallback)") from e
+        m.init(BLError)
+        _binding = m
+    return _binding
 
 
-def _scratch(nbytes, device):
-    return _torch().empty(nbytes, dtype=_torch().uint8, device=device)
-
-
-def _grad_lists(tensors, out=None):
-    """(count, dtypes, pointers, sizes, out pointers, device): the host arrays of a list of dense
-    CUDA tensors. Any memory order will do, as long as a tensor's elements fill one block of
-    memory (row-major, column-major, permuted)."""
-    torch = _torch()
-    tensors = list(tensors)
-    codes = {torch.float32: BL_F32, torch.float64: BL_F64, torch.bfloat16: BL_BF16, torch.float16: BL_F16}
-    n = len(tensors)
-    device = tensors[0].device if n else torch.device("cuda", torch.cuda.current_device())
-    kinds = []
-    for i, t in enumerate(tensors):
-        code = codes.get(t.dtype)
-        if code is None:
-            raise TypeError(f"unsupported dtype {t.dtype}")
-        kinds.append(code)
-        if t.device != device or not t.is_cuda:
-            raise ValueError("the tensors must be on one CUDA device")
-        if not t.is_contiguous() and not _is_dense(t):
-            raise ValueError(f"tensor {i} has gaps or overlaps in memory (strides {t.stride()})")
-    outs = None
-    if out is not None:
-        out = list(out)
-        if len(out) != n:
-            raise ValueError(f"out has {len(out)} tensors for {n}")
-        for i, (t, o) in enumerate(zip(tensors, out)):
-            if o.dtype != t.dtype or o.shape != t.shape or o.device != device:
-                raise ValueError(f"out {i} must have its tensor's type, shape and device")
-            if o.stride() != t.stride() and not (t.is_contiguous() and o.is_contiguous()):
-                raise ValueError(f"out {i} must have its tensor's strides")
-        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
-    return n, (ctypes.c_int32 * n)(*kinds), ptrs, (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), outs, device
-
-
-def _is_dense(t):
-    want = 1
-    for stride, size in sorted(zip(t.stride(), t.shape)):
-        if size != 1:
-            if stride != want:
-                return False
-            want *= size
-    return True
+def _raw(stream):
+    return getattr(stream, "cuda_stream", stream)
 
 
 def gnorm(tensors, stream=None):
     """Global norm sqrt(sum of all squares) of a list of f32, f64, bf16 or f16 tensors, in any
-    mix. Returns a 0-dim f32 tensor on their device."""
-    torch = _torch()
-    n, kinds, ptrs, sizes, _, device = _grad_lists(tensors)
-    s, lib = _stream_on(stream, device), get_lib()
-    with torch.cuda.device(device), _on(s, device):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = _scratch(lib.bl_gnorm_workspace(n), device)
-        _check(lib.bl_gnorm(n, kinds, ptrs, sizes, norm.data_ptr(), ws.data_ptr(), ws.numel(), s))
-    return norm
+    mix and any memory order (no gaps, no overlaps). Returns a 0-dim f32 tensor on their device."""
+    return (_binding or _training()).gnorm(tensors, _raw(stream))
 
 
 def gclip(tensors, max_norm, out=None, stream=None):
     """Scale the tensors to a global norm of at most max_norm, in place or into the tensors of
     `out` (same types, shapes and strides). A norm that is not finite leaves the values as they
     are. Returns the norm before scaling, a 0-dim f32 tensor."""
-    torch = _torch()
-    tensors = list(tensors)
-    n, kinds, ptrs, sizes, outs, device = _grad_lists(tensors, out)
-    s, lib = _stream_on(stream, device), get_lib()
-    with torch.cuda.device(device), _on(s, device):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = _scratch(lib.bl_gnorm_workspace(n), device)
-        _check(lib.bl_gclip(n, kinds, ptrs, ptrs if outs is None else outs, sizes, float(max_norm), norm.data_ptr(),
-                            ws.data_ptr(), ws.numel(), s))
-    return norm
-
-
-def _rows_view(M, name, dtype=None, shape=None, device=None):
-    """Leading dimension of a (rows, cols) CUDA tensor whose rows are stored back to back or apart."""
-    if M.dim() != 2:
-        raise ValueError(f"{name} must be (rows, cols)")
-    if not M.is_cuda or (device is not None and M.device != device):
-        raise ValueError(f"{name} must be a CUDA tensor on H's device")
-    if dtype is not None and M.dtype != dtype:
-        raise TypeError(f"{name} must have H's dtype {dtype}, not {M.dtype}")
-    if shape is not None and tuple(M.shape) != shape:
-        raise ValueError(f"{name} must be {shape}, not {tuple(M.shape)}")
-    if M.shape[1] > 1 and M.stride(1) != 1:
-        raise ValueError(f"{name}'s rows must be contiguous (stride(1) == 1)")
-    return M.stride(0) if M.shape[0] > 1 else max(M.shape[1], 1)
-
-
-def _row_vector(v, name, dtype, rows, device):
-    if tuple(v.shape) != (rows,) or v.dtype != dtype or v.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of {rows} values on H's device")
-    if rows > 1 and v.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _xent_args(H, W, target):
-    torch = _torch()
-    codes = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
-    if H.dtype not in codes:
-        raise TypeError(f"unsupported dtype {H.dtype}")
-    ldh = _rows_view(H, "H")
-    ldw = _rows_view(W, "W", H.dtype, device=H.device)
-    if W.shape[1] != H.shape[1]:
-        raise ValueError(f"H has {H.shape[1]} columns and W {W.shape[1]}")
-    _row_vector(target, "target", torch.int64, H.shape[0], H.device)
-    return codes[H.dtype], ldh, ldw
-
-
-def _xent_scratch(lib, code, H, W, ldw, grad):
-    need = lib.bl_xent_workspace(code, H.shape[0], H.shape[1], W.shape[0], W.data_ptr(), ldw, grad)
-    if need < 0:
-        raise BLError(1, lib.bl_last_error().decode())
-    return _scratch(need, H.device)
+    return (_binding or _training()).gclip(tensors, max_norm, out, _raw(stream))
 
 
 def xent(H, W, target, stream=None):
     """Softmax cross entropy of the tokens H (rows, dim) over the vocabulary W (vocab, dim), both
     bf16 or both f32, for int64 targets: (loss, lse), f32 tensors of one value a row. A row whose
     target lies outside [0, vocab) does not count: 0, 0. The logits are never stored."""
-    torch = _torch()
-    code, ldh, ldw = _xent_args(H, W, target)
-    device = H.device
-    s, lib = _stream_on(stream, device), get_lib()
-    with torch.cuda.device(device), _on(s, device):
-        loss = torch.empty(H.shape[0], dtype=torch.float32, device=device)
-        lse = torch.empty_like(loss)
-        ws = _xent_scratch(lib, code, H, W, ldw, 0)
-        _check(lib.bl_xent(code, H.shape[0], H.shape[1], W.shape[0], H.data_ptr(), ldh, W.data_ptr(), ldw,
-                           target.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
-    return loss, lse
+    return (_binding or _training()).xent(H, W, target, _raw(stream))
 
 
 def xent_grad(H, W, target, lse, g, dH=None, dW=None, stream=None):
     """Gradients of sum_r g_r loss_r: (dH, dW) in H's and W's type, given xent's lse. dH and dW
     may be tensors to write to; False leaves that gradient out (None is returned for it)."""
-    torch = _torch()
-    code, ldh, ldw = _xent_args(H, W, target)
-    device = H.device
-    for v, name in ((lse, "lse"), (g, "g")):
-        _row_vector(v, name, torch.float32, H.shape[0], device)
-    if dH is False and dW is False:
-        raise ValueError("dH and dW are both left out")
-    s, lib = _stream_on(stream, device), get_lib()
-    with torch.cuda.device(device), _on(s, device):
-        if dH is None:
-            dH = torch.empty(H.shape, dtype=H.dtype, device=device)
-        if dW is None:
-            dW = torch.empty(W.shape, dtype=W.dtype, device=device)
-        lddh = _rows_view(dH, "dH", H.dtype, tuple(H.shape), device) if dH is not False else 0
-        lddw = _rows_view(dW, "dW", W.dtype, tuple(W.shape), device) if dW is not False else 0
-        ws = _xent_scratch(lib, code, H, W, ldw, 1)
-        _check(lib.bl_xent_grad(code, H.shape[0], H.shape[1], W.shape[0], H.data_ptr(), ldh, W.data_ptr(), ldw,
-                                target.data_ptr(), lse.data_ptr(), g.data_ptr(), dH.data_ptr() if dH is not False else None,
-                                lddh, dW.data_ptr() if dW is not False else None, lddw, ws.data_ptr(), ws.numel(), s))
-    return (None if dH is False else dH), (None if dW is False else dW)
+    return (_binding or _training()).xent_grad(H, W, target, lse, g, dH, dW, _raw(stream))

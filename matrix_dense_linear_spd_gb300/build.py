@@ -1,5 +1,6 @@
 """Build libbl.so in-tree: nvcc for sm_103a, one translation unit per dtype compiled in
-parallel, plus the host dispatcher. The tuned selection tables (tuned/*.txt) are embedded as
+parallel, plus the host dispatcher; and _torch_binding.so, the training operators' binding to
+torch tensors, with the host compiler against the installed torch's headers. The tuned selection tables (tuned/*.txt) are embedded as
 string literals so the library needs no data files at run time (BL_TUNED_DIR still overrides).
 
 Usage: python -m matrix_dense_linear_spd_gb300.build [--force] [--jobs N]
@@ -10,16 +11,19 @@ import argparse
 import concurrent.futures as cf
 import glob
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 TUNED = os.path.join(PKG, "tuned")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbl.so")
+BINDING = os.path.join(PKG, "_torch_binding.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -95,6 +99,46 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")          # without importing it
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: the training operators' binding needs its headers")
+    return spec.submodule_search_locations[0]
+
+
+def _compile_binding() -> str:
+    src = os.path.join(CSRC, "binding", "torch_binding.cpp")
+    obj = os.path.join(BUILD, "torch_binding.cpp.o")
+    stamp = obj + ".sha"
+    torch_dir = _torch_dir()
+    with open(os.path.join(torch_dir, "version.py")) as fh:
+        version = fh.read()
+    flags = ["-O2", "-std=c++17", "-fPIC", "-I", os.path.join(torch_dir, "include"),
+             "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+             "-I", sysconfig.get_paths()["include"],
+             "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    digest = hashlib.sha1((_deps_hash(src) + version + " ".join(flags)).encode()).hexdigest()
+    if os.path.exists(obj) and os.path.exists(stamp) and open(stamp).read() == digest:
+        return obj
+    r = subprocess.run(["g++"] + flags + ["-c", src, "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as fh:
+        fh.write(digest)
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, LIB, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def parse_ptxas(text: str):
     """[{name, registers, stack, spill_stores, spill_loads}] for every function in a ptxas -v
     report (the mangled name; functions that report no register line have registers None)."""
@@ -134,13 +178,16 @@ def build(force: bool = False, jobs: int | None = None) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
     jobs = jobs or max(1, min(len(srcs), os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
+        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xlinker", "--no-undefined"]
+    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xlinker", "--no-undefined", "-Xlinker", "-soname=libbl.so"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 
