@@ -185,10 +185,10 @@ bl_status bl_xent_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab,
                        int64_t workspace_bytes, bl_stream_t stream);
 
 /* Bytes of workspace that bl_xent (grad = 0) or bl_xent_grad (grad = 1) needs on the current
- * device for these arguments; -1 if they are invalid (see bl_last_error()). Of W only the
- * address is looked at. */
-int64_t bl_xent_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw,
-                          int grad);
+ * device for these arguments; -1 if they are invalid (see bl_last_error()). Of H and
+ * W only the addresses are looked at. */
+int64_t bl_xent_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
+                          const void *W, int64_t ldw, int grad);
 
 /* Static, human-readable name of a status code. */
 const char *bl_status_string(bl_status status);

@@ -76,7 +76,7 @@ def _load():
     lib.bl_xent.restype = ctypes.c_int
     lib.bl_xent_grad.argtypes = [ctypes.c_int, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp]
     lib.bl_xent_grad.restype = ctypes.c_int
-    lib.bl_xent_workspace.argtypes = [ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_int]
+    lib.bl_xent_workspace.argtypes = [ctypes.c_int, i64, i64, i64, vp, i64, vp, i64, ctypes.c_int]
     lib.bl_xent_workspace.restype = i64
     return lib
 

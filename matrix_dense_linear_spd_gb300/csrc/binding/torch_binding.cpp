@@ -175,7 +175,7 @@ struct Xent {
         target = values_of<const int64_t>(tensor(to, "target"), "target", at::kLong, h);
     }
     int64_t need(int grad) const {
-        const int64_t n = bl_xent_workspace(code, rows, dim, vocab, w.data_ptr(), ldw, grad);
+        const int64_t n = bl_xent_workspace(code, rows, dim, vocab, h.data_ptr(), ldh, w.data_ptr(), ldw, grad);
         if (n < 0) failed(BL_ERR_INVALID_ARGUMENT);
         return n;
     }

@@ -8,10 +8,12 @@
 // bf16, or as the three bf16 planes of f32) is all that is ever stored of them, and its two
 // products follow. The products run in xent_gemm.cuh.
 //
-// H is copied once per call, with the rows that have no target zeroed: what stands in such a row
-// (NaN included) reaches no result, and the copy's rows start where TMA wants them. W is read in
-// place if it is bf16 and its rows start on 16-byte boundaries; otherwise each piece is copied
-// (f32: as planes) before its products.
+// Rows without a target are left out: the rows that count are copied together (their order kept),
+// so that the products do not spend time on a prompt's rows, and what stands in the others (NaN
+// included) reaches no result. How many they are is known on the device only; the products read it
+// there. Up to one tile of rows there is nothing to gain: rows keep their places, and the loss reads
+// H itself if TMA can. W is read in place if it is bf16 and its rows start on 16-byte boundaries;
+// otherwise each piece is copied (f32: as planes) before its products.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,6 +22,7 @@
 #include <cstdint>
 
 #include "host.h"
+#include "pdl.cuh"
 #include "xent_gemm.cuh"
 
 namespace bl {
@@ -31,38 +34,75 @@ __device__ __forceinline__ bool has_target(const int64_t *target, int64_t row, i
     return !target || (target[row] >= 0 && target[row] < vocab);
 }
 
-// Copy rows into bf16 planes of row length ldp (a multiple of 8; the tail is zero). Rows without
-// a target become zero. Thread 0 also clears the call's status word.
+// One block: the rows that count, in order; each row's place among them (-1: does not count); how
+// many they are. The rows that do not count get the results they have (loss, lse: or null).
+__global__ void __launch_bounds__(1024)
+    index_kernel(const int64_t *target, int64_t vocab, int rows, int *order, int *place, int *kept, float *loss, float *lse) {
+    __shared__ int sums[2][32];
+    pdl_release();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int before = 0;
+    for (int r0 = 0, turn = 0; r0 < rows; r0 += 1024, turn ^= 1) {
+        const int row = r0 + threadIdx.x;
+        const bool in = row < rows, counts = in && has_target(target, row, vocab);
+        const uint32_t votes = __ballot_sync(0xffffffffu, counts);
+        if (lane == 0) sums[turn][warp] = __popc(votes);
+        __syncthreads();                    // sums[turn] is written again two rounds, and a barrier, from here
+        const int mine = sums[turn][lane];
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const int at = before + __shfl_sync(0xffffffffu, upto - mine, warp) + __popc(votes & ((1u << lane) - 1));
+        before += __shfl_sync(0xffffffffu, upto, 31);
+        if (in) {
+            place[row] = counts ? at : -1;
+            if (counts) order[at] = row;
+            else if (loss) loss[row] = lse[row] = 0.f;
+        }
+    }
+    if (threadIdx.x == 0) *kept = before;
+}
+
+// Copy rows into bf16 planes of row length ldp (a multiple of 8; the tail is zero). With `order`
+// row j of the copy is row order[j]; whole row tiles are filled, with zeros after the last row. Rows
+// without a target (`target` given) become zero too.
 template <typename T, int PLANES>
 __global__ void __launch_bounds__(256)
-    pack_kernel(const T *src, int64_t ld, int64_t rows, int dim, const int64_t *target, int64_t vocab,
-                __nv_bfloat16 *dst, int64_t ldp, int64_t plane, int vec, int32_t *status) {
-    if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
-    const int64_t per_row = ldp / 8, all = rows * per_row;
+    pack_kernel(const T *src, int64_t ld, int64_t rows, int dim, const int64_t *target, int64_t vocab, const int *order,
+                const int *kept, int tile, __nv_bfloat16 *dst, int64_t ldp, int64_t plane, int vec) {
+    pdl_release();
+    pdl_wait();
+    const int64_t count = kept ? *kept : rows, filled = max((count + tile - 1) / tile, int64_t(1)) * tile;
+    const int64_t per_row = ldp / 8, all = filled * per_row;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all;
          i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / per_row;
-        const int c = static_cast<int>(i - row * per_row) * 8;
+        const int64_t j = i / per_row;
+        const int c = static_cast<int>(i - j * per_row) * 8;
+        const int64_t row = j >= count ? -1 : order ? order[j] : j;
         const T *const s = src + row * ld + c;
         __align__(16) T x[8];
-        if (!has_target(target, row, vocab)) {
+        if (row < 0 || (target && !has_target(target, row, vocab))) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = T(0.f);
+            for (int e = 0; e < 8; ++e) x[e] = T(0.f);
         } else if (vec && c + 8 <= dim) {
 #pragma unroll
-            for (int j = 0; j < static_cast<int>(sizeof(x) / 16); ++j)
-                reinterpret_cast<uint4 *>(x)[j] = reinterpret_cast<const uint4 *>(s)[j];
+            for (int e = 0; e < static_cast<int>(sizeof(x) / 16); ++e)
+                reinterpret_cast<uint4 *>(x)[e] = reinterpret_cast<const uint4 *>(s)[e];
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = c + j < dim ? s[j] : T(0.f);
+            for (int e = 0; e < 8; ++e) x[e] = c + e < dim ? s[e] : T(0.f);
         }
-        __nv_bfloat16 *const d = dst + row * ldp + c;
+        __nv_bfloat16 *const d = dst + j * ldp + c;
         if constexpr (PLANES == 1) {
             *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(x);
         } else {
             float p[3][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) split3(x[j], p[0][j], p[1][j], p[2][j]);
+            for (int e = 0; e < 8; ++e) split3(x[e], p[0][e], p[1][e], p[2][e]);
 #pragma unroll
             for (int q = 0; q < 3; ++q)
                 *reinterpret_cast<uint4 *>(d + q * plane) = make_uint4(bf16x2(p[q][0], p[q][1]), bf16x2(p[q][2], p[q][3]),
@@ -71,15 +111,26 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// Whether any CTA of the call's products gave up (all threads of the block ask).
+__device__ __forceinline__ bool any_gave_up(const int32_t *flags, int count) {
+    int bad = 0;
+    for (int i = threadIdx.x; i < count; i += blockDim.x) bad |= flags[i];
+    return __syncthreads_or(bad) != 0;
+}
+
 // One warp a row: join the tiles' maxima and sums. A product that gave up makes every loss NaN.
 __global__ void __launch_bounds__(256)
-    loss_kernel(const float2 *part, int64_t part_ld, const float *picked, const int64_t *target, int64_t vocab,
-                int rows, const int32_t *status, float *loss, float *lse) {
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= rows) return;
+    loss_kernel(const float2 *part, int64_t part_ld, const float *picked, const int64_t *target, int64_t vocab, int rows,
+                const int *order, const int *kept, const int32_t *flags, int flag_count, float *loss, float *lse) {
+    pdl_release();
+    pdl_wait();
+    const bool bad = any_gave_up(flags, flag_count);
+    const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (j >= (kept ? *kept : rows)) return;
+    const int row = order ? order[j] : j;
     float l = 0.f, v = 0.f;
     if (has_target(target, row, vocab)) {
-        const float2 *const p = part + row * part_ld;
+        const float2 *const p = part + j * part_ld;
         float top = -INFINITY, sum = 0.f;
         for (int64_t i = lane; i < part_ld; i += 32) top = fmaxf(top, p[i].x);
 #pragma unroll
@@ -89,30 +140,54 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         v = ref + logf(sum);
-        l = v - picked[row];
+        l = v - picked[j];
     }
-    if (*status != 0) l = v = NAN;
+    if (bad) l = v = NAN;
     if (lane == 0) {
         loss[row] = l;
         lse[row] = v;
     }
 }
 
-// dH from the parts' sums; rows without a target are zero. A product that gave up makes it NaN.
+__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+}
+
+// dH from the parts' sums, four columns a thread; rows without a target are zero. A product that
+// gave up makes it NaN.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    dh_kernel(const float *part, int splits, int64_t ldo, const int64_t *target, int64_t vocab, int64_t rows, int dim,
-              const int32_t *status, T *dh, int64_t ld) {
-    const bool bad = *status != 0;
-    const int64_t all = rows * dim;
+    dh_kernel(const float *part, int splits, int64_t rows, int64_t ldo, const int64_t *target, int64_t vocab,
+              const int *place, int dim, const int32_t *flags, int flag_count, T *dh, int64_t ld, int vec) {
+    pdl_release();
+    pdl_wait();
+    const bool bad = any_gave_up(flags, flag_count);
+    const int64_t per_row = (dim + 3) / 4, all = rows * per_row;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all;
          i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / dim;
-        const int c = static_cast<int>(i - row * dim);
-        float v = 0.f;
-        if (has_target(target, row, vocab))
-            for (int s = 0; s < splits; ++s) v += part[(s * rows + row) * ldo + c];
-        put(dh + row * ld + c, bad ? NAN : v);
+        const int64_t row = i / per_row;
+        const int c = static_cast<int>(i - row * per_row) * 4;
+        const int64_t j = place ? place[row] : has_target(target, row, vocab) ? row : -1;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j >= 0) {
+            const float4 *p = reinterpret_cast<const float4 *>(part + j * ldo + c);
+#pragma unroll 4
+            for (int s = 0; s < splits; ++s, p += rows * ldo / 4) {
+                const float4 x = *p;
+                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+        }
+        if (bad) v = make_float4(NAN, NAN, NAN, NAN);
+        T *const d = dh + row * ld + c;
+        if (vec && c + 4 <= dim) {
+            put4(d, v);
+        } else {
+            const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < dim) put(d + e, x[e]);
+        }
     }
 }
 
@@ -127,57 +202,87 @@ int64_t cdiv(int64_t v, int64_t by) { return (v + by - 1) / by; }
 
 struct Plan {
     int planes, pairs;
-    bool copy_w, grad;
+    int ctas;                 // that share a tile
+    bool copy_h, copy_w, compact, grad;
     int64_t rows, dim, vocab;
+    int64_t tiled;            // rows of the copy of H and of P: whole tiles
     int64_t ldp;              // row length of the copies of H and W
     int64_t piece, pieces;    // vocabulary entries per piece
     int64_t part_ld;          // partial maxima and sums of a row: two per tile
     int splits;
     int64_t kb_per_split;     // 64-deep steps of one part of dH
     int64_t ldo;              // row length of dH's partial sums
-    int64_t status, h, w, part, picked, p, dh, bytes;   // offsets into the workspace
+    int64_t flags, kept, order, place, h, w, part, picked, p, dh, bytes;   // offsets into the workspace
 };
 
-Plan plan_for(int dtype, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw, bool grad, int sms) {
+bool for_tma(const void *p, int64_t ld, int64_t elem) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * elem % 16 == 0;
+}
+
+// Parts of a K axis of kb steps, so that tiles * parts fill `sms` CTAs (or pairs) evenly: the number that
+// minimises the rounds times a part's steps, plus what a part's partial sums cost to write and
+// read again (in steps of 0.27 us, the time of 128 x 256 x 64 products on one SM).
+int64_t parts_of(int64_t tiles, int64_t kb, int64_t result_bytes, int sms) {
+    int64_t best = 1;
+    double least = 0;
+    for (int64_t s = 1; s <= std::max<int64_t>(1, std::min<int64_t>(kb / 4, std::max<int64_t>(8, 2 * sms / tiles))); ++s) {
+        const double t = static_cast<double>(cdiv(tiles * s, sms)) * (static_cast<double>(cdiv(kb, s)) + 4) +
+                         static_cast<double>(s) * result_bytes * 2 / 6.8e12 / 0.27e-6;
+        if (s == 1 || t < least) best = s, least = t;
+    }
+    return best;
+}
+
+Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw,
+              bool grad, int sms) {
     Plan q{};
     q.planes = dtype == BL_F32 ? 3 : 1;
     q.pairs = dtype == BL_F32 ? 6 : 1;
-    q.copy_w = dtype == BL_F32 || reinterpret_cast<uintptr_t>(W) % 16 != 0 || ldw % 8 != 0;
+    q.compact = rows > kTileM;
+    q.ctas = rows > kTileM ? 2 : 1;
+    // a row without a target may hold anything: only the loss of uncopied rows ignores it
+    q.copy_h = dtype == BL_F32 || grad || q.compact || !for_tma(H, ldh, 2);
+    q.copy_w = dtype == BL_F32 || !for_tma(W, ldw, 2);
     q.grad = grad;
     q.rows = rows;
     q.dim = dim;
     q.vocab = vocab;
+    q.tiled = up(rows, q.ctas * kTileM);
     q.ldp = up(dim, 8);
     // a piece: what keeps P and the copy of W within their size, but 4096 entries at least, so
     // that a piece's products fill the GPU; pieces of one size
     int64_t most = up(vocab, kTileN);
-    if (grad) most = std::min(most, kPieceBytes / (rows * 2 * q.planes));
+    if (grad) most = std::min(most, kPieceBytes / (q.tiled * 2 * q.planes));
     if (q.copy_w) most = std::min(most, kPieceBytes / (q.ldp * 2 * q.planes));
     most = std::max<int64_t>(most / kTileN * kTileN, 4096);
     q.pieces = cdiv(vocab, most);
     q.piece = up(cdiv(vocab, q.pieces), kTileN);
     q.pieces = cdiv(vocab, q.piece);
     q.part_ld = 2 * cdiv(vocab, kTileN);
-    // dH has few tiles and a long K axis (the piece): cut K until there is work for every SM
-    const int64_t tiles = cdiv(rows, kTileM) * cdiv(dim, kTileN), kb = cdiv(std::min(q.piece, vocab), kTileK);
-    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(sms / tiles, kb / 4));
-    q.kb_per_split = cdiv(kb, splits);
-    q.splits = static_cast<int>(cdiv(kb, q.kb_per_split));
     q.ldo = up(dim, 32);
-    int64_t at = 256;
+    // dH has few tiles and a long K axis, the piece
+    const int64_t kb = cdiv(std::min(q.piece, vocab), kTileK);
+    q.kb_per_split = cdiv(kb, parts_of(cdiv(rows, q.ctas * kTileM) * cdiv(dim, kTileN), kb * q.pairs, rows * q.ldo * 4, sms / q.ctas));
+    q.splits = static_cast<int>(cdiv(kb, q.kb_per_split));
+    int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t r = at;
         at += up(bytes, 256);
         return r;
     };
-    q.status = 0;
-    q.h = take(q.planes * rows * q.ldp * 2);
+    q.flags = take(q.pieces * 3 * sms * 4);
+    q.kept = take(4);
+    if (q.compact) {
+        q.order = take(rows * 4);
+        q.place = take(rows * 4);
+    }
+    if (q.copy_h) q.h = take(q.planes * q.tiled * q.ldp * 2);
     if (q.copy_w) q.w = take(q.planes * std::min(q.piece, vocab) * q.ldp * 2);
     if (!grad) {
         q.part = take(rows * q.part_ld * 8);
         q.picked = take(rows * 4);
     } else {
-        q.p = take(q.planes * rows * q.piece * 2);
+        q.p = take(q.planes * q.tiled * q.piece * 2);
         q.dh = take(q.splits * rows * q.ldo * 4);
     }
     q.bytes = at;
@@ -201,46 +306,81 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// Planes of rows x inner bf16 values, copied in boxes of box_rows x 64 with the 128-byte swizzle;
-// what lies outside reads as zero.
-bool make_map(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t planes, int64_t ld, int64_t plane,
-              int box_rows) {
+// Planes of rows x inner values, copied in boxes of box_rows lines of line_bytes (128 or 64, the
+// swizzle's width too); what lies outside reads as zero and is not written. Planes are `plane`
+// values apart; with one plane any multiple of 16 bytes will do.
+bool make_map(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *base, int64_t inner, int64_t rows, int64_t planes,
+              int64_t ld, int64_t plane, int box_rows, int line_bytes = 128) {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(plane * 2)};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, step,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * elem), static_cast<cuuint64_t>(plane * elem)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(line_bytes / elem), static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
+    return fn(map, type, 3, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              line_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+bool map_bf16(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t planes, int64_t ld, int64_t plane,
+              int box_rows, int line_bytes = 128) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, rows, planes, ld, plane, box_rows, line_bytes);
+}
+bool map_f32(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t planes, int64_t ld, int64_t plane) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, inner, rows, planes, ld, plane, 32);
+}
 
-template <int MODE, int PLANES>
-cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const GemmArgs &a, int sms, cudaStream_t s) {
-    static std::atomic<unsigned long long> done{0};
+// Launch a product; its CTAs' flags follow those of the call's earlier products.
+template <int MODE, int PLANES, int CTAS>
+cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, GemmArgs &a, int &flags, int sms,
+                         cudaStream_t s) {
+    constexpr int kSmem = Ring<CTAS>::kSmem;
+    const auto kernel = gemm_kernel<MODE, PLANES, CTAS>;
+    static std::atomic<int> groups[64];         // CTAs, or pairs of CTAs, that the device runs at once
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-    if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(gemm_kernel<MODE, PLANES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    int most = dev < 64 ? groups[dev].load(std::memory_order_acquire) : 0;
+    if (most == 0) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        done.fetch_or(bit, std::memory_order_acq_rel);
+        most = sms;
+        if constexpr (CTAS > 1) {
+            cudaLaunchConfig_t c{};
+            c.gridDim = dim3(sms / CTAS * CTAS);
+            c.blockDim = dim3(kThreads);
+            c.dynamicSmemBytes = kSmem;
+            cudaLaunchAttribute at{};
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = CTAS;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            c.attrs = &at;
+            c.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&most, kernel, &c);
+            if (e != cudaSuccess) return e;
+            most = std::max(1, std::min(most, sms / CTAS));
+        }
+        if (dev < 64) groups[dev].store(most, std::memory_order_release);
     }
-    const int64_t total = static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.splits;
-    gemm_kernel<MODE, PLANES><<<static_cast<unsigned>(std::min<int64_t>(total, sms)), kThreads, kSmem, s>>>(ma, mb, a);
-    return cudaGetLastError();
+    const int64_t total = cdiv(a.m, CTAS * kTileM) * a.tiles_n * a.splits;
+    const int grid = static_cast<int>(std::min<int64_t>(total, most)) * CTAS;
+    a.flags += flags;
+    flags += grid;
+    return launch_pdl_cluster(kernel, grid, kThreads, kSmem, CTAS, s, ma, mb, mo, a);
+}
+template <int MODE, int PLANES>
+cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, GemmArgs &a, int ctas, int &flags,
+                        int sms, cudaStream_t s) {
+    return ctas == 1 ? launch_tiles<MODE, PLANES, 1>(ma, mb, mo, a, flags, sms, s)
+                     : launch_tiles<MODE, PLANES, 2>(ma, mb, mo, a, flags, sms, s);
 }
 
 template <typename T, int PLANES>
 cudaError_t launch_pack(const void *src, int64_t ld, int64_t rows, int64_t dim, const int64_t *target, int64_t vocab,
-                        void *dst, int64_t ldp, int64_t plane, int32_t *status, int sms, cudaStream_t s) {
-    const int vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld * sizeof(T) % 16 == 0;
-    const int64_t blocks = std::min<int64_t>(cdiv(rows * (ldp / 8), 256), static_cast<int64_t>(sms) * 8);
-    pack_kernel<T, PLANES><<<static_cast<unsigned>(blocks), 256, 0, s>>>(
-        static_cast<const T *>(src), ld, rows, static_cast<int>(dim), target, vocab, static_cast<__nv_bfloat16 *>(dst), ldp,
-        plane, vec, status);
-    return cudaGetLastError();
+                        const int *order, const int *kept, int tile, void *dst, int64_t ldp, int64_t plane, int sms,
+                        cudaStream_t s) {
+    const int vec = for_tma(src, ld, sizeof(T));
+    const int64_t blocks = std::min<int64_t>(cdiv(up(rows, tile) * (ldp / 8), 256), static_cast<int64_t>(sms) * 8);
+    return launch_pdl(pack_kernel<T, PLANES>, static_cast<unsigned>(blocks), 256, 0, s, static_cast<const T *>(src), ld, rows,
+                      static_cast<int>(dim), target, vocab, order, kept, tile, static_cast<__nv_bfloat16 *>(dst), ldp, plane, vec);
 }
 
 struct Call {
@@ -273,39 +413,55 @@ struct Call {
 
 template <typename T, int PLANES>
 bl_status run(const char *op, const Plan &q, const Call &c) {
-    int32_t *const status = reinterpret_cast<int32_t *>(c.ws + q.status);
-    char *const hp = c.ws + q.h;
-    const int64_t h_plane = c.rows * q.ldp, piece_w = std::min(q.piece, c.vocab), w_plane = piece_w * q.ldp;
-    BL_TRY((launch_pack<T, PLANES>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, hp, q.ldp, h_plane, status, c.sms, c.s)));
-    CUtensorMap h_k, h_mn;
-    BL_MAP(make_map(&h_k, hp, c.dim, c.rows, PLANES, q.ldp, h_plane, kTileM));
-    BL_MAP(make_map(&h_mn, hp, c.dim, c.rows, PLANES, q.ldp, h_plane, kTileK));
+    const int64_t h_plane = q.tiled * q.ldp, piece_w = std::min(q.piece, c.vocab), w_plane = piece_w * q.ldp;
+    const int rows = static_cast<int>(c.rows), dim = static_cast<int>(c.dim);
+    int *const kept = q.compact ? reinterpret_cast<int *>(c.ws + q.kept) : nullptr;
+    int *const order = q.compact ? reinterpret_cast<int *>(c.ws + q.order) : nullptr;
+    int *const place = q.compact ? reinterpret_cast<int *>(c.ws + q.place) : nullptr;
+    int32_t *const flags = reinterpret_cast<int32_t *>(c.ws + q.flags);
+    int flag_count = 0;
+    const void *hp = c.H;
+    int64_t ldh = c.ldh, h_rows = c.rows;
+    if (q.compact)
+        BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept, c.loss, c.lse));
+    if (q.copy_h) {
+        hp = c.ws + q.h;
+        BL_TRY((launch_pack<T, PLANES>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, order, kept, q.ctas * kTileM, c.ws + q.h, q.ldp, h_plane,
+                                       c.sms, c.s)));
+        ldh = q.ldp;
+        h_rows = q.tiled;
+    }
+    CUtensorMap h_k;
+    BL_MAP(map_bf16(&h_k, hp, c.dim, h_rows, PLANES, ldh, q.copy_h ? h_plane : ldh, kTileM));
     GemmArgs base{};
-    base.status = status;
+    base.rows = rows;
+    base.kept = kept;
+    base.order = order;
+    base.flags = flags;
     base.pairs = q.pairs;
+    base.chunk = PLANES == 3 ? kChunkF32 : kWhole;
+    base.kb_per_split = kWhole;
+    base.splits = 1;
     base.target = c.target;
     base.vocab = c.vocab;
-    base.splits = 1;
-    base.chunk = PLANES == 3 ? kChunkF32 : kWhole;
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t v0 = i * q.piece, n = std::min(q.piece, c.vocab - v0);
         const char *const w_at = static_cast<const char *>(c.W) + v0 * c.ldw * static_cast<int64_t>(sizeof(T));
         const void *wp = w_at;
-        int64_t ldw = c.ldw, wpl = ldw;                     // one plane in place: its stride is not used
+        int64_t ldw = c.ldw, wpl = ldw;
         if (q.copy_w) {
-            BL_TRY((launch_pack<T, PLANES>(w_at, c.ldw, n, c.dim, nullptr, 0, c.ws + q.w, q.ldp, w_plane, nullptr, c.sms, c.s)));
+            BL_TRY((launch_pack<T, PLANES>(w_at, c.ldw, n, c.dim, nullptr, 0, nullptr, nullptr, 1, c.ws + q.w, q.ldp, w_plane, c.sms,
+                                           c.s)));
             wp = c.ws + q.w;
             ldw = q.ldp;
             wpl = w_plane;
         }
         CUtensorMap w_k;
-        BL_MAP(make_map(&w_k, wp, c.dim, n, PLANES, ldw, wpl, kTileN));
+        BL_MAP(map_bf16(&w_k, wp, c.dim, n, PLANES, ldw, wpl, kTileN / q.ctas));
         GemmArgs a = base;
-        a.m = static_cast<int>(c.rows);
+        a.m = rows;
         a.n = static_cast<int>(n);
         a.kblocks = static_cast<int>(cdiv(c.dim, kTileK));
-        a.kb_per_split = a.kblocks;
-        a.tiles_m = static_cast<int>(cdiv(c.rows, kTileM));
         a.tiles_n = static_cast<int>(cdiv(n, kTileN));
         a.v0 = static_cast<int>(v0);
         if (!q.grad) {
@@ -313,62 +469,64 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             a.part = reinterpret_cast<float2 *>(c.ws + q.part) + 2 * (v0 / kTileN);
             a.part_ld = q.part_ld;
             a.picked = reinterpret_cast<float *>(c.ws + q.picked);
-            BL_TRY((launch_gemm<LOGITS, PLANES>(h_k, w_k, a, c.sms, c.s)));
+            BL_TRY((launch_gemm<LOGITS, PLANES>(h_k, w_k, w_k, a, q.ctas, flag_count, c.sms, c.s)));
             continue;
         }
         char *const pp = c.ws + q.p;
-        const int64_t p_plane = c.rows * q.piece;
+        const int64_t p_plane = q.tiled * q.piece;
+        CUtensorMap p_out;
+        BL_MAP(map_bf16(&p_out, pp, n, q.tiled, PLANES, q.piece, p_plane, 32, PLANES == 1 ? 128 : 64));
         a.lse = c.lse_in;
         a.g = c.g;
-        a.p = reinterpret_cast<__nv_bfloat16 *>(pp);
-        a.ldp = q.piece;
-        a.p_plane = p_plane;
-        BL_TRY((launch_gemm<PROBS, PLANES>(h_k, w_k, a, c.sms, c.s)));
+        BL_TRY((launch_gemm<PROBS, PLANES>(h_k, w_k, p_out, a, q.ctas, flag_count, c.sms, c.s)));
         if (c.dH) {
-            CUtensorMap p_k, w_mn;
-            BL_MAP(make_map(&p_k, pp, n, c.rows, PLANES, q.piece, p_plane, kTileM));
-            BL_MAP(make_map(&w_mn, wp, c.dim, n, PLANES, ldw, wpl, kTileK));
+            CUtensorMap p_k, w_mn, sums;
+            BL_MAP(map_bf16(&p_k, pp, n, q.tiled, PLANES, q.piece, p_plane, kTileM));
+            BL_MAP(map_bf16(&w_mn, wp, c.dim, n, PLANES, ldw, wpl, kTileK));
+            BL_MAP(map_f32(&sums, c.ws + q.dh, c.dim, c.rows, q.splits, q.ldo, c.rows * q.ldo));
             GemmArgs d = base;
-            d.m = static_cast<int>(c.rows);
-            d.n = static_cast<int>(c.dim);
+            d.m = rows;
+            d.n = dim;
             d.kblocks = static_cast<int>(cdiv(n, kTileK));
             // the last piece may be shorter: its parts shrink, and every part still has a step
             d.kb_per_split = static_cast<int>(i == 0 ? q.kb_per_split : cdiv(d.kblocks, q.splits));
             d.splits = static_cast<int>(cdiv(d.kblocks, d.kb_per_split));
-            d.tiles_m = static_cast<int>(cdiv(c.rows, kTileM));
             d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
             d.accumulate = i > 0;
-            d.out = c.ws + q.dh;
-            d.ldo = q.ldo;
-            BL_TRY((launch_gemm<DH, PLANES>(p_k, w_mn, d, c.sms, c.s)));
+            BL_TRY((launch_gemm<DH, PLANES>(p_k, w_mn, sums, d, q.ctas, flag_count, c.sms, c.s)));
         }
         if (c.dW) {
-            CUtensorMap p_mn;
-            BL_MAP(make_map(&p_mn, pp, n, c.rows, PLANES, q.piece, p_plane, kTileK));
+            CUtensorMap p_mn, h_mn, to;
+            BL_MAP(map_bf16(&p_mn, pp, n, q.tiled, PLANES, q.piece, p_plane, kTileK));
+            BL_MAP(map_bf16(&h_mn, hp, c.dim, h_rows, PLANES, ldh, h_plane, kTileK));
             GemmArgs d = base;
             d.m = static_cast<int>(n);
-            d.n = static_cast<int>(c.dim);
-            d.kblocks = static_cast<int>(cdiv(c.rows, kTileK));
-            d.kb_per_split = d.kblocks;
-            d.tiles_m = static_cast<int>(cdiv(n, kTileM));
+            d.n = dim;
             d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
-            d.out = static_cast<char *>(c.dW) + v0 * c.lddw * static_cast<int64_t>(sizeof(T));
-            d.ldo = c.lddw;
-            d.out_vec = reinterpret_cast<uintptr_t>(c.dW) % 16 == 0 && c.lddw * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-            BL_TRY((launch_gemm<DW, PLANES>(p_mn, h_mn, d, c.sms, c.s)));
+            char *const out = static_cast<char *>(c.dW) + v0 * c.lddw * static_cast<int64_t>(sizeof(T));
+            if (!for_tma(c.dW, c.lddw, sizeof(T))) {
+                d.out = out;
+                d.ldo = c.lddw;
+                to = p_mn;
+            } else if (PLANES == 1) {
+                BL_MAP(map_bf16(&to, out, c.dim, n, 1, c.lddw, c.lddw, 32));
+            } else {
+                BL_MAP(map_f32(&to, out, c.dim, n, 1, c.lddw, c.lddw));
+            }
+            BL_TRY((launch_gemm<DW, PLANES>(p_mn, h_mn, to, d, q.ctas, flag_count, c.sms, c.s)));
         }
     }
     if (!q.grad) {
-        loss_kernel<<<static_cast<unsigned>(cdiv(c.rows, 8)), 256, 0, c.s>>>(
-            reinterpret_cast<const float2 *>(c.ws + q.part), q.part_ld, reinterpret_cast<const float *>(c.ws + q.picked),
-            c.target, c.vocab, static_cast<int>(c.rows), status, c.loss, c.lse);
-        BL_TRY(cudaGetLastError());
+        BL_TRY(launch_pdl(loss_kernel, static_cast<unsigned>(cdiv(c.rows, 8)), 256, 0, c.s,
+                          reinterpret_cast<const float2 *>(c.ws + q.part), q.part_ld, reinterpret_cast<const float *>(c.ws + q.picked),
+                          c.target, c.vocab, rows, order, kept, flags, flag_count, c.loss, c.lse));
     } else if (c.dH) {
-        const int64_t blocks = std::min<int64_t>(cdiv(c.rows * c.dim, 256), static_cast<int64_t>(c.sms) * 8);
-        dh_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, c.s>>>(reinterpret_cast<const float *>(c.ws + q.dh), q.splits,
-                                                                    q.ldo, c.target, c.vocab, c.rows, static_cast<int>(c.dim),
-                                                                    status, static_cast<T *>(c.dH), c.lddh);
-        BL_TRY(cudaGetLastError());
+        const int64_t blocks = std::min<int64_t>(cdiv(c.rows * cdiv(c.dim, 4), 256), static_cast<int64_t>(c.sms) * 8);
+        const int64_t es = sizeof(T);
+        const int vec = reinterpret_cast<uintptr_t>(c.dH) % (4 * es) == 0 && c.lddh % 4 == 0;
+        BL_TRY(launch_pdl(dh_kernel<T>, static_cast<unsigned>(blocks), 256, 0, c.s, reinterpret_cast<const float *>(c.ws + q.dh),
+                          q.splits, c.rows, q.ldo, c.target, c.vocab, place, dim, flags, flag_count, static_cast<T *>(c.dH), c.lddh,
+                          vec));
     }
     return BL_SUCCESS;
 }
@@ -422,7 +580,7 @@ bl_status entry(const char *op, int dtype, Call &c, bool grad, void *ws, int64_t
     if (st != BL_SUCCESS) return st;
     c.sms = sm_count();
     if (c.sms <= 0) return fail(BL_ERR_CUDA, "%s: cannot query the current CUDA device", op);
-    const Plan q = plan_for(dtype, c.rows, c.dim, c.vocab, c.W, c.ldw, grad, c.sms);
+    const Plan q = plan_for(dtype, c.H, c.ldh, c.rows, c.dim, c.vocab, c.W, c.ldw, grad, c.sms);
     if (ws_bytes < q.bytes)
         return fail(BL_ERR_INVALID_ARGUMENT, "%s: workspace of %lld bytes is smaller than %lld", op, (long long)ws_bytes,
                     (long long)q.bytes);
@@ -436,7 +594,8 @@ bl_status entry(const char *op, int dtype, Call &c, bool grad, void *ws, int64_t
 
 extern "C" {
 
-int64_t bl_xent_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw, int grad) {
+int64_t bl_xent_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
+                          const void *W, int64_t ldw, int grad) {
     using namespace bl::xent;
     bl::clear_error();
     if (check_shape("xent_workspace", dtype, rows, dim, vocab) != BL_SUCCESS) return -1;
@@ -445,7 +604,7 @@ int64_t bl_xent_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t voc
         bl::fail(BL_ERR_CUDA, "xent_workspace: cannot query the current CUDA device");
         return -1;
     }
-    return plan_for(dtype, rows, dim, vocab, W, ldw, grad != 0, sms).bytes;
+    return plan_for(dtype, H, ldh, rows, dim, vocab, W, ldw, grad != 0, sms).bytes;
 }
 
 bl_status bl_xent(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh, const void *W,

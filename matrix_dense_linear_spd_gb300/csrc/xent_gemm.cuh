@@ -5,8 +5,10 @@
 //   DH      dH = P W            A = P (K-major), B = W (MN-major); f32 partial sums
 //   DW      dW = P^T H          A = P (MN-major), B = H (MN-major); stored in W's type
 //
-// A CTA computes 128 x 256 tiles. One thread streams 64-deep operand tiles into a ring of shared
-// memory by TMA, one thread issues tcgen05.mma (bf16 operands, f32 accumulators in tensor
+// A CTA computes 128 x 256 tiles, or a pair of CTAs 256 x 256 tiles (CTAS = 2: each holds its 128
+// rows of A and of the result and half of B, so B crosses shared memory once for 256 rows). One
+// thread streams 64-deep operand tiles into a ring of shared memory by TMA, one thread (of the
+// pair's leader) issues tcgen05.mma (bf16 operands, f32 accumulators in tensor
 // memory), and eight warps turn finished accumulators into the mode's output while the next tile's
 // products already run: tensor memory holds two accumulators of 256 columns.
 //
@@ -19,8 +21,8 @@
 // product of f32 operands) the chain is cut into chunks of K, whose sums are added in registers.
 // Measured at rows 1024, dim 1024, vocabulary 32000, f32: dH 9.6e-6 off without chunks.
 //
-// Every wait is bounded: a role that gives up marks *status, waits (bounded) for its own copies
-// and products in flight, and leaves; the others then run out of time too.
+// Every wait is bounded: a role that gives up marks its CTA's flag, waits (bounded) for its own
+// copies and products in flight, and leaves; the others then run out of time too.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,6 +30,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "pdl.cuh"
 #include "tma_sm100.cuh"
 
 namespace bl {
@@ -35,31 +38,37 @@ namespace xent {
 
 enum Mode : int { LOGITS = 0, PROBS = 1, DH = 2, DW = 3 };
 
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
-constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2;
-constexpr int kStages = 4;
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;          // rows are each CTA's
 constexpr int kEpilogueWarps = 8, kHalf = kTileN / 2;           // two warps share 32 rows: 128 columns each
-constexpr int kStageRow = 17;                                   // f32 words per row of the store staging
-constexpr int kStagingBytes = kEpilogueWarps * 32 * kStageRow * 4;
-constexpr int kSmem = kStages * (kBytesA + kBytesB) + kStagingBytes + 1024;
+constexpr int kStageBytes = 32 * 128;                           // an epilogue warp's lines on their way out
+// Operand ring of a CTA that is one of CTAS that share a tile: A whole, its part of B.
+template <int CTAS>
+struct Ring {
+    static constexpr int kBytesA = kTileM * kTileK * 2, kRowsB = kTileN / CTAS, kBytesB = kRowsB * kTileK * 2;
+    static constexpr int kStages = CTAS == 1 ? 4 : 6;           // 192 KB
+    static constexpr int kSmem = kStages * (kBytesA + kBytesB) + kEpilogueWarps * kStageBytes + 1024;
+};
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;             // producer, issuer (and two idle warps), epilogue
 // 384 threads start with 168 registers each; the first four warps give most of theirs to the
-// epilogue, whose rows hold 128 sums: 128 * 40 + 256 * 232 = 384 * 168.
-constexpr int kRegsLaunch = 168, kRegsFew = 40, kRegsMany = 232;
+// epilogue, whose rows hold 128 sums: 128 * 56 + 256 * 224 = 384 * 168.
+constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
 static_assert(128 * kRegsFew + 32 * kEpilogueWarps * kRegsMany <= kThreads * kRegsLaunch, "more registers than the block has");
 constexpr uint32_t kPolls = 1u << 22;
 constexpr int kGroupM = 16;                                     // row tiles that share a column of B tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct GemmArgs {
-    int m, n;                  // rows and columns of the product
-    int kblocks;               // 64-deep steps of one pair of planes
+    int m, n;                  // rows and columns of the product (m: at most, see `kept`)
+    int rows;                  // rows of H
+    const int *kept;           // how many of them count; null: all. LOGITS, PROBS, DH: m; DW: K
+    const int *order;          // the rows that count, in order; null: every row in its place
+    int kblocks;               // 64-deep steps of one pair of planes (DW: follows from `kept`)
     int chunk;                 // of them, how many are added in tensor memory before registers take over
-    int tiles_m, tiles_n;
+    int tiles_n;
     int splits, kb_per_split;  // DH: the K axis is cut and every part has its own partial sums
     int pairs;                 // pairs of planes multiplied, 1 or 6
     int accumulate;            // DH: add to the partial sums of earlier pieces
-    int32_t *status;
+    int32_t *flags;            // one word per CTA: not 0 if it gave up
     // LOGITS, PROBS
     const int64_t *target;
     int64_t vocab;
@@ -68,12 +77,8 @@ struct GemmArgs {
     int64_t part_ld;
     float *picked;             // LOGITS: the target's logit of each row
     const float *lse, *g;      // PROBS
-    __nv_bfloat16 *p;          // PROBS: planes of [row][ldp]
-    int64_t ldp, p_plane;
-    // DH: f32 partial sums [split][m][ldo]; DW: the result's rows
-    void *out;
+    void *out;                 // DW: the result, where its rows do not start on 16-byte boundaries
     int64_t ldo;
-    int out_vec;               // DW: rows start on 16-byte boundaries
 };
 
 __device__ __forceinline__ void pair_of(int i, int pairs, int &a, int &b) {
@@ -85,25 +90,45 @@ __device__ __forceinline__ void pair_of(int i, int pairs, int &a, int &b) {
     b = (bs >> (4 * j)) & 15;
 }
 
-struct Work {
-    int tm, tn, split;
+// What depends on how many rows count. One row tile and one step of K remain where none does, so
+// that P and dW become zero.
+struct Shape {
+    int m, tiles_m, kblocks, total;
 };
-__device__ __forceinline__ Work work_of(int w, const GemmArgs &a) {
+template <int MODE, int CTAS>
+__device__ __forceinline__ Shape shape_of(const GemmArgs &a) {
+    const int kept = a.kept ? *a.kept : a.rows;
+    Shape s;
+    s.m = MODE == DW ? a.m : kept;
+    s.tiles_m = max(1, (s.m + CTAS * kTileM - 1) / (CTAS * kTileM));
+    s.kblocks = MODE == DW ? max(1, (kept + kTileK - 1) / kTileK) : a.kblocks;
+    s.total = s.tiles_m * a.tiles_n * a.splits;
+    return s;
+}
+
+struct Work {
+    int tm, tn, kb0, kb1, split;
+};
+__device__ __forceinline__ Work work_of(int w, const GemmArgs &a, const Shape &s) {
     Work r;
-    const int tiles = a.tiles_m * a.tiles_n;
+    const int tiles = s.tiles_m * a.tiles_n;
     r.split = w / tiles;
     w -= r.split * tiles;
     const int per = kGroupM * a.tiles_n, g = w / per;
     w -= g * per;
-    const int rest = a.tiles_m - g * kGroupM, gm = rest < kGroupM ? rest : kGroupM;
+    const int rest = s.tiles_m - g * kGroupM, gm = rest < kGroupM ? rest : kGroupM;
     r.tn = w / gm;
     r.tm = g * kGroupM + (w - r.tn * gm);
+    r.kb0 = r.split * a.kb_per_split;
+    r.kb1 = min(s.kblocks, r.kb0 + a.kb_per_split);
     return r;
 }
-// Columns of the tile that the product has, rounded up to the instruction's granularity.
+// Columns of the tile that the product has, rounded up to the instruction's granularity (16, or 32
+// for a pair, whose CTAs hold half of them each).
+template <int CTAS>
 __device__ __forceinline__ int cols_of(int tn, const GemmArgs &a) {
     const int left = a.n - tn * kTileN;
-    return left >= kTileN ? kTileN : (left + 15) & ~15;
+    return left >= kTileN ? kTileN : (left + 16 * CTAS - 1) & ~(16 * CTAS - 1);
 }
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
@@ -128,25 +153,27 @@ __device__ __forceinline__ void split3(float x, float &x0, float &x1, float &x2)
 // ---- epilogues. A warp owns 32 rows (a lane each) and 128 columns, in blocks of 32 columns.
 
 struct Row {              // what an epilogue keeps of its row
-    int row, at;          // row of the product; the target's column within this tile or -1
+    int row, m, at;       // row of the product, its rows; the target's column within this tile or -1
     bool counted;
     float top, sum, picked;    // LOGITS
     float lse, ref, g;         // PROBS
 };
 
 template <int MODE>
-__device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Work &w, int row) {
+__device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s, const Work &w, int row) {
     r.row = row;
+    r.m = s.m;
     if constexpr (MODE == LOGITS || MODE == PROBS) {
         const int n0 = w.tn * kTileN;
-        const int64_t t = row < a.m ? a.target[row] : -1, at = t - a.v0 - n0;
+        const int64_t src = row < s.m ? (a.order ? a.order[row] : row) : -1;
+        const int64_t t = src >= 0 ? a.target[src] : -1, at = t - a.v0 - n0;
         r.counted = t >= 0 && t < a.vocab;
         r.at = r.counted && at >= 0 && at < min(a.n - n0, kTileN) ? static_cast<int>(at) : -1;
         r.top = -INFINITY;
         r.sum = r.picked = 0.f;
         if constexpr (MODE == PROBS) {
-            r.lse = r.counted ? a.lse[row] : 0.f;
-            r.g = r.counted ? a.g[row] : 0.f;
+            r.lse = r.counted ? a.lse[src] : 0.f;
+            r.g = r.counted ? a.g[src] : 0.f;
             r.ref = r.lse * kLog2e;
         }
     }
@@ -173,130 +200,145 @@ __device__ __forceinline__ void block_logits(Row &r, const GemmArgs &a, const Wo
     r.top = m;
 }
 
-template <int PLANES>
-__device__ __forceinline__ void block_probs(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        // the f32 form keeps s - lse exact where it can; the bf16 form rounds the result to 8
-        // bits anyway
-        float e = PLANES == 1 ? exp2f(fmaf(v[i], kLog2e, -r.ref)) : expf(v[i] - r.lse);
-        if (i == r.at - c0) e -= 1.f;
-        v[i] = r.counted ? r.g * e : 0.f;
-    }
-    if (r.row >= a.m) return;
-    __nv_bfloat16 *const dst = a.p + static_cast<int64_t>(r.row) * a.ldp + w.tn * kTileN + c0;
-    if constexpr (PLANES == 1) {
-        uint4 *const q = reinterpret_cast<uint4 *>(dst);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            q[j] = make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                              bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float x[3][8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) split3(v[8 * j + i], x[0][i], x[1][i], x[2][i]);
-#pragma unroll
-            for (int pl = 0; pl < 3; ++pl)
-                *reinterpret_cast<uint4 *>(dst + pl * a.p_plane + 8 * j) =
-                    make_uint4(bf16x2(x[pl][0], x[pl][1]), bf16x2(x[pl][2], x[pl][3]),
-                               bf16x2(x[pl][4], x[pl][5]), bf16x2(x[pl][6], x[pl][7]));
-        }
-    }
-}
-
-__device__ __forceinline__ void block_dh(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
-    if (r.row >= a.m) return;
-    float4 *const q = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
-                                                 (static_cast<int64_t>(w.split) * a.m + r.row) * a.ldo + w.tn * kTileN + c0);
-    if (a.accumulate) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float4 o = q[j];
-            v[4 * j] += o.x, v[4 * j + 1] += o.y, v[4 * j + 2] += o.z, v[4 * j + 3] += o.w;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-}
-
-// A row that starts on a 16-byte boundary and has all 32 columns.
-template <typename T>
-__device__ __forceinline__ void block_dw(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
-    if (r.row >= a.m) return;
-    T *const dst = static_cast<T *>(a.out) + r.row * a.ldo + w.tn * kTileN + c0;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            reinterpret_cast<float4 *>(dst)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            reinterpret_cast<uint4 *>(dst)[j] =
-                make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                           bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
-    }
-}
-
-// Rows that start anywhere, or end within the block: through shared memory, 16 columns at a time,
-// so that a warp stores along its rows.
-template <typename T>
-__device__ __forceinline__ void block_dw_any(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32],
-                                             float *staging) {
-    const int left = a.n - w.tn * kTileN - c0, lane = threadIdx.x & 31, rows = a.m - (r.row - lane);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) staging[lane * kStageRow + i] = v[16 * h + i];
-        __syncwarp();
-        const int col = 16 * h + (lane & 15);
-        T *p = static_cast<T *>(a.out) + (r.row - lane + (lane >> 4)) * a.ldo + w.tn * kTileN + c0 + col;
-#pragma unroll 1
-        for (int q = lane >> 4; q < 32 && q < rows && col < left; q += 2, p += 2 * a.ldo)
-            put(p, staging[q * kStageRow + (lane & 15)]);
-    }
-}
-
-template <int MODE, int PLANES, bool ANY>
-__device__ __forceinline__ void block(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32], float *staging) {
-    using T = std::conditional_t<PLANES == 1, __nv_bfloat16, float>;
-    if constexpr (MODE == LOGITS) block_logits(r, a, w, c0, v);
-    else if constexpr (MODE == PROBS) block_probs<PLANES>(r, a, w, c0, v);
-    else if constexpr (MODE == DH) block_dh(r, a, w, c0, v);
-    else if constexpr (ANY) block_dw_any<T>(r, a, w, c0, v, staging);
-    else block_dw<T>(r, a, w, c0, v);
-}
-
 template <int MODE>
 __device__ __forceinline__ void end(const Row &r, const GemmArgs &a, const Work &w, int half) {
     if constexpr (MODE == LOGITS) {
-        if (r.row < a.m) {
+        if (r.row < r.m) {
             a.part[r.row * a.part_ld + 2 * w.tn + half] = make_float2(r.top, r.sum);
             if (r.at >= half * kHalf && r.at < (half + 1) * kHalf) a.picked[r.row] = r.picked;
         }
     }
 }
 
+// Results leave through a warp's 4 KB of shared memory: 32 lines (a lane's row each) of 128 bytes,
+// in the 128-byte swizzle, that one thread hands to TMA. Lines are stored whole whatever the
+// lanes hold, and TMA drops what lies past the result's edges.
+__device__ __forceinline__ void line_put(unsigned char *stage, int chunk, uint4 q) {
+    const int lane = threadIdx.x & 31;
+    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = q;
+}
+__device__ __forceinline__ void lines_free() {          // the last store has read its lines
+    if ((threadIdx.x & 31) == 0) tc::bulk_wait_read_all();
+    __syncwarp();
+}
+__device__ __forceinline__ void lines_store(const CUtensorMap *map, unsigned char *stage, int x, int y, int z, bool add) {
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        tc::tma_store_3d(map, stage, x, y, z, add);
+        tc::bulk_commit();
+    }
+}
+__device__ __forceinline__ void put_bf16(unsigned char *stage, int c0, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        line_put(stage, (c0 & 32) / 8 + j, make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                                      bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7])));
+}
+
+// DW, where the result's rows start off the 16-byte boundaries that TMA wants: the warp stores the
+// lines itself, one row after the other.
+template <typename T>
+__device__ __forceinline__ void lines_copy(const GemmArgs &a, const unsigned char *stage, int row0, int col0) {
+    constexpr int PER = 4 / sizeof(T);                  // values in a lane's word
+    const int lane = threadIdx.x & 31, rows = min(32, a.m - row0), col = col0 + lane * PER;
+    T *p = static_cast<T *>(a.out) + row0 * a.ldo + col;
+    __syncwarp();
+#pragma unroll 1
+    for (int q = 0; q < rows; ++q, p += a.ldo) {
+        const uint32_t x = *reinterpret_cast<const uint32_t *>(stage + q * 128 + (((lane >> 2) ^ (q & 7)) << 4) + (lane & 3) * 4);
+        if constexpr (PER == 1) {
+            if (col < a.n) *p = __uint_as_float(x);
+        } else {
+            const __nv_bfloat162 t = *reinterpret_cast<const __nv_bfloat162 *>(&x);
+            if (col < a.n) p[0] = t.x;
+            if (col + 1 < a.n) p[1] = t.y;
+        }
+    }
+    __syncwarp();
+}
+
+// PROBS, DH and DW. `cols`: where this warp's columns of the tile end. A line holds two blocks of
+// bf16 values or one of f32 values.
 template <int MODE, int PLANES>
+__device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const Work &w, int c0, int cols, float (&v)[32],
+                                          const CUtensorMap *map, unsigned char *stage) {
+    const int n0 = w.tn * kTileN, row0 = r.row - (threadIdx.x & 31);
+    if constexpr (MODE == PROBS) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            // the f32 form keeps s - lse exact where it can; the bf16 form rounds the result to 8
+            // bits anyway
+            float e = PLANES == 1 ? exp2f(fmaf(v[i], kLog2e, -r.ref)) : expf(v[i] - r.lse);
+            if (i == r.at - c0) e -= 1.f;
+            v[i] = r.counted ? r.g * e : 0.f;
+        }
+    }
+    const bool there = MODE == PROBS || row0 < r.m;      // P has whole row tiles; rows that do not count are zero
+    if constexpr (MODE == DH || PLANES == 3) {
+        if constexpr (MODE == PROBS) {
+            // three planes of 32 values: 64 bytes a line each
+#pragma unroll
+            for (int pl = 0; pl < 3; ++pl) {
+                lines_free();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = __bfloat162float(__float2bfloat16_rn(v[8 * j + i]));
+                        v[8 * j + i] -= x[i];
+                    }
+                    *reinterpret_cast<uint4 *>(stage + (threadIdx.x & 31) * 64 + ((j ^ ((threadIdx.x >> 1) & 3)) << 4)) =
+                        make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+                }
+                lines_store(map, stage, n0 + c0, row0, pl, false);
+            }
+        } else {
+            lines_free();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                line_put(stage, j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                              __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+            if (MODE == DW && a.out) lines_copy<float>(a, stage, row0, n0 + c0);
+            else if (there) lines_store(map, stage, n0 + c0, row0, MODE == DH ? w.split : 0, MODE == DH && a.accumulate);
+        }
+    } else {
+        if ((c0 & 32) == 0) lines_free();
+        put_bf16(stage, c0, v);
+        if ((c0 & 32) || c0 + 32 >= cols) {
+            if (MODE == DW && a.out) lines_copy<__nv_bfloat16>(a, stage, row0, n0 + (c0 & ~63));
+            else if (there) lines_store(map, stage, n0 + (c0 & ~63), row0, 0, false);
+        }
+    }
+}
+
+template <int MODE, int PLANES>
+__device__ __forceinline__ void block(Row &r, const GemmArgs &a, const Work &w, int c0, int cols, float (&v)[32],
+                                      const CUtensorMap *map, unsigned char *stage) {
+    if constexpr (MODE == LOGITS) block_logits(r, a, w, c0, v);
+    else block_out<MODE, PLANES>(r, a, w, c0, cols, v, map, stage);
+}
+
+template <int MODE, int PLANES, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ GemmArgs a) {
+                const __grid_constant__ CUtensorMap map_out, const __grid_constant__ GemmArgs a) {
+    using R = Ring<CTAS>;
+    constexpr int kBytesA = R::kBytesA, kBytesB = R::kBytesB, kStages = R::kStages;
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DH || MODE == DW;
     constexpr bool SUMS = MODE == LOGITS || PLANES == 3;      // chunks are added in registers
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kBytesA;
-    float *const staging = reinterpret_cast<float *>(base + kStages * (kBytesA + kBytesB));
+    unsigned char *const staging = base + kStages * (kBytesA + kBytesB);
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (warp == 1) {
-        tc::tmem_alloc(&tmem_slot, 512);
-        tc::tmem_relinquish();
-    }
+    const uint32_t rank = CTAS == 1 ? 0 : tc::cluster_rank();
+    if (warp == 1) tc::tmem_take<CTAS>(&tmem_slot, 512);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(&full[s], 1);
@@ -304,80 +346,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&acc_full[s], 1);
-            tc::mbar_init(&acc_empty[s], 32 * kEpilogueWarps);
+            tc::mbar_init(&acc_empty[s], CTAS * kEpilogueWarps);
         }
         tc::mbar_init(&drained, 1);
         tc::mbar_fence_init();
+        gave_up = 0;
         tc::tma_prefetch_map(&map_a);
         tc::tma_prefetch_map(&map_b);
+        tc::tma_prefetch_map(&map_out);
     }
+    __syncwarp();
+    pdl_release();
     tc::fence_before_sync();
-    __syncthreads();
+    if constexpr (CTAS == 1) __syncthreads();
+    else tc::cluster_sync();                 // the peer's barriers are ready too
     tc::fence_after_sync();
+    pdl_wait();
     const uint32_t tmem = tmem_slot;
-    const int total = a.tiles_m * a.tiles_n * a.splits;
 
     if (warp < 4) {
       tc::regs_dec<kRegsFew>();
       if (warp == 0) {
         if (lane == 0) {
+            const Shape sh = shape_of<MODE, CTAS>(a);
             uint32_t it = 0;
             bool ok = true;
-            for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-                const Work k = work_of(w, a);
-                const int m0 = k.tm * kTileM, n0 = k.tn * kTileN;
-                const int kb0 = k.split * a.kb_per_split, kb1 = min(a.kblocks, kb0 + a.kb_per_split);
-                const int groups_b = (cols_of(k.tn, a) + 63) >> 6;
-                const uint32_t bytes = kBytesA + (B_MN ? groups_b * (kTileK * 128) : kBytesB);
-                for (int c = kb0; ok && c < kb1; c += a.chunk)
+            for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
+                const Work k = work_of(w, a, sh);
+                const int part = cols_of<CTAS>(k.tn, a) / CTAS;       // this CTA's columns of B
+                const int m0 = (k.tm * CTAS + rank) * kTileM, n0 = k.tn * kTileN + rank * part;
+                const int groups_b = (part + 63) >> 6;
+                const uint32_t bytes = CTAS * (kBytesA + (B_MN ? groups_b * (kTileK * 128) : kBytesB));
+                for (int c = k.kb0; ok && c < k.kb1; c += a.chunk)
                 for (int pr = 0; ok && pr < a.pairs; ++pr) {
                     int pa, pb;
                     pair_of(pr, a.pairs, pa, pb);
-                    for (int kb = c; kb < min(c + a.chunk, kb1); ++kb, ++it) {
+                    for (int kb = c; kb < min(c + a.chunk, k.kb1); ++kb, ++it) {
                         const uint32_t s = it % kStages;
                         if (!tc::mbar_wait(&empty[s], (it / kStages & 1) ^ 1, kPolls)) {
                             ok = false;
                             break;
                         }
-                        tc::mbar_expect_tx(&full[s], bytes);
+                        if (rank == 0) tc::mbar_expect_tx(&full[s], bytes);      // of both CTAs
+                        const uint32_t bar = CTAS == 1 ? tc::smem_u32(&full[s]) : tc::at_leader(&full[s]);
                         unsigned char *const da = tiles_a + s * kBytesA, *const db = tiles_b + s * kBytesB;
                         if constexpr (A_MN) {
                             for (int j = 0; j < kTileM / 64; ++j)
-                                tc::tma_load_3d(da + j * kTileK * 128, &map_a, &full[s], m0 + 64 * j, kb * kTileK, pa);
+                                tc::tma_load_3d<CTAS>(da + j * kTileK * 128, &map_a, bar, m0 + 64 * j, kb * kTileK, pa);
                         } else {
-                            tc::tma_load_3d(da, &map_a, &full[s], kb * kTileK, m0, pa);
+                            tc::tma_load_3d<CTAS>(da, &map_a, bar, kb * kTileK, m0, pa);
                         }
                         if constexpr (B_MN) {
+#pragma unroll 1
                             for (int j = 0; j < groups_b; ++j)
-                                tc::tma_load_3d(db + j * kTileK * 128, &map_b, &full[s], n0 + 64 * j, kb * kTileK, pb);
+                                tc::tma_load_3d<CTAS>(db + j * kTileK * 128, &map_b, bar, n0 + 64 * j, kb * kTileK, pb);
                         } else {
-                            tc::tma_load_3d(db, &map_b, &full[s], kb * kTileK, n0, pb);
+                            tc::tma_load_3d<CTAS>(db, &map_b, bar, kb * kTileK, n0, pb);
                         }
                     }
                 }
             }
             if (!ok) {
-                atomicExch(a.status, 2);
-                for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                gave_up = 1;
+                for (uint32_t i = rank != 0 ? it : it > kStages ? it - kStages : 0; i < it; ++i)
                     tc::mbar_wait(&full[i % kStages], i / kStages & 1, kPolls);
             }
         }
       } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
+            const Shape sh = shape_of<MODE, CTAS>(a);
             uint32_t it = 0, done = 0;
             bool ok = true;
-            for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-                const Work k = work_of(w, a);
-                const int kb0 = k.split * a.kb_per_split, kb1 = min(a.kblocks, kb0 + a.kb_per_split);
-                const uint32_t idesc = tc::idesc_bf16(kTileM, cols_of(k.tn, a), A_MN, B_MN);
-                for (int c = kb0; ok && c < kb1; c += a.chunk, ++done) {
+            for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
+                const Work k = work_of(w, a, sh);
+                const uint32_t idesc = tc::idesc_bf16(CTAS * kTileM, cols_of<CTAS>(k.tn, a), A_MN, B_MN);
+                for (int c = k.kb0; ok && c < k.kb1; c += a.chunk, ++done) {
                     const uint32_t acc = tmem + (done & 1) * kTileN;
                     if (!tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    const int steps = (min(c + a.chunk, kb1) - c) * a.pairs;
+                    const int steps = (min(c + a.chunk, k.kb1) - c) * a.pairs;
                     for (int i = 0; i < steps; ++i, ++it) {
                         const uint32_t s = it % kStages;
                         if (!tc::mbar_wait(&full[s], it / kStages & 1, kPolls)) {
@@ -390,16 +440,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t db = B_MN ? tc::sdesc_mn_sw128(sb, kTileK * 128) : tc::sdesc_sw128(sb);
 #pragma unroll
                         for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
-                            tc::mma_f16(acc, da + j * (A_MN ? 2048 / 16 : 2), db + j * (B_MN ? 2048 / 16 : 2), idesc,
+                            tc::mma_f16<CTAS>(acc, da + j * (A_MN ? 2048 / 16 : 2), db + j * (B_MN ? 2048 / 16 : 2), idesc,
                                         i > 0 || j > 0);
-                        tc::mma_commit(&empty[s]);
+                        tc::mma_commit_all<CTAS>(&empty[s]);
                     }
-                    if (ok) tc::mma_commit(&acc_full[done & 1]);
+                    if (ok) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
                 }
             }
             if (!ok) {
-                atomicExch(a.status, 2);
-                tc::mma_commit(&drained);
+                gave_up = 1;
+                tc::mma_commit_all<CTAS>(&drained);
                 tc::mbar_wait(&drained, 0, kPolls);
             }
         }
@@ -407,16 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         tc::regs_inc<kRegsMany>();
         const int quad = warp & 3, half = (warp - 4) >> 2;  // a warp may read its quarter of the lanes
-        float *const stage = staging + (warp - 4) * 32 * kStageRow;
+        unsigned char *const stage = staging + (warp - 4) * kStageBytes;
+        const Shape sh = shape_of<MODE, CTAS>(a);
         uint32_t done = 0;
         bool ok = true;
-        for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
-            const Work k = work_of(w, a);
+        for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
+            const Work k = work_of(w, a, sh);
             const int cols = min(a.n - k.tn * kTileN, (half + 1) * kHalf);     // this warp's columns end there
-            const int kb0 = k.split * a.kb_per_split, kb1 = min(a.kblocks, kb0 + a.kb_per_split);
-            const bool any = MODE == DW && !(a.out_vec && cols == (half + 1) * kHalf);
             Row r;
-            begin<MODE>(r, a, k, k.tm * kTileM + quad * 32 + lane);
+            begin<MODE>(r, a, sh, k, (k.tm * CTAS + rank) * kTileM + quad * 32 + lane);
             float v[SUMS ? kHalf / 32 : 1][32];
             if constexpr (SUMS) {
 #pragma unroll
@@ -425,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i) v[b][i] = 0.f;
             }
 #pragma unroll 1
-            for (int c = kb0; c < kb1; c += a.chunk, ++done) {
+            for (int c = k.kb0; c < k.kb1; c += a.chunk, ++done) {
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls));
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -446,38 +495,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
                         __syncwarp();
                         tc::tmem_ld32(acc + c0, v[0]);
-                        if (any) block<MODE, PLANES, true>(r, a, k, c0, v[0], stage);
-                        else block<MODE, PLANES, false>(r, a, k, c0, v[0], stage);
+                        block<MODE, PLANES>(r, a, k, c0, cols, v[0], &map_out, stage);
                     }
                 }
                 __syncwarp();
                 tc::fence_before_sync();
-                tc::mbar_arrive(&acc_empty[done & 1]);
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[done & 1]);
+                    else tc::mbar_arrive_at(tc::at_leader(&acc_empty[done & 1]));
+                }
             }
             if (!ok) {
-                if (lane == 0) atomicExch(a.status, 2);
+                if (lane == 0) gave_up = 1;
                 break;
             }
             if constexpr (SUMS) {
-                if (any) {
 #pragma unroll
-                    for (int b = 0; b < kHalf / 32; ++b)
-                        if (half * kHalf + 32 * b < cols) block<MODE, PLANES, true>(r, a, k, half * kHalf + 32 * b, v[b], stage);
-                } else {
-#pragma unroll
-                    for (int b = 0; b < kHalf / 32; ++b)
-                        if (half * kHalf + 32 * b < cols) block<MODE, PLANES, false>(r, a, k, half * kHalf + 32 * b, v[b], stage);
-                }
+                for (int b = 0; b < kHalf / 32; ++b)
+                    if (half * kHalf + 32 * b < cols)
+                        block<MODE, PLANES>(r, a, k, half * kHalf + 32 * b, cols, v[b], &map_out, stage);
                 __syncwarp();
             }
             end<MODE>(r, a, k, half);
         }
+        if (MODE != LOGITS && lane == 0) tc::bulk_wait_all();
     }
     __syncwarp();
     tc::fence_before_sync();
-    __syncthreads();
+    if constexpr (CTAS == 1) __syncthreads();
+    else tc::cluster_sync();                 // nothing of the pair's is in flight towards either CTA
     tc::fence_after_sync();
-    if (warp == 1) tc::tmem_dealloc(tmem, 512);
+    if (warp == 1) tc::tmem_give<CTAS>(tmem, 512);
+    if (threadIdx.x == 0) a.flags[blockIdx.x] = gave_up;
 }
 
 }  // namespace xent

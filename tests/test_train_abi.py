@@ -73,4 +73,4 @@ def test_matrix_ops_refuse_the_training_types(bl):
     lib = bl.get_lib()
     for dtype in (bl.BL_BF16, bl.BL_F16):
         assert lib.bl_potrf(0, dtype, 4, 1, F, 4, 16, F, None) == 1
-    assert lib.bl_xent_workspace(1, 8, 16, 32, F, 16, 0) == -1
+    assert lib.bl_xent_workspace(1, 8, 16, 32, F, 16, F, 16, 0) == -1
