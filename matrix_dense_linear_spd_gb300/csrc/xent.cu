@@ -67,17 +67,17 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0) *kept = before;
 }
 
-// Copy rows into bf16 planes of row length ldp (a multiple of 8; the tail is zero). With `order`
-// row j of the copy is row order[j]; whole row tiles are filled, with zeros after the last row. Rows
-// without a target (`target` given) become zero too.
+// Copy rows into bf16 planes of 64-column panels ([plane][panel][height][64]); columns past dim are
+// zero. With `order` row j of the copy is row order[j]; whole row tiles are filled, with zeros after
+// the last row. Rows without a target (`target` given) become zero too.
 template <typename T, int PLANES>
 __global__ void __launch_bounds__(256)
     pack_kernel(const T *src, int64_t ld, int64_t rows, int dim, const int64_t *target, int64_t vocab, const int *order,
-                const int *kept, int tile, __nv_bfloat16 *dst, int64_t ldp, int64_t plane, int vec) {
+                const int *kept, int tile, __nv_bfloat16 *dst, int panels, int64_t height, int vec) {
     pdl_release();
     pdl_wait();
     const int64_t count = kept ? *kept : rows, filled = max((count + tile - 1) / tile, int64_t(1)) * tile;
-    const int64_t per_row = ldp / 8, all = filled * per_row;
+    const int64_t per_row = panels * 8, all = filled * per_row, plane = panels * height * 64;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all;
          i += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t j = i / per_row;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = c + e < dim ? s[e] : T(0.f);
         }
-        __nv_bfloat16 *const d = dst + j * ldp + c;
+        __nv_bfloat16 *const d = dst + ((c >> 6) * height + j) * 64 + (c & 63);
         if constexpr (PLANES == 1) {
             *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(x);
         } else {
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ plan
 
 // K is added in tensor memory over so many 64-deep steps at a time where the result is f32
-constexpr int kChunkF32 = 4, kChunkLoss = 8, kWhole = 1 << 30;
+constexpr int kChunkF32 = 4, kChunkLoss = 16, kWhole = 1 << 30;
 constexpr int64_t kPieceBytes = int64_t(512) << 20;     // of P, and of a piece's copy of W
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -206,7 +206,7 @@ struct Plan {
     bool copy_h, copy_w, compact, grad;
     int64_t rows, dim, vocab;
     int64_t tiled;            // rows of the copy of H and of P: whole tiles
-    int64_t ldp;              // row length of the copies of H and W
+    int64_t panels;           // of 64 columns in the copies of H and W
     int64_t piece, pieces;    // vocabulary entries per piece
     int64_t part_ld;          // partial maxima and sums of a row: two per tile
     int splits;
@@ -248,12 +248,12 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     q.dim = dim;
     q.vocab = vocab;
     q.tiled = up(rows, q.ctas * kTileM);
-    q.ldp = up(dim, 8);
+    q.panels = cdiv(dim, 64);
     // a piece: what keeps P and the copy of W within their size, but 4096 entries at least, so
     // that a piece's products fill the GPU; pieces of one size
     int64_t most = up(vocab, kTileN);
     if (grad) most = std::min(most, kPieceBytes / (q.tiled * 2 * q.planes));
-    if (q.copy_w) most = std::min(most, kPieceBytes / (q.ldp * 2 * q.planes));
+    if (q.copy_w) most = std::min(most, kPieceBytes / (q.panels * 128 * q.planes));
     most = std::max<int64_t>(most / kTileN * kTileN, 4096);
     q.pieces = cdiv(vocab, most);
     q.piece = up(cdiv(vocab, q.pieces), kTileN);
@@ -276,8 +276,8 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
         q.order = take(rows * 4);
         q.place = take(rows * 4);
     }
-    if (q.copy_h) q.h = take(q.planes * q.tiled * q.ldp * 2);
-    if (q.copy_w) q.w = take(q.planes * std::min(q.piece, vocab) * q.ldp * 2);
+    if (q.copy_h) q.h = take(q.planes * q.tiled * q.panels * 128);
+    if (q.copy_w) q.w = take(q.planes * std::min(q.piece, vocab) * q.panels * 128);
     if (!grad) {
         q.part = take(rows * q.part_ld * 8);
         q.picked = take(rows * 4);
@@ -323,6 +323,11 @@ bool make_map(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *
 bool map_bf16(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t planes, int64_t ld, int64_t plane,
               int box_rows, int line_bytes = 128) {
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, rows, planes, ld, plane, box_rows, line_bytes);
+}
+// The first `rows` rows of 64-column panels of `height` rows.
+bool map_panels(CUtensorMap *map, const void *base, int64_t rows, int64_t height, int64_t panels, int box_rows,
+                int line_bytes = 128) {
+    return map_bf16(map, base, 64, rows, panels, 64, height * 64, box_rows, line_bytes);
 }
 bool map_f32(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t planes, int64_t ld, int64_t plane) {
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, inner, rows, planes, ld, plane, 32);
@@ -375,12 +380,13 @@ cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUte
 
 template <typename T, int PLANES>
 cudaError_t launch_pack(const void *src, int64_t ld, int64_t rows, int64_t dim, const int64_t *target, int64_t vocab,
-                        const int *order, const int *kept, int tile, void *dst, int64_t ldp, int64_t plane, int sms,
-                        cudaStream_t s) {
+                        const int *order, const int *kept, int tile, void *dst, int64_t height, int sms, cudaStream_t s) {
     const int vec = for_tma(src, ld, sizeof(T));
-    const int64_t blocks = std::min<int64_t>(cdiv(up(rows, tile) * (ldp / 8), 256), static_cast<int64_t>(sms) * 8);
+    const int64_t panels = cdiv(dim, 64);
+    const int64_t blocks = std::min<int64_t>(cdiv(up(rows, tile) * panels * 8, 256), static_cast<int64_t>(sms) * 8);
     return launch_pdl(pack_kernel<T, PLANES>, static_cast<unsigned>(blocks), 256, 0, s, static_cast<const T *>(src), ld, rows,
-                      static_cast<int>(dim), target, vocab, order, kept, tile, static_cast<__nv_bfloat16 *>(dst), ldp, plane, vec);
+                      static_cast<int>(dim), target, vocab, order, kept, tile, static_cast<__nv_bfloat16 *>(dst),
+                      static_cast<int>(panels), height, vec);
 }
 
 struct Call {
@@ -413,26 +419,24 @@ struct Call {
 
 template <typename T, int PLANES>
 bl_status run(const char *op, const Plan &q, const Call &c) {
-    const int64_t h_plane = q.tiled * q.ldp, piece_w = std::min(q.piece, c.vocab), w_plane = piece_w * q.ldp;
+    const int64_t piece_w = std::min(q.piece, c.vocab);
     const int rows = static_cast<int>(c.rows), dim = static_cast<int>(c.dim);
     int *const kept = q.compact ? reinterpret_cast<int *>(c.ws + q.kept) : nullptr;
     int *const order = q.compact ? reinterpret_cast<int *>(c.ws + q.order) : nullptr;
     int *const place = q.compact ? reinterpret_cast<int *>(c.ws + q.place) : nullptr;
     int32_t *const flags = reinterpret_cast<int32_t *>(c.ws + q.flags);
     int flag_count = 0;
-    const void *hp = c.H;
-    int64_t ldh = c.ldh, h_rows = c.rows;
     if (q.compact)
         BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept, c.loss, c.lse));
-    if (q.copy_h) {
-        hp = c.ws + q.h;
-        BL_TRY((launch_pack<T, PLANES>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, order, kept, q.ctas * kTileM, c.ws + q.h, q.ldp, h_plane,
-                                       c.sms, c.s)));
-        ldh = q.ldp;
-        h_rows = q.tiled;
-    }
+    const Columns in_place{64, 0, 1}, in_panels{0, 1, static_cast<int>(q.panels)};
     CUtensorMap h_k;
-    BL_MAP(map_bf16(&h_k, hp, c.dim, h_rows, PLANES, ldh, q.copy_h ? h_plane : ldh, kTileM));
+    if (q.copy_h) {
+        BL_TRY((launch_pack<T, PLANES>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, order, kept, q.ctas * kTileM, c.ws + q.h, q.tiled,
+                                       c.sms, c.s)));
+        BL_MAP(map_panels(&h_k, c.ws + q.h, q.tiled, q.tiled, PLANES * q.panels, kTileM));
+    } else {
+        BL_MAP(map_bf16(&h_k, c.H, c.dim, c.rows, 1, c.ldh, c.ldh, kTileM));
+    }
     GemmArgs base{};
     base.rows = rows;
     base.kept = kept;
@@ -447,23 +451,24 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t v0 = i * q.piece, n = std::min(q.piece, c.vocab - v0);
         const char *const w_at = static_cast<const char *>(c.W) + v0 * c.ldw * static_cast<int64_t>(sizeof(T));
-        const void *wp = w_at;
-        int64_t ldw = c.ldw, wpl = ldw;
+        CUtensorMap w_k, w_mn;
         if (q.copy_w) {
-            BL_TRY((launch_pack<T, PLANES>(w_at, c.ldw, n, c.dim, nullptr, 0, nullptr, nullptr, 1, c.ws + q.w, q.ldp, w_plane, c.sms,
-                                           c.s)));
-            wp = c.ws + q.w;
-            ldw = q.ldp;
-            wpl = w_plane;
+            BL_TRY((launch_pack<T, PLANES>(w_at, c.ldw, n, c.dim, nullptr, 0, nullptr, nullptr, 1, c.ws + q.w, piece_w, c.sms, c.s)));
+            BL_MAP(map_panels(&w_k, c.ws + q.w, n, piece_w, PLANES * q.panels, kTileN / q.ctas));
+            BL_MAP(map_panels(&w_mn, c.ws + q.w, n, piece_w, PLANES * q.panels, kTileK));
+        } else {
+            BL_MAP(map_bf16(&w_k, w_at, c.dim, n, 1, c.ldw, c.ldw, kTileN / q.ctas));
+            BL_MAP(map_bf16(&w_mn, w_at, c.dim, n, 1, c.ldw, c.ldw, kTileK));
         }
-        CUtensorMap w_k;
-        BL_MAP(map_bf16(&w_k, wp, c.dim, n, PLANES, ldw, wpl, kTileN / q.ctas));
+        const Columns cols_h = q.copy_h ? in_panels : in_place, cols_w = q.copy_w ? in_panels : in_place;
         GemmArgs a = base;
         a.m = rows;
         a.n = static_cast<int>(n);
         a.kblocks = static_cast<int>(cdiv(c.dim, kTileK));
         a.tiles_n = static_cast<int>(cdiv(n, kTileN));
         a.v0 = static_cast<int>(v0);
+        a.ca = cols_h;
+        a.cb = cols_w;
         if (!q.grad) {
             if (PLANES == 1) a.chunk = kChunkLoss;
             a.part = reinterpret_cast<float2 *>(c.ws + q.part) + 2 * (v0 / kTileN);
@@ -473,16 +478,17 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             continue;
         }
         char *const pp = c.ws + q.p;
-        const int64_t p_plane = q.tiled * q.piece;
+        const int64_t p_panels = cdiv(n, 64);
+        const Columns cols_p{0, 1, static_cast<int>(p_panels)};
         CUtensorMap p_out;
-        BL_MAP(map_bf16(&p_out, pp, n, q.tiled, PLANES, q.piece, p_plane, 32, PLANES == 1 ? 128 : 64));
+        BL_MAP(map_panels(&p_out, pp, q.tiled, q.tiled, PLANES * p_panels, 32, PLANES == 1 ? 128 : 64));
+        a.p_panels = static_cast<int>(p_panels);
         a.lse = c.lse_in;
         a.g = c.g;
         BL_TRY((launch_gemm<PROBS, PLANES>(h_k, w_k, p_out, a, q.ctas, flag_count, c.sms, c.s)));
         if (c.dH) {
-            CUtensorMap p_k, w_mn, sums;
-            BL_MAP(map_bf16(&p_k, pp, n, q.tiled, PLANES, q.piece, p_plane, kTileM));
-            BL_MAP(map_bf16(&w_mn, wp, c.dim, n, PLANES, ldw, wpl, kTileK));
+            CUtensorMap p_k, sums;
+            BL_MAP(map_panels(&p_k, pp, q.tiled, q.tiled, PLANES * p_panels, kTileM));
             BL_MAP(map_f32(&sums, c.ws + q.dh, c.dim, c.rows, q.splits, q.ldo, c.rows * q.ldo));
             GemmArgs d = base;
             d.m = rows;
@@ -493,16 +499,20 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             d.splits = static_cast<int>(cdiv(d.kblocks, d.kb_per_split));
             d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
             d.accumulate = i > 0;
+            d.ca = cols_p;
+            d.cb = cols_w;
             BL_TRY((launch_gemm<DH, PLANES>(p_k, w_mn, sums, d, q.ctas, flag_count, c.sms, c.s)));
         }
         if (c.dW) {
             CUtensorMap p_mn, h_mn, to;
-            BL_MAP(map_bf16(&p_mn, pp, n, q.tiled, PLANES, q.piece, p_plane, kTileK));
-            BL_MAP(map_bf16(&h_mn, hp, c.dim, h_rows, PLANES, ldh, h_plane, kTileK));
+            BL_MAP(map_panels(&p_mn, pp, q.tiled, q.tiled, PLANES * p_panels, kTileK));
+            BL_MAP(map_panels(&h_mn, c.ws + q.h, q.tiled, q.tiled, PLANES * q.panels, kTileK));      // the gradient always copies H
             GemmArgs d = base;
             d.m = static_cast<int>(n);
             d.n = dim;
             d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
+            d.ca = cols_p;
+            d.cb = in_panels;
             char *const out = static_cast<char *>(c.dW) + v0 * c.lddw * static_cast<int64_t>(sizeof(T));
             if (!for_tma(c.dW, c.lddw, sizeof(T))) {
                 d.out = out;

@@ -21,6 +21,9 @@
 // product of f32 operands) the chain is cut into chunks of K, whose sums are added in registers.
 // Measured at rows 1024, dim 1024, vocabulary 32000, f32: dH 9.6e-6 off without chunks.
 //
+// P and the copies of H and W are stored in panels of 64 columns ([plane][panel][row][64]), so that
+// every operand tile is one contiguous piece of memory in either direction of use.
+//
 // Every wait is bounded: a role that gives up marks its CTA's flag, waits (bounded) for its own
 // copies and products in flight, and leaves; the others then run out of time too.
 #pragma once
@@ -57,7 +60,14 @@ constexpr uint32_t kPolls = 1u << 22;
 constexpr int kGroupM = 16;                                     // row tiles that share a column of B tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Where an operand's tile of 64 columns starts in its tensor map: x = column group * x, z = column
+// group * z + plane * plane. Rows as they are stored: (64, 0, 1); panels: (0, 1, panels).
+struct Columns {
+    int x, z, plane;
+};
+
 struct GemmArgs {
+    Columns ca, cb;
     int m, n;                  // rows and columns of the product (m: at most, see `kept`)
     int rows;                  // rows of H
     const int *kept;           // how many of them count; null: all. LOGITS, PROBS, DH: m; DW: K
@@ -77,6 +87,7 @@ struct GemmArgs {
     int64_t part_ld;
     float *picked;             // LOGITS: the target's logit of each row
     const float *lse, *g;      // PROBS
+    int p_panels;              // of a plane of P
     void *out;                 // DW: the result, where its rows do not start on 16-byte boundaries
     int64_t ldo;
 };
@@ -123,12 +134,13 @@ __device__ __forceinline__ Work work_of(int w, const GemmArgs &a, const Shape &s
     r.kb1 = min(s.kblocks, r.kb0 + a.kb_per_split);
     return r;
 }
-// Columns of the tile that the product has, rounded up to the instruction's granularity (16, or 32
-// for a pair, whose CTAs hold half of them each).
-template <int CTAS>
+// Columns of the tile that the product has, rounded up to what one CTA can hold of them: 16, the
+// instruction's granularity (a pair: 32), or for a pair's halves of an MN-major B whole groups of 64.
+template <bool B_MN, int CTAS>
 __device__ __forceinline__ int cols_of(int tn, const GemmArgs &a) {
+    constexpr int UNIT = CTAS == 1 ? 16 : B_MN ? 128 : 32;
     const int left = a.n - tn * kTileN;
-    return left >= kTileN ? kTileN : (left + 16 * CTAS - 1) & ~(16 * CTAS - 1);
+    return left >= kTileN ? kTileN : (left + UNIT - 1) & ~(UNIT - 1);
 }
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
@@ -271,10 +283,10 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
             // bits anyway
             float e = PLANES == 1 ? exp2f(fmaf(v[i], kLog2e, -r.ref)) : expf(v[i] - r.lse);
             if (i == r.at - c0) e -= 1.f;
-            v[i] = r.counted ? r.g * e : 0.f;
+            v[i] = r.counted && n0 + c0 + i < a.n ? r.g * e : 0.f;      // panels are whole: zero to their end
         }
     }
-    const bool there = MODE == PROBS || row0 < r.m;      // P has whole row tiles; rows that do not count are zero
+    const bool there = row0 < r.m;      // P has whole row tiles as well: rows that do not count are zero
     if constexpr (MODE == DH || PLANES == 3) {
         if constexpr (MODE == PROBS) {
             // three planes of 32 values: 64 bytes a line each
@@ -292,7 +304,7 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
                     *reinterpret_cast<uint4 *>(stage + (threadIdx.x & 31) * 64 + ((j ^ ((threadIdx.x >> 1) & 3)) << 4)) =
                         make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
                 }
-                lines_store(map, stage, n0 + c0, row0, pl, false);
+                lines_store(map, stage, c0 & 32, row0, pl * a.p_panels + (n0 + c0) / 64, false);
             }
         } else {
             lines_free();
@@ -308,6 +320,7 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
         put_bf16(stage, c0, v);
         if ((c0 & 32) || c0 + 32 >= cols) {
             if (MODE == DW && a.out) lines_copy<__nv_bfloat16>(a, stage, row0, n0 + (c0 & ~63));
+            else if (MODE == PROBS) lines_store(map, stage, 0, row0, (n0 + c0) / 64, false);
             else if (there) lines_store(map, stage, n0 + (c0 & ~63), row0, 0, false);
         }
     }
@@ -373,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
                 const Work k = work_of(w, a, sh);
-                const int part = cols_of<CTAS>(k.tn, a) / CTAS;       // this CTA's columns of B
+                const int part = cols_of<B_MN, CTAS>(k.tn, a) / CTAS;       // this CTA's columns of B
                 const int m0 = (k.tm * CTAS + rank) * kTileM, n0 = k.tn * kTileN + rank * part;
                 const int groups_b = (part + 63) >> 6;
                 const uint32_t bytes = CTAS * (kBytesA + (B_MN ? groups_b * (kTileK * 128) : kBytesB));
@@ -390,18 +403,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (rank == 0) tc::mbar_expect_tx(&full[s], bytes);      // of both CTAs
                         const uint32_t bar = CTAS == 1 ? tc::smem_u32(&full[s]) : tc::at_leader(&full[s]);
                         unsigned char *const da = tiles_a + s * kBytesA, *const db = tiles_b + s * kBytesB;
+                        const int za = pa * a.ca.plane, zb = pb * a.cb.plane;
                         if constexpr (A_MN) {
-                            for (int j = 0; j < kTileM / 64; ++j)
-                                tc::tma_load_3d<CTAS>(da + j * kTileK * 128, &map_a, bar, m0 + 64 * j, kb * kTileK, pa);
+                            for (int j = 0; j < kTileM / 64; ++j) {
+                                const int g = m0 / 64 + j;
+                                tc::tma_load_3d<CTAS>(da + j * kTileK * 128, &map_a, bar, g * a.ca.x, kb * kTileK, za + g * a.ca.z);
+                            }
                         } else {
-                            tc::tma_load_3d<CTAS>(da, &map_a, bar, kb * kTileK, m0, pa);
+                            tc::tma_load_3d<CTAS>(da, &map_a, bar, kb * a.ca.x, m0, za + kb * a.ca.z);
                         }
                         if constexpr (B_MN) {
 #pragma unroll 1
-                            for (int j = 0; j < groups_b; ++j)
-                                tc::tma_load_3d<CTAS>(db + j * kTileK * 128, &map_b, bar, n0 + 64 * j, kb * kTileK, pb);
+                            for (int j = 0; j < groups_b; ++j) {
+                                const int g = n0 / 64 + j;
+                                tc::tma_load_3d<CTAS>(db + j * kTileK * 128, &map_b, bar, g * a.cb.x, kb * kTileK, zb + g * a.cb.z);
+                            }
                         } else {
-                            tc::tma_load_3d<CTAS>(db, &map_b, bar, kb * kTileK, n0, pb);
+                            tc::tma_load_3d<CTAS>(db, &map_b, bar, kb * a.cb.x, n0, zb + kb * a.cb.z);
                         }
                     }
                 }
@@ -419,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
                 const Work k = work_of(w, a, sh);
-                const uint32_t idesc = tc::idesc_bf16(CTAS * kTileM, cols_of<CTAS>(k.tn, a), A_MN, B_MN);
+                const uint32_t idesc = tc::idesc_bf16(CTAS * kTileM, cols_of<B_MN, CTAS>(k.tn, a), A_MN, B_MN);
                 for (int c = k.kb0; ok && c < k.kb1; c += a.chunk, ++done) {
                     const uint32_t acc = tmem + (done & 1) * kTileN;
                     if (!tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls)) {
@@ -463,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
             const Work k = work_of(w, a, sh);
-            const int cols = min(a.n - k.tn * kTileN, (half + 1) * kHalf);     // this warp's columns end there
+            int cols = a.n - k.tn * kTileN;                                    // this warp's columns end there
+            if (MODE == PROBS) cols = (cols + 63) & ~63;
+            cols = min(cols, (half + 1) * kHalf);
             Row r;
             begin<MODE>(r, a, sh, k, (k.tm * CTAS + rank) * kTileM + quad * 32 + lane);
             float v[SUMS ? kHalf / 32 : 1][32];
