@@ -7,7 +7,7 @@
 //
 // A CTA computes 128 x 256 tiles, or a pair of CTAs 256 x 256 tiles (CTAS = 2: each holds its 128
 // rows of A and of the result and half of B, so B crosses shared memory once for 256 rows). One
-// thread streams 64-deep operand tiles into a ring of shared memory by TMA, one thread (of the
+// thread per operand streams 64-deep tiles into a ring of shared memory by TMA, one thread (of the
 // pair's leader) issues tcgen05.mma (bf16 operands, f32 accumulators in tensor
 // memory), and eight warps turn finished accumulators into the mode's output while the next tile's
 // products already run: tensor memory holds two accumulators of 256 columns.
@@ -51,7 +51,7 @@ struct Ring {
     static constexpr int kStages = CTAS == 1 ? 4 : 6;           // 192 KB
     static constexpr int kSmem = kStages * (kBytesA + kBytesB) + kEpilogueWarps * kStageBytes + 1024;
 };
-constexpr int kThreads = 128 + 32 * kEpilogueWarps;             // producer, issuer (and two idle warps), epilogue
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;             // producers, issuer (and an idle warp), epilogue
 // 384 threads start with 168 registers each; the first four warps give most of theirs to the
 // epilogue, whose rows hold 128 sums: 128 * 56 + 256 * 224 = 384 * 168.
 constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
@@ -379,10 +379,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
       tc::regs_dec<kRegsFew>();
-      if (warp == 0) {
+      if (warp == 0 || warp == 2) {
+        // Two producers, one for each operand: a thread needs 100 to 200 cycles to issue a copy, and
+        // a stage's products take 512. The leader's first announces the bytes of both CTAs.
         if (lane == 0) {
             const Shape sh = shape_of<MODE, CTAS>(a);
-            uint32_t it = 0;
+            const bool for_a = warp == 0, announce = for_a && rank == 0;
+            const uint32_t bar0 = CTAS == 1 ? tc::smem_u32(full) : tc::at_leader(full);
+            uint32_t s = 0, phase = 0, issued = 0;
             bool ok = true;
             for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
                 const Work k = work_of(w, a, sh);
@@ -394,46 +398,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int pr = 0; ok && pr < a.pairs; ++pr) {
                     int pa, pb;
                     pair_of(pr, a.pairs, pa, pb);
-                    for (int kb = c; kb < min(c + a.chunk, k.kb1); ++kb, ++it) {
-                        const uint32_t s = it % kStages;
-                        if (!tc::mbar_wait(&empty[s], (it / kStages & 1) ^ 1, kPolls)) {
+                    const int za = pa * a.ca.plane, zb = pb * a.cb.plane, end = min(c + a.chunk, k.kb1);
+                    for (int kb = c; kb < end; ++kb) {
+                        if (!tc::mbar_wait(&empty[s], phase ^ 1, kPolls)) {
                             ok = false;
                             break;
                         }
-                        if (rank == 0) tc::mbar_expect_tx(&full[s], bytes);      // of both CTAs
-                        const uint32_t bar = CTAS == 1 ? tc::smem_u32(&full[s]) : tc::at_leader(&full[s]);
-                        unsigned char *const da = tiles_a + s * kBytesA, *const db = tiles_b + s * kBytesB;
-                        const int za = pa * a.ca.plane, zb = pb * a.cb.plane;
-                        if constexpr (A_MN) {
-                            for (int j = 0; j < kTileM / 64; ++j) {
-                                const int g = m0 / 64 + j;
-                                tc::tma_load_3d<CTAS>(da + j * kTileK * 128, &map_a, bar, g * a.ca.x, kb * kTileK, za + g * a.ca.z);
+                        if (announce) tc::mbar_expect_tx(&full[s], bytes);
+                        const uint32_t bar = bar0 + 8 * s;
+                        if (for_a) {
+                            unsigned char *const d = tiles_a + s * kBytesA;
+                            if constexpr (A_MN) {
+#pragma unroll
+                                for (int j = 0; j < kTileM / 64; ++j) {
+                                    const int g = m0 / 64 + j;
+                                    tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_a, bar, g * a.ca.x, kb * kTileK, za + g * a.ca.z);
+                                }
+                            } else {
+                                tc::tma_load_3d<CTAS>(d, &map_a, bar, kb * a.ca.x, m0, za + kb * a.ca.z);
                             }
                         } else {
-                            tc::tma_load_3d<CTAS>(da, &map_a, bar, kb * a.ca.x, m0, za + kb * a.ca.z);
-                        }
-                        if constexpr (B_MN) {
+                            unsigned char *const d = tiles_b + s * kBytesB;
+                            if constexpr (B_MN) {
 #pragma unroll 1
-                            for (int j = 0; j < groups_b; ++j) {
-                                const int g = n0 / 64 + j;
-                                tc::tma_load_3d<CTAS>(db + j * kTileK * 128, &map_b, bar, g * a.cb.x, kb * kTileK, zb + g * a.cb.z);
+                                for (int j = 0; j < groups_b; ++j) {
+                                    const int g = n0 / 64 + j;
+                                    tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_b, bar, g * a.cb.x, kb * kTileK, zb + g * a.cb.z);
+                                }
+                            } else {
+                                tc::tma_load_3d<CTAS>(d, &map_b, bar, kb * a.cb.x, n0, zb + kb * a.cb.z);
                             }
-                        } else {
-                            tc::tma_load_3d<CTAS>(db, &map_b, bar, kb * a.cb.x, n0, zb + kb * a.cb.z);
                         }
+                        issued = min(issued + 1, static_cast<uint32_t>(kStages));
+                        if (++s == kStages) s = 0, phase ^= 1;
                     }
                 }
             }
             if (!ok) {
                 gave_up = 1;
-                for (uint32_t i = rank != 0 ? it : it > kStages ? it - kStages : 0; i < it; ++i)
-                    tc::mbar_wait(&full[i % kStages], i / kStages & 1, kPolls);
+                // the copies in flight: the last `issued` stages before s, oldest first
+                for (uint32_t i = 0; rank == 0 && i < issued; ++i) {
+                    const uint32_t t = s + kStages - issued + i;
+                    tc::mbar_wait(&full[t % kStages], t >= kStages ? phase : phase ^ 1, kPolls);
+                }
             }
         }
       } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             const Shape sh = shape_of<MODE, CTAS>(a);
-            uint32_t it = 0, done = 0;
+            const uint64_t da0 = A_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_a), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_a));
+            const uint64_t db0 = B_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_b), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_b));
+            uint32_t s = 0, phase = 0, done = 0;
             bool ok = true;
             for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
                 const Work k = work_of(w, a, sh);
@@ -446,21 +461,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc::fence_after_sync();
                     const int steps = (min(c + a.chunk, k.kb1) - c) * a.pairs;
-                    for (int i = 0; i < steps; ++i, ++it) {
-                        const uint32_t s = it % kStages;
-                        if (!tc::mbar_wait(&full[s], it / kStages & 1, kPolls)) {
+                    for (int i = 0; i < steps; ++i) {
+                        if (!tc::mbar_wait(&full[s], phase, kPolls)) {
                             ok = false;
                             break;
                         }
                         tc::fence_after_sync();
-                        const uint32_t sa = tc::smem_u32(tiles_a + s * kBytesA), sb = tc::smem_u32(tiles_b + s * kBytesB);
-                        const uint64_t da = A_MN ? tc::sdesc_mn_sw128(sa, kTileK * 128) : tc::sdesc_sw128(sa);
-                        const uint64_t db = B_MN ? tc::sdesc_mn_sw128(sb, kTileK * 128) : tc::sdesc_sw128(sb);
+                        const uint64_t da = da0 + s * (kBytesA >> 4), db = db0 + s * (kBytesB >> 4);
 #pragma unroll
                         for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
                             tc::mma_f16<CTAS>(acc, da + j * (A_MN ? 2048 / 16 : 2), db + j * (B_MN ? 2048 / 16 : 2), idesc,
-                                        i > 0 || j > 0);
+                                              i > 0 || j > 0);
                         tc::mma_commit_all<CTAS>(&empty[s]);
+                        if (++s == kStages) s = 0, phase ^= 1;
                     }
                     if (ok) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
                 }
