@@ -70,33 +70,48 @@ __global__ void __launch_bounds__(1024)
 // Copy rows into bf16 planes of 64-column panels ([plane][panel][height][64]); columns past dim are
 // zero. With `order` row j of the copy is row order[j]; whole row tiles are filled, with zeros after
 // the last row. Rows without a target (`target` given) become zero too.
+struct Copy {
+    const void *src;
+    int64_t ld, rows;
+    int dim;
+    const int64_t *target;
+    int64_t vocab;
+    const int *order, *kept;
+    int tile;
+    __nv_bfloat16 *dst;
+    int panels;
+    int64_t height;
+    int vec, blocks;
+};
+// Two copies in one launch, H's and the first piece's of W (either may be without blocks).
 template <typename T, int PLANES>
-__global__ void __launch_bounds__(256)
-    pack_kernel(const T *src, int64_t ld, int64_t rows, int dim, const int64_t *target, int64_t vocab, const int *order,
-                const int *kept, int tile, __nv_bfloat16 *dst, int panels, int64_t height, int vec) {
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ Copy one, const __grid_constant__ Copy two) {
     pdl_release();
     pdl_wait();
-    const int64_t count = kept ? *kept : rows, filled = max((count + tile - 1) / tile, int64_t(1)) * tile;
-    const int64_t per_row = panels * 8, all = filled * per_row, plane = panels * height * 64;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
+    const bool second = static_cast<int>(blockIdx.x) >= one.blocks;
+    const int block = second ? blockIdx.x - one.blocks : blockIdx.x;
+    const Copy &w = second ? two : one;
+    const int64_t count = w.kept ? *w.kept : w.rows, filled = max((count + w.tile - 1) / w.tile, int64_t(1)) * w.tile;
+    const int64_t per_row = w.panels * 8, all = filled * per_row, plane = w.panels * w.height * 64;
+    for (int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x; i < all;
+         i += static_cast<int64_t>(w.blocks) * 256) {
         const int64_t j = i / per_row;
         const int c = static_cast<int>(i - j * per_row) * 8;
-        const int64_t row = j >= count ? -1 : order ? order[j] : j;
-        const T *const s = src + row * ld + c;
+        const int64_t row = j >= count ? -1 : w.order ? w.order[j] : j;
+        const T *const s = static_cast<const T *>(w.src) + row * w.ld + c;
         __align__(16) T x[8];
-        if (row < 0 || (target && !has_target(target, row, vocab))) {
+        if (row < 0 || (w.target && !has_target(w.target, row, w.vocab))) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = T(0.f);
-        } else if (vec && c + 8 <= dim) {
+        } else if (w.vec && c + 8 <= w.dim) {
 #pragma unroll
             for (int e = 0; e < static_cast<int>(sizeof(x) / 16); ++e)
                 reinterpret_cast<uint4 *>(x)[e] = reinterpret_cast<const uint4 *>(s)[e];
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = c + e < dim ? s[e] : T(0.f);
+            for (int e = 0; e < 8; ++e) x[e] = c + e < w.dim ? s[e] : T(0.f);
         }
-        __nv_bfloat16 *const d = dst + ((c >> 6) * height + j) * 64 + (c & 63);
+        __nv_bfloat16 *const d = w.dst + ((c >> 6) * w.height + j) * 64 + (c & 63);
         if constexpr (PLANES == 1) {
             *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(x);
         } else {
@@ -111,41 +126,52 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Whether any CTA of the call's products gave up (all threads of the block ask).
-__device__ __forceinline__ bool any_gave_up(const int32_t *flags, int count) {
+// Whether any CTA of the call's products gave up: this thread's share of the flags.
+__device__ __forceinline__ int flags_seen(const int32_t *flags, int count) {
     int bad = 0;
     for (int i = threadIdx.x; i < count; i += blockDim.x) bad |= flags[i];
-    return __syncthreads_or(bad) != 0;
+    return bad;
 }
 
 // One warp a row: join the tiles' maxima and sums. A product that gave up makes every loss NaN.
+// Latency is all there is to it for few rows, so every load that can be is issued at once.
 __global__ void __launch_bounds__(256)
     loss_kernel(const float2 *part, int64_t part_ld, const float *picked, const int64_t *target, int64_t vocab, int rows,
                 const int *order, const int *kept, const int32_t *flags, int flag_count, float *loss, float *lse) {
+    constexpr int HELD = 8;
     pdl_release();
     pdl_wait();
-    const bool bad = any_gave_up(flags, flag_count);
     const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (j >= (kept ? *kept : rows)) return;
-    const int row = order ? order[j] : j;
-    float l = 0.f, v = 0.f;
+    const bool in = j < rows;                       // rows past the last that counts hold anything and are dropped below
+    const float2 *const p = part + (in ? j : 0) * part_ld;
+    float2 v[HELD];
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) v[h] = lane + 32 * h < part_ld ? p[lane + 32 * h] : make_float2(-INFINITY, 0.f);
+    const float chosen = in ? picked[j] : 0.f;
+    const int count = kept ? *kept : rows, row = in ? (order ? order[j] : j) : 0;
+    const bool bad = __syncthreads_or(flags_seen(flags, flag_count)) != 0;
+    if (j >= count) return;
+    float l = 0.f, s = 0.f;
     if (has_target(target, row, vocab)) {
-        const float2 *const p = part + j * part_ld;
         float top = -INFINITY, sum = 0.f;
-        for (int64_t i = lane; i < part_ld; i += 32) top = fmaxf(top, p[i].x);
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) top = fmaxf(top, v[h].x);
+        for (int64_t i = lane + 32 * HELD; i < part_ld; i += 32) top = fmaxf(top, p[i].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float ref = top == -INFINITY ? 0.f : top;
-        for (int64_t i = lane; i < part_ld; i += 32) sum += p[i].y * expf(p[i].x - ref);
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) sum += v[h].y * expf(v[h].x - ref);
+        for (int64_t i = lane + 32 * HELD; i < part_ld; i += 32) sum += p[i].y * expf(p[i].x - ref);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        v = ref + logf(sum);
-        l = v - picked[j];
+        s = ref + logf(sum);
+        l = s - chosen;
     }
-    if (bad) l = v = NAN;
+    if (bad) l = s = NAN;
     if (lane == 0) {
         loss[row] = l;
-        lse[row] = v;
+        lse[row] = s;
     }
 }
 
@@ -155,30 +181,42 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
 }
 
 // dH from the parts' sums, four columns a thread; rows without a target are zero. A product that
-// gave up makes it NaN.
-template <typename T>
+// gave up makes it NaN. With SHARE = 8 eight lanes of a warp add every eighth part each (many parts
+// mean few results: 64 rows x 1024 in 38 parts took 14 us with one thread a result).
+template <typename T, int SHARE>
 __global__ void __launch_bounds__(256)
     dh_kernel(const float *part, int splits, int64_t rows, int64_t ldo, const int64_t *target, int64_t vocab,
               const int *place, int dim, const int32_t *flags, int flag_count, T *dh, int64_t ld, int vec) {
+    constexpr int SIDE = 32 / SHARE;                // results that a warp works on at once
     pdl_release();
     pdl_wait();
-    const bool bad = any_gave_up(flags, flag_count);
-    const int64_t per_row = (dim + 3) / 4, all = rows * per_row;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / per_row;
-        const int c = static_cast<int>(i - row * per_row) * 4;
-        const int64_t j = place ? place[row] : has_target(target, row, vocab) ? row : -1;
+    const bool bad = __syncthreads_or(flags_seen(flags, flag_count)) != 0;
+    const int lane = threadIdx.x & 31, mine = SHARE == 1 ? 0 : lane / SIDE;
+    const int64_t per_row = (dim + 3) / 4, all = rows * per_row, step = static_cast<int64_t>(gridDim.x) * 256 / SHARE;
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & ~31)) / SHARE;
+    for (int64_t i0 = first; i0 < all; i0 += step) {        // the warp's first result: all lanes stay together
+        const int64_t i = i0 + lane % SIDE;
+        const int64_t row = i < all ? i / per_row : 0;
+        const int c = i < all ? static_cast<int>(i - row * per_row) * 4 : 0;
+        const int64_t j = i >= all ? -1 : place ? place[row] : has_target(target, row, vocab) ? row : -1;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (j >= 0) {
-            const float4 *p = reinterpret_cast<const float4 *>(part + j * ldo + c);
+            const float4 *p = reinterpret_cast<const float4 *>(part + (mine * rows + j) * ldo + c);
 #pragma unroll 4
-            for (int s = 0; s < splits; ++s, p += rows * ldo / 4) {
+            for (int s = mine; s < splits; s += SHARE, p += SHARE * rows * ldo / 4) {
                 const float4 x = *p;
                 v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
             }
         }
+#pragma unroll
+        for (int o = SIDE; o < 32; o <<= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+            v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+        }
         if (bad) v = make_float4(NAN, NAN, NAN, NAN);
+        if (i >= all || mine != 0) continue;
         T *const d = dh + row * ld + c;
         if (vec && c + 4 <= dim) {
             put4(d, v);
@@ -208,6 +246,7 @@ struct Plan {
     int64_t tiled;            // rows of the copy of H and of P: whole tiles
     int64_t panels;           // of 64 columns in the copies of H and W
     int64_t piece, pieces;    // vocabulary entries per piece
+    int tile_n;               // vocabulary entries per tile of logits
     int64_t part_ld;          // partial maxima and sums of a row: two per tile
     int splits;
     int64_t kb_per_split;     // 64-deep steps of one part of dH
@@ -258,7 +297,16 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     q.pieces = cdiv(vocab, most);
     q.piece = up(cdiv(vocab, q.pieces), kTileN);
     q.pieces = cdiv(vocab, q.piece);
-    q.part_ld = 2 * cdiv(vocab, kTileN);
+    // tiles of logits: the width that takes the least time in rounds of all SMs, when a tile takes as
+    // long as its width plus 64 columns (f32 loss, 77 rows, vocabulary 5003: 20 tiles of 256, 79 of 64)
+    q.tile_n = kTileN;
+    const int64_t groups = std::max(1, sms / q.ctas), tall = cdiv(rows, q.ctas * kTileM);
+    int64_t least = 0;
+    for (int t = kTileN; t >= 64; t /= 2) {
+        const int64_t cost = cdiv(tall * cdiv(std::min(q.piece, vocab), t), groups) * (t + 64);
+        if (t == kTileN || cost < least) q.tile_n = t, least = cost;
+    }
+    q.part_ld = 2 * cdiv(vocab, q.tile_n);
     q.ldo = up(dim, 32);
     // dH has few tiles and a long K axis, the piece
     const int64_t kb = cdiv(std::min(q.piece, vocab), kTileK);
@@ -378,15 +426,18 @@ cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUte
                      : launch_tiles<MODE, PLANES, 2>(ma, mb, mo, a, flags, sms, s);
 }
 
-template <typename T, int PLANES>
-cudaError_t launch_pack(const void *src, int64_t ld, int64_t rows, int64_t dim, const int64_t *target, int64_t vocab,
-                        const int *order, const int *kept, int tile, void *dst, int64_t height, int sms, cudaStream_t s) {
-    const int vec = for_tma(src, ld, sizeof(T));
-    const int64_t panels = cdiv(dim, 64);
-    const int64_t blocks = std::min<int64_t>(cdiv(up(rows, tile) * panels * 8, 256), static_cast<int64_t>(sms) * 8);
-    return launch_pdl(pack_kernel<T, PLANES>, static_cast<unsigned>(blocks), 256, 0, s, static_cast<const T *>(src), ld, rows,
-                      static_cast<int>(dim), target, vocab, order, kept, tile, static_cast<__nv_bfloat16 *>(dst),
-                      static_cast<int>(panels), height, vec);
+template <typename T>
+Copy copy_of(const void *src, int64_t ld, int64_t rows, int64_t dim, const int64_t *target, int64_t vocab, const int *order,
+             const int *kept, int tile, void *dst, int64_t height, int sms) {
+    Copy w{};
+    w.src = src, w.ld = ld, w.rows = rows, w.dim = static_cast<int>(dim);
+    w.target = target, w.vocab = vocab, w.order = order, w.kept = kept, w.tile = tile;
+    w.dst = static_cast<__nv_bfloat16 *>(dst);
+    w.panels = static_cast<int>(cdiv(dim, 64));
+    w.height = height;
+    w.vec = for_tma(src, ld, sizeof(T));
+    w.blocks = static_cast<int>(std::min<int64_t>(cdiv(up(rows, tile) * w.panels * 8, 256), static_cast<int64_t>(sms) * 8));
+    return w;
 }
 
 struct Call {
@@ -430,9 +481,9 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept, c.loss, c.lse));
     const Columns in_place{64, 0, 1}, in_panels{0, 1, static_cast<int>(q.panels)};
     CUtensorMap h_k;
+    Copy copy_h{};
     if (q.copy_h) {
-        BL_TRY((launch_pack<T, PLANES>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, order, kept, q.ctas * kTileM, c.ws + q.h, q.tiled,
-                                       c.sms, c.s)));
+        copy_h = copy_of<T>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, order, kept, q.ctas * kTileM, c.ws + q.h, q.tiled, c.sms);
         BL_MAP(map_panels(&h_k, c.ws + q.h, q.tiled, q.tiled, PLANES * q.panels, kTileM));
     } else {
         BL_MAP(map_bf16(&h_k, c.H, c.dim, c.rows, 1, c.ldh, c.ldh, kTileM));
@@ -452,12 +503,17 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         const int64_t v0 = i * q.piece, n = std::min(q.piece, c.vocab - v0);
         const char *const w_at = static_cast<const char *>(c.W) + v0 * c.ldw * static_cast<int64_t>(sizeof(T));
         CUtensorMap w_k, w_mn;
+        Copy copy_w{};
+        if (q.copy_w)
+            copy_w = copy_of<T>(w_at, c.ldw, n, c.dim, nullptr, 0, nullptr, nullptr, 1, c.ws + q.w, piece_w, c.sms);
+        if (i > 0) copy_h.blocks = 0;
+        if (copy_h.blocks + copy_w.blocks > 0)
+            BL_TRY(launch_pdl(pack_kernel<T, PLANES>, copy_h.blocks + copy_w.blocks, 256, 0, c.s, copy_h, copy_w));
         if (q.copy_w) {
-            BL_TRY((launch_pack<T, PLANES>(w_at, c.ldw, n, c.dim, nullptr, 0, nullptr, nullptr, 1, c.ws + q.w, piece_w, c.sms, c.s)));
-            BL_MAP(map_panels(&w_k, c.ws + q.w, n, piece_w, PLANES * q.panels, kTileN / q.ctas));
+            BL_MAP(map_panels(&w_k, c.ws + q.w, n, piece_w, PLANES * q.panels, q.tile_n / q.ctas));
             BL_MAP(map_panels(&w_mn, c.ws + q.w, n, piece_w, PLANES * q.panels, kTileK));
         } else {
-            BL_MAP(map_bf16(&w_k, w_at, c.dim, n, 1, c.ldw, c.ldw, kTileN / q.ctas));
+            BL_MAP(map_bf16(&w_k, w_at, c.dim, n, 1, c.ldw, c.ldw, q.tile_n / q.ctas));
             BL_MAP(map_bf16(&w_mn, w_at, c.dim, n, 1, c.ldw, c.ldw, kTileK));
         }
         const Columns cols_h = q.copy_h ? in_panels : in_place, cols_w = q.copy_w ? in_panels : in_place;
@@ -465,13 +521,14 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         a.m = rows;
         a.n = static_cast<int>(n);
         a.kblocks = static_cast<int>(cdiv(c.dim, kTileK));
-        a.tiles_n = static_cast<int>(cdiv(n, kTileN));
+        a.tile_n = q.tile_n;
+        a.tiles_n = static_cast<int>(cdiv(n, q.tile_n));
         a.v0 = static_cast<int>(v0);
         a.ca = cols_h;
         a.cb = cols_w;
         if (!q.grad) {
             if (PLANES == 1) a.chunk = kChunkLoss;
-            a.part = reinterpret_cast<float2 *>(c.ws + q.part) + 2 * (v0 / kTileN);
+            a.part = reinterpret_cast<float2 *>(c.ws + q.part) + 2 * (v0 / q.tile_n);
             a.part_ld = q.part_ld;
             a.picked = reinterpret_cast<float *>(c.ws + q.picked);
             BL_TRY((launch_gemm<LOGITS, PLANES>(h_k, w_k, w_k, a, q.ctas, flag_count, c.sms, c.s)));
@@ -497,6 +554,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             // the last piece may be shorter: its parts shrink, and every part still has a step
             d.kb_per_split = static_cast<int>(i == 0 ? q.kb_per_split : cdiv(d.kblocks, q.splits));
             d.splits = static_cast<int>(cdiv(d.kblocks, d.kb_per_split));
+            d.tile_n = kTileN;
             d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
             d.accumulate = i > 0;
             d.ca = cols_p;
@@ -510,6 +568,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             GemmArgs d = base;
             d.m = static_cast<int>(n);
             d.n = dim;
+            d.tile_n = kTileN;
             d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
             d.ca = cols_p;
             d.cb = in_panels;
@@ -531,12 +590,13 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
                           reinterpret_cast<const float2 *>(c.ws + q.part), q.part_ld, reinterpret_cast<const float *>(c.ws + q.picked),
                           c.target, c.vocab, rows, order, kept, flags, flag_count, c.loss, c.lse));
     } else if (c.dH) {
-        const int64_t blocks = std::min<int64_t>(cdiv(c.rows * cdiv(c.dim, 4), 256), static_cast<int64_t>(c.sms) * 8);
+        const int share = q.splits >= 8 ? 8 : 1;
+        const int64_t blocks = std::min<int64_t>(cdiv(c.rows * cdiv(c.dim, 4) * share, 256), static_cast<int64_t>(c.sms) * 8);
         const int64_t es = sizeof(T);
         const int vec = reinterpret_cast<uintptr_t>(c.dH) % (4 * es) == 0 && c.lddh % 4 == 0;
-        BL_TRY(launch_pdl(dh_kernel<T>, static_cast<unsigned>(blocks), 256, 0, c.s, reinterpret_cast<const float *>(c.ws + q.dh),
-                          q.splits, c.rows, q.ldo, c.target, c.vocab, place, dim, flags, flag_count, static_cast<T *>(c.dH), c.lddh,
-                          vec));
+        BL_TRY(launch_pdl(share == 8 ? dh_kernel<T, 8> : dh_kernel<T, 1>, static_cast<unsigned>(blocks), 256, 0, c.s,
+                          reinterpret_cast<const float *>(c.ws + q.dh), q.splits, c.rows, q.ldo, c.target, c.vocab, place, dim, flags,
+                          flag_count, static_cast<T *>(c.dH), c.lddh, vec));
     }
     return BL_SUCCESS;
 }

@@ -74,7 +74,7 @@ struct GemmArgs {
     const int *order;          // the rows that count, in order; null: every row in its place
     int kblocks;               // 64-deep steps of one pair of planes (DW: follows from `kept`)
     int chunk;                 // of them, how many are added in tensor memory before registers take over
-    int tiles_n;
+    int tile_n, tiles_n;       // columns of a tile: 256, or 128 or 64 where tiles are few (LOGITS, PROBS)
     int splits, kb_per_split;  // DH: the K axis is cut and every part has its own partial sums
     int pairs;                 // pairs of planes multiplied, 1 or 6
     int accumulate;            // DH: add to the partial sums of earlier pieces
@@ -139,8 +139,8 @@ __device__ __forceinline__ Work work_of(int w, const GemmArgs &a, const Shape &s
 template <bool B_MN, int CTAS>
 __device__ __forceinline__ int cols_of(int tn, const GemmArgs &a) {
     constexpr int UNIT = CTAS == 1 ? 16 : B_MN ? 128 : 32;
-    const int left = a.n - tn * kTileN;
-    return left >= kTileN ? kTileN : (left + UNIT - 1) & ~(UNIT - 1);
+    const int left = min(a.n - tn * a.tile_n, a.tile_n);
+    return (left + UNIT - 1) & ~(UNIT - 1);
 }
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
@@ -176,11 +176,11 @@ __device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s,
     r.row = row;
     r.m = s.m;
     if constexpr (MODE == LOGITS || MODE == PROBS) {
-        const int n0 = w.tn * kTileN;
+        const int n0 = w.tn * a.tile_n;
         const int64_t src = row < s.m ? (a.order ? a.order[row] : row) : -1;
         const int64_t t = src >= 0 ? a.target[src] : -1, at = t - a.v0 - n0;
         r.counted = t >= 0 && t < a.vocab;
-        r.at = r.counted && at >= 0 && at < min(a.n - n0, kTileN) ? static_cast<int>(at) : -1;
+        r.at = r.counted && at >= 0 && at < min(a.n - n0, a.tile_n) ? static_cast<int>(at) : -1;
         r.top = -INFINITY;
         r.sum = r.picked = 0.f;
         if constexpr (MODE == PROBS) {
@@ -193,7 +193,7 @@ __device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s,
 
 // Columns c0 .. c0 + 31 of the tile; those past the product's edge hold anything.
 __device__ __forceinline__ void block_logits(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
-    const int left = a.n - w.tn * kTileN - c0;
+    const int left = a.n - w.tn * a.tile_n - c0;
     if (left < 32) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = i < left ? v[i] : -INFINITY;
@@ -275,7 +275,7 @@ __device__ __forceinline__ void lines_copy(const GemmArgs &a, const unsigned cha
 template <int MODE, int PLANES>
 __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const Work &w, int c0, int cols, float (&v)[32],
                                           const CUtensorMap *map, unsigned char *stage) {
-    const int n0 = w.tn * kTileN, row0 = r.row - (threadIdx.x & 31);
+    const int n0 = w.tn * a.tile_n, row0 = r.row - (threadIdx.x & 31);
     if constexpr (MODE == PROBS) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -391,9 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
                 const Work k = work_of(w, a, sh);
                 const int part = cols_of<B_MN, CTAS>(k.tn, a) / CTAS;       // this CTA's columns of B
-                const int m0 = (k.tm * CTAS + rank) * kTileM, n0 = k.tn * kTileN + rank * part;
+                const int m0 = (k.tm * CTAS + rank) * kTileM, n0 = k.tn * a.tile_n + rank * part;
                 const int groups_b = (part + 63) >> 6;
-                const uint32_t bytes = CTAS * (kBytesA + (B_MN ? groups_b * (kTileK * 128) : kBytesB));
+                const uint32_t bytes = CTAS * (kBytesA + (B_MN ? groups_b * (kTileK * 128) : a.tile_n / CTAS * 128));
                 for (int c = k.kb0; ok && c < k.kb1; c += a.chunk)
                 for (int pr = 0; ok && pr < a.pairs; ++pr) {
                     int pa, pb;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
             const Work k = work_of(w, a, sh);
-            int cols = a.n - k.tn * kTileN;                                    // this warp's columns end there
+            int cols = min(a.n - k.tn * a.tile_n, a.tile_n);                   // this warp's columns end there
             if (MODE == PROBS) cols = (cols + 63) & ~63;
             cols = min(cols, (half + 1) * kHalf);
             Row r;
