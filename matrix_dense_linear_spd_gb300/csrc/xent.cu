@@ -35,9 +35,10 @@ __device__ __forceinline__ bool has_target(const int64_t *target, int64_t row, i
 }
 
 // One block: the rows that count, in order; each row's place among them (-1: does not count); how
-// many they are. The rows that do not count get the results they have (loss, lse: or null).
+// many they are, and the parts of dH's K axis. The rows that do not count get the results they have (loss, lse: or null).
 __global__ void __launch_bounds__(1024)
-    index_kernel(const int64_t *target, int64_t vocab, int rows, int *order, int *place, int *kept, float *loss, float *lse) {
+    index_kernel(const int64_t *target, int64_t vocab, int rows, int *order, int *place, int *kept, Cut cut, float *loss,
+                 float *lse) {
     __shared__ int sums[2][32];
     pdl_release();
     pdl_wait();
@@ -64,7 +65,10 @@ __global__ void __launch_bounds__(1024)
             else if (loss) loss[row] = lse[row] = 0.f;
         }
     }
-    if (threadIdx.x == 0) *kept = before;
+    if (threadIdx.x == 0) {
+        kept[0] = before;
+        kept[1] = parts_for(cut, before);
+    }
 }
 
 // Copy rows into bf16 planes of 64-column panels ([plane][panel][height][64]); columns past dim are
@@ -185,12 +189,14 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
 // mean few results: 64 rows x 1024 in 38 parts took 14 us with one thread a result).
 template <typename T, int SHARE>
 __global__ void __launch_bounds__(256)
-    dh_kernel(const float *part, int splits, int64_t rows, int64_t ldo, const int64_t *target, int64_t vocab,
-              const int *place, int dim, const int32_t *flags, int flag_count, T *dh, int64_t ld, int vec) {
+    dh_kernel(const float *part, int all_parts, int64_t rows, int64_t ldo, int dim, const int64_t *target, int64_t vocab,
+              const int *place, const int *kept_rows, const int32_t *flags, int flag_count, T *dh, int64_t ld, int vec) {
     constexpr int SIDE = 32 / SHARE;                // results that a warp works on at once
     pdl_release();
     pdl_wait();
     const bool bad = __syncthreads_or(flags_seen(flags, flag_count)) != 0;
+    const int kept = kept_rows ? kept_rows[0] : static_cast<int>(rows), splits = kept_rows ? kept_rows[1] : all_parts;
+    const int64_t height = part_rows(kept), part_step = SHARE * height * (ldo / 4);
     const int lane = threadIdx.x & 31, mine = SHARE == 1 ? 0 : lane / SIDE;
     const int64_t per_row = (dim + 3) / 4, all = rows * per_row, step = static_cast<int64_t>(gridDim.x) * 256 / SHARE;
     const int64_t first = (static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & ~31)) / SHARE;
@@ -201,9 +207,9 @@ __global__ void __launch_bounds__(256)
         const int64_t j = i >= all ? -1 : place ? place[row] : has_target(target, row, vocab) ? row : -1;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (j >= 0) {
-            const float4 *p = reinterpret_cast<const float4 *>(part + (mine * rows + j) * ldo + c);
+            const float4 *p = reinterpret_cast<const float4 *>(part + (mine * height + j) * ldo + c);
 #pragma unroll 4
-            for (int s = mine; s < splits; s += SHARE, p += SHARE * rows * ldo / 4) {
+            for (int s = mine; s < splits; s += SHARE, p += part_step) {
                 const float4 x = *p;
                 v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
             }
@@ -241,35 +247,24 @@ int64_t cdiv(int64_t v, int64_t by) { return (v + by - 1) / by; }
 struct Plan {
     int planes, pairs;
     int ctas;                 // that share a tile
+    int groups;               // CTAs or pairs that the device's SMs hold
     bool copy_h, copy_w, compact, grad;
     int64_t rows, dim, vocab;
     int64_t tiled;            // rows of the copy of H and of P: whole tiles
+    int64_t seen;             // of them, those that tensor maps see: the rest reads as zero without being read
     int64_t panels;           // of 64 columns in the copies of H and W
     int64_t piece, pieces;    // vocabulary entries per piece
     int tile_n;               // vocabulary entries per tile of logits
     int64_t part_ld;          // partial maxima and sums of a row: two per tile
-    int splits;
-    int64_t kb_per_split;     // 64-deep steps of one part of dH
+    int parts;                // of dH's K axis if every row counts
+    int first_kb;             // 64-deep steps of the first piece
+    int64_t slab_rows;        // of dH's partial sums, all parts together
     int64_t ldo;              // row length of dH's partial sums
     int64_t flags, kept, order, place, h, w, part, picked, p, dh, bytes;   // offsets into the workspace
 };
 
 bool for_tma(const void *p, int64_t ld, int64_t elem) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * elem % 16 == 0;
-}
-
-// Parts of a K axis of kb steps, so that tiles * parts fill `sms` CTAs (or pairs) evenly: the number that
-// minimises the rounds times a part's steps, plus what a part's partial sums cost to write and
-// read again (in steps of 0.27 us, the time of 128 x 256 x 64 products on one SM).
-int64_t parts_of(int64_t tiles, int64_t kb, int64_t result_bytes, int sms) {
-    int64_t best = 1;
-    double least = 0;
-    for (int64_t s = 1; s <= std::max<int64_t>(1, std::min<int64_t>(kb / 4, std::max<int64_t>(8, 2 * sms / tiles))); ++s) {
-        const double t = static_cast<double>(cdiv(tiles * s, sms)) * (static_cast<double>(cdiv(kb, s)) + 4) +
-                         static_cast<double>(s) * result_bytes * 2 / 6.8e12 / 0.27e-6;
-        if (s == 1 || t < least) best = s, least = t;
-    }
-    return best;
 }
 
 Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw,
@@ -279,6 +274,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     q.pairs = dtype == BL_F32 ? 6 : 1;
     q.compact = rows > kTileM;
     q.ctas = rows > kTileM ? 2 : 1;
+    q.groups = std::max(1, sms / q.ctas);
     // a row without a target may hold anything: only the loss of uncopied rows ignores it
     q.copy_h = dtype == BL_F32 || grad || q.compact || !for_tma(H, ldh, 2);
     q.copy_w = dtype == BL_F32 || !for_tma(W, ldw, 2);
@@ -287,6 +283,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     q.dim = dim;
     q.vocab = vocab;
     q.tiled = up(rows, q.ctas * kTileM);
+    q.seen = q.compact ? q.tiled : rows;
     q.panels = cdiv(dim, 64);
     // a piece: what keeps P and the copy of W within their size, but 4096 entries at least, so
     // that a piece's products fill the GPU; pieces of one size
@@ -300,7 +297,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     // tiles of logits: the width that takes the least time in rounds of all SMs, when a tile takes as
     // long as its width plus 64 columns (f32 loss, 77 rows, vocabulary 5003: 20 tiles of 256, 79 of 64)
     q.tile_n = kTileN;
-    const int64_t groups = std::max(1, sms / q.ctas), tall = cdiv(rows, q.ctas * kTileM);
+    const int64_t groups = q.groups, tall = cdiv(rows, q.ctas * kTileM);
     int64_t least = 0;
     for (int t = kTileN; t >= 64; t /= 2) {
         const int64_t cost = cdiv(tall * cdiv(std::min(q.piece, vocab), t), groups) * (t + 64);
@@ -308,10 +305,14 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     }
     q.part_ld = 2 * cdiv(vocab, q.tile_n);
     q.ldo = up(dim, 32);
-    // dH has few tiles and a long K axis, the piece
-    const int64_t kb = cdiv(std::min(q.piece, vocab), kTileK);
-    q.kb_per_split = cdiv(kb, parts_of(cdiv(rows, q.ctas * kTileM) * cdiv(dim, kTileN), kb * q.pairs, rows * q.ldo * 4, sms / q.ctas));
-    q.splits = static_cast<int>(cdiv(kb, q.kb_per_split));
+    // dH's partial sums: room for as many parts as are wanted if every row counts, and up to six (256 MB)
+    // for the case that few do
+    q.first_kb = static_cast<int>(cdiv(std::min(q.piece, vocab), kTileK));
+    const int64_t high = part_rows(static_cast<int>(rows));
+    const Cut roomy{q.ctas, static_cast<int>(dim), q.first_kb, q.pairs, static_cast<int>(std::min<int64_t>(1 << 28, high * 1024)), q.groups};
+    q.parts = parts_for(roomy, static_cast<int>(rows));
+    const int64_t spare = q.compact ? std::min<int64_t>(6, (int64_t(256) << 20) / (high * q.ldo * 4)) : 1;
+    q.slab_rows = high * std::max<int64_t>(q.parts, spare);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t r = at;
@@ -319,7 +320,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
         return r;
     };
     q.flags = take(q.pieces * 3 * sms * 4);
-    q.kept = take(4);
+    q.kept = take(8);
     if (q.compact) {
         q.order = take(rows * 4);
         q.place = take(rows * 4);
@@ -331,7 +332,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
         q.picked = take(rows * 4);
     } else {
         q.p = take(q.planes * q.tiled * q.piece * 2);
-        q.dh = take(q.splits * rows * q.ldo * 4);
+        q.dh = take(q.slab_rows * q.ldo * 4);
     }
     q.bytes = at;
     return q;
@@ -413,8 +414,8 @@ cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUt
         }
         if (dev < 64) groups[dev].store(most, std::memory_order_release);
     }
-    const int64_t total = cdiv(a.m, CTAS * kTileM) * a.tiles_n * a.splits;
-    const int grid = static_cast<int>(std::min<int64_t>(total, most)) * CTAS;
+    const int64_t total = cdiv(a.m, CTAS * kTileM) * a.tiles_n;
+    const int grid = static_cast<int>(MODE == DH ? most : std::min<int64_t>(total, most)) * CTAS;    // DH is cut to fill the device
     a.flags += flags;
     flags += grid;
     return launch_pdl_cluster(kernel, grid, kThreads, kSmem, CTAS, s, ma, mb, mo, a);
@@ -478,13 +479,14 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     int32_t *const flags = reinterpret_cast<int32_t *>(c.ws + q.flags);
     int flag_count = 0;
     if (q.compact)
-        BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept, c.loss, c.lse));
+        BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept,
+                          Cut{q.ctas, dim, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.loss, c.lse));
     const Columns in_place{64, 0, 1}, in_panels{0, 1, static_cast<int>(q.panels)};
     CUtensorMap h_k;
     Copy copy_h{};
     if (q.copy_h) {
         copy_h = copy_of<T>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, order, kept, q.ctas * kTileM, c.ws + q.h, q.tiled, c.sms);
-        BL_MAP(map_panels(&h_k, c.ws + q.h, q.tiled, q.tiled, PLANES * q.panels, kTileM));
+        BL_MAP(map_panels(&h_k, c.ws + q.h, q.seen, q.tiled, PLANES * q.panels, kTileM));
     } else {
         BL_MAP(map_bf16(&h_k, c.H, c.dim, c.rows, 1, c.ldh, c.ldh, kTileM));
     }
@@ -495,8 +497,6 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     base.flags = flags;
     base.pairs = q.pairs;
     base.chunk = PLANES == 3 ? kChunkF32 : kWhole;
-    base.kb_per_split = kWhole;
-    base.splits = 1;
     base.target = c.target;
     base.vocab = c.vocab;
     for (int64_t i = 0; i < q.pieces; ++i) {
@@ -538,22 +538,20 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         const int64_t p_panels = cdiv(n, 64);
         const Columns cols_p{0, 1, static_cast<int>(p_panels)};
         CUtensorMap p_out;
-        BL_MAP(map_panels(&p_out, pp, q.tiled, q.tiled, PLANES * p_panels, 32, PLANES == 1 ? 128 : 64));
+        BL_MAP(map_panels(&p_out, pp, q.seen, q.tiled, PLANES * p_panels, 32, PLANES == 1 ? 128 : 64));
         a.p_panels = static_cast<int>(p_panels);
         a.lse = c.lse_in;
         a.g = c.g;
         BL_TRY((launch_gemm<PROBS, PLANES>(h_k, w_k, p_out, a, q.ctas, flag_count, c.sms, c.s)));
         if (c.dH) {
             CUtensorMap p_k, sums;
-            BL_MAP(map_panels(&p_k, pp, q.tiled, q.tiled, PLANES * p_panels, kTileM));
-            BL_MAP(map_f32(&sums, c.ws + q.dh, c.dim, c.rows, q.splits, q.ldo, c.rows * q.ldo));
+            BL_MAP(map_panels(&p_k, pp, q.seen, q.tiled, PLANES * p_panels, kTileM));
+            BL_MAP(map_f32(&sums, c.ws + q.dh, c.dim, q.slab_rows, 1, q.ldo, q.ldo));
             GemmArgs d = base;
             d.m = rows;
             d.n = dim;
             d.kblocks = static_cast<int>(cdiv(n, kTileK));
-            // the last piece may be shorter: its parts shrink, and every part still has a step
-            d.kb_per_split = static_cast<int>(i == 0 ? q.kb_per_split : cdiv(d.kblocks, q.splits));
-            d.splits = static_cast<int>(cdiv(d.kblocks, d.kb_per_split));
+            d.parts = q.parts;
             d.tile_n = kTileN;
             d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
             d.accumulate = i > 0;
@@ -563,8 +561,8 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         }
         if (c.dW) {
             CUtensorMap p_mn, h_mn, to;
-            BL_MAP(map_panels(&p_mn, pp, q.tiled, q.tiled, PLANES * p_panels, kTileK));
-            BL_MAP(map_panels(&h_mn, c.ws + q.h, q.tiled, q.tiled, PLANES * q.panels, kTileK));      // the gradient always copies H
+            BL_MAP(map_panels(&p_mn, pp, q.seen, q.tiled, PLANES * p_panels, kTileK));
+            BL_MAP(map_panels(&h_mn, c.ws + q.h, q.seen, q.tiled, PLANES * q.panels, kTileK));      // the gradient always copies H
             GemmArgs d = base;
             d.m = static_cast<int>(n);
             d.n = dim;
@@ -590,12 +588,12 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
                           reinterpret_cast<const float2 *>(c.ws + q.part), q.part_ld, reinterpret_cast<const float *>(c.ws + q.picked),
                           c.target, c.vocab, rows, order, kept, flags, flag_count, c.loss, c.lse));
     } else if (c.dH) {
-        const int share = q.splits >= 8 ? 8 : 1;
+        const int share = q.parts >= 8 ? 8 : 1;
         const int64_t blocks = std::min<int64_t>(cdiv(c.rows * cdiv(c.dim, 4) * share, 256), static_cast<int64_t>(c.sms) * 8);
         const int64_t es = sizeof(T);
         const int vec = reinterpret_cast<uintptr_t>(c.dH) % (4 * es) == 0 && c.lddh % 4 == 0;
         BL_TRY(launch_pdl(share == 8 ? dh_kernel<T, 8> : dh_kernel<T, 1>, static_cast<unsigned>(blocks), 256, 0, c.s,
-                          reinterpret_cast<const float *>(c.ws + q.dh), q.splits, c.rows, q.ldo, c.target, c.vocab, place, dim, flags,
+                          reinterpret_cast<const float *>(c.ws + q.dh), q.parts, c.rows, q.ldo, dim, c.target, c.vocab, place, kept, flags,
                           flag_count, static_cast<T *>(c.dH), c.lddh, vec));
     }
     return BL_SUCCESS;

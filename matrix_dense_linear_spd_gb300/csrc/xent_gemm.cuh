@@ -70,12 +70,12 @@ struct GemmArgs {
     Columns ca, cb;
     int m, n;                  // rows and columns of the product (m: at most, see `kept`)
     int rows;                  // rows of H
-    const int *kept;           // how many of them count; null: all. LOGITS, PROBS, DH: m; DW: K
+    const int *kept;           // how many of them count (LOGITS, PROBS, DH: m; DW: K), parts; null: all
     const int *order;          // the rows that count, in order; null: every row in its place
     int kblocks;               // 64-deep steps of one pair of planes (DW: follows from `kept`)
     int chunk;                 // of them, how many are added in tensor memory before registers take over
     int tile_n, tiles_n;       // columns of a tile: 256, or 128 or 64 where tiles are few (LOGITS, PROBS)
-    int splits, kb_per_split;  // DH: the K axis is cut and every part has its own partial sums
+    int parts;                 // DH: of the K axis, if every row counts (else kept[1])
     int pairs;                 // pairs of planes multiplied, 1 or 6
     int accumulate;            // DH: add to the partial sums of earlier pieces
     int32_t *flags;            // one word per CTA: not 0 if it gave up
@@ -101,11 +101,45 @@ __device__ __forceinline__ void pair_of(int i, int pairs, int &a, int &b) {
     b = (bs >> (4 * j)) & 15;
 }
 
+// DH has few tiles and a long K axis, so K is cut into parts that have partial sums of their own:
+// as many as make the least of the rounds that the device needs, times a part's steps (and 4 to
+// start), plus what writing and reading a part's sums costs; all in steps, the 0.27 us of a
+// 128 x 256 x 64 product on one SM. Only the numbers that fill whole rounds are looked at.
+// In 1024ths of a step.
+__host__ __device__ inline int parts_of(int tiles, int kblocks, int pairs, int64_t result_bytes, int groups, int most) {
+    int best = 1;
+    int64_t least = 0;
+    for (int rounds = 1; rounds <= 8; ++rounds) {
+        int s = rounds * groups / tiles;
+        s = s < 1 ? 1 : s > most ? most : s;
+        const int64_t need = (tiles * s + groups - 1) / groups, steps = (kblocks + s - 1) / s * pairs + 4;
+        const int64_t cost = need * steps * 1024 + s * (result_bytes >> 10);
+        if (rounds == 1 || cost < least) best = s, least = cost;
+    }
+    const int per = (kblocks + best - 1) / best;
+    return (kblocks + per - 1) / per;
+}
+
 // What depends on how many rows count. One row tile and one step of K remain where none does, so
 // that P and dW become zero.
 struct Shape {
-    int m, tiles_m, kblocks, total;
+    int m, tiles_m, kblocks, splits, kb_per_split, total;
 };
+// Rows of a part's partial sums: what the epilogue's warps, 32 rows each, store.
+__host__ __device__ inline int part_rows(int kept) { return kept < 32 ? 32 : (kept + 31) & ~31; }
+// How the first piece's K axis is cut into parts whose sums fit slab_rows; the others' likewise.
+struct Cut {
+    int ctas, dim, first_kb, pairs, slab_rows, groups;
+};
+__host__ __device__ inline int parts_for(const Cut &q, int kept) {
+    const int tile = q.ctas * kTileM, tall = kept < tile ? 1 : (kept + tile - 1) / tile;
+    int most = q.slab_rows / part_rows(kept);
+    const int longest = q.pairs > 1 ? q.first_kb : q.first_kb / 4;
+    if (most > longest) most = longest;
+    if (most < 1) most = 1;
+    return parts_of(tall * ((q.dim + kTileN - 1) / kTileN), q.first_kb, q.pairs, static_cast<int64_t>(part_rows(kept)) * q.dim * 4,
+                    q.groups, most);
+}
 template <int MODE, int CTAS>
 __device__ __forceinline__ Shape shape_of(const GemmArgs &a) {
     const int kept = a.kept ? *a.kept : a.rows;
@@ -113,7 +147,14 @@ __device__ __forceinline__ Shape shape_of(const GemmArgs &a) {
     s.m = MODE == DW ? a.m : kept;
     s.tiles_m = max(1, (s.m + CTAS * kTileM - 1) / (CTAS * kTileM));
     s.kblocks = MODE == DW ? max(1, (kept + kTileK - 1) / kTileK) : a.kblocks;
-    s.total = s.tiles_m * a.tiles_n * a.splits;
+    s.splits = 1;
+    s.kb_per_split = s.kblocks;
+    if constexpr (MODE == DH) {
+        const int parts = a.kept ? a.kept[1] : a.parts;     // the first piece's; a shorter one has no more
+        s.kb_per_split = (s.kblocks + parts - 1) / parts;
+        s.splits = (s.kblocks + s.kb_per_split - 1) / s.kb_per_split;
+    }
+    s.total = s.tiles_m * a.tiles_n * s.splits;
     return s;
 }
 
@@ -130,8 +171,8 @@ __device__ __forceinline__ Work work_of(int w, const GemmArgs &a, const Shape &s
     const int rest = s.tiles_m - g * kGroupM, gm = rest < kGroupM ? rest : kGroupM;
     r.tn = w / gm;
     r.tm = g * kGroupM + (w - r.tn * gm);
-    r.kb0 = r.split * a.kb_per_split;
-    r.kb1 = min(s.kblocks, r.kb0 + a.kb_per_split);
+    r.kb0 = r.split * s.kb_per_split;
+    r.kb1 = min(s.kblocks, r.kb0 + s.kb_per_split);
     return r;
 }
 // Columns of the tile that the product has, rounded up to what one CTA can hold of them: 16, the
@@ -166,6 +207,7 @@ __device__ __forceinline__ void split3(float x, float &x0, float &x1, float &x2)
 
 struct Row {              // what an epilogue keeps of its row
     int row, m, at;       // row of the product, its rows; the target's column within this tile or -1
+    int part_rows;        // DH
     bool counted;
     float top, sum, picked;    // LOGITS
     float lse, ref, g;         // PROBS
@@ -175,6 +217,7 @@ template <int MODE>
 __device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s, const Work &w, int row) {
     r.row = row;
     r.m = s.m;
+    if constexpr (MODE == DH) r.part_rows = part_rows(s.m);
     if constexpr (MODE == LOGITS || MODE == PROBS) {
         const int n0 = w.tn * a.tile_n;
         const int64_t src = row < s.m ? (a.order ? a.order[row] : row) : -1;
@@ -313,7 +356,7 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
                 line_put(stage, j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
                                               __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
             if (MODE == DW && a.out) lines_copy<float>(a, stage, row0, n0 + c0);
-            else if (there) lines_store(map, stage, n0 + c0, row0, MODE == DH ? w.split : 0, MODE == DH && a.accumulate);
+            else if (there) lines_store(map, stage, n0 + c0, row0 + (MODE == DH ? w.split * r.part_rows : 0), 0, MODE == DH && a.accumulate);
         }
     } else {
         if ((c0 & 32) == 0) lines_free();
