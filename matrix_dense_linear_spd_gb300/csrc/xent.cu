@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ plan
 
 // K is added in tensor memory over so many 64-deep steps at a time where the result is f32
-constexpr int kChunkF32 = 4, kChunkLoss = 16, kWhole = 1 << 30;
+constexpr int kChunkF32 = 2, kChunkLoss = 16, kWhole = 1 << 30;
 constexpr int64_t kPieceBytes = int64_t(512) << 20;     // of P, and of a piece's copy of W
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -254,7 +254,7 @@ struct Plan {
     int64_t seen;             // of them, those that tensor maps see: the rest reads as zero without being read
     int64_t panels;           // of 64 columns in the copies of H and W
     int64_t piece, pieces;    // vocabulary entries per piece
-    int tile_n;               // vocabulary entries per tile of logits
+    int wide, tile_n;         // columns of a tile, at most; of a tile of logits
     int64_t part_ld;          // partial maxima and sums of a row: two per tile
     int parts;                // of dH's K axis if every row counts
     int first_kb;             // 64-deep steps of the first piece
@@ -275,6 +275,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     q.compact = rows > kTileM;
     q.ctas = rows > kTileM ? 2 : 1;
     q.groups = std::max(1, sms / q.ctas);
+    q.wide = q.ctas == 1 && q.planes == 3 ? Ring<1, 3>::kTile : kTileN;
     // a row without a target may hold anything: only the loss of uncopied rows ignores it
     q.copy_h = dtype == BL_F32 || grad || q.compact || !for_tma(H, ldh, 2);
     q.copy_w = dtype == BL_F32 || !for_tma(W, ldw, 2);
@@ -296,12 +297,12 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     q.pieces = cdiv(vocab, q.piece);
     // tiles of logits: the width that takes the least time in rounds of all SMs, when a tile takes as
     // long as its width plus 64 columns (f32 loss, 77 rows, vocabulary 5003: 20 tiles of 256, 79 of 64)
-    q.tile_n = kTileN;
+    q.tile_n = q.wide;
     const int64_t groups = q.groups, tall = cdiv(rows, q.ctas * kTileM);
     int64_t least = 0;
-    for (int t = kTileN; t >= 64; t /= 2) {
+    for (int t = q.wide; t >= 64; t /= 2) {
         const int64_t cost = cdiv(tall * cdiv(std::min(q.piece, vocab), t), groups) * (t + 64);
-        if (t == kTileN || cost < least) q.tile_n = t, least = cost;
+        if (t == q.wide || cost < least) q.tile_n = t, least = cost;
     }
     q.part_ld = 2 * cdiv(vocab, q.tile_n);
     q.ldo = up(dim, 32);
@@ -309,7 +310,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     // for the case that few do
     q.first_kb = static_cast<int>(cdiv(std::min(q.piece, vocab), kTileK));
     const int64_t high = part_rows(static_cast<int>(rows));
-    const Cut roomy{q.ctas, static_cast<int>(dim), q.first_kb, q.pairs, static_cast<int>(std::min<int64_t>(1 << 28, high * 1024)), q.groups};
+    const Cut roomy{q.ctas, static_cast<int>(dim), q.wide, q.first_kb, q.pairs, static_cast<int>(std::min<int64_t>(1 << 28, high * 1024)), q.groups};
     q.parts = parts_for(roomy, static_cast<int>(rows));
     const int64_t spare = q.compact ? std::min<int64_t>(6, (int64_t(256) << 20) / (high * q.ldo * 4)) : 1;
     q.slab_rows = high * std::max<int64_t>(q.parts, spare);
@@ -386,7 +387,7 @@ bool map_f32(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, in
 template <int MODE, int PLANES, int CTAS>
 cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, GemmArgs &a, int &flags, int sms,
                          cudaStream_t s) {
-    constexpr int kSmem = Ring<CTAS>::kSmem;
+    constexpr int kSmem = Ring<CTAS, PLANES>::kSmem;
     const auto kernel = gemm_kernel<MODE, PLANES, CTAS>;
     static std::atomic<int> groups[64];         // CTAs, or pairs of CTAs, that the device runs at once
     int dev = 0;
@@ -480,7 +481,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     int flag_count = 0;
     if (q.compact)
         BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept,
-                          Cut{q.ctas, dim, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.loss, c.lse));
+                          Cut{q.ctas, dim, q.wide, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.loss, c.lse));
     const Columns in_place{64, 0, 1}, in_panels{0, 1, static_cast<int>(q.panels)};
     CUtensorMap h_k;
     Copy copy_h{};
@@ -495,7 +496,6 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     base.kept = kept;
     base.order = order;
     base.flags = flags;
-    base.pairs = q.pairs;
     base.chunk = PLANES == 3 ? kChunkF32 : kWhole;
     base.target = c.target;
     base.vocab = c.vocab;
@@ -552,8 +552,8 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             d.n = dim;
             d.kblocks = static_cast<int>(cdiv(n, kTileK));
             d.parts = q.parts;
-            d.tile_n = kTileN;
-            d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
+            d.tile_n = q.wide;
+            d.tiles_n = static_cast<int>(cdiv(c.dim, q.wide));
             d.accumulate = i > 0;
             d.ca = cols_p;
             d.cb = cols_w;
@@ -566,8 +566,8 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             GemmArgs d = base;
             d.m = static_cast<int>(n);
             d.n = dim;
-            d.tile_n = kTileN;
-            d.tiles_n = static_cast<int>(cdiv(c.dim, kTileN));
+            d.tile_n = q.wide;
+            d.tiles_n = static_cast<int>(cdiv(c.dim, q.wide));
             d.ca = cols_p;
             d.cb = in_panels;
             char *const out = static_cast<char *>(c.dW) + v0 * c.lddw * static_cast<int64_t>(sizeof(T));
