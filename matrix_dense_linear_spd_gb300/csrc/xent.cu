@@ -179,6 +179,129 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// The loss of a few rows (a token or a handful): too few for a tile, so each W row meets all of them
+// while it is in registers, in f32 multiply-adds. HBM bandwidth bounds it up to four rows (one row,
+// dim 4096, vocabulary 131072: bf16 153 us, 7.0 TB/s; f32 296 us, 7.2 TB/s), the multiply-adds and
+// shared-memory reads of H above. A warp takes four vocabulary entries
+// at a time, its lanes share K; H waits in shared memory as f32. Each CTA leaves one maximum and sum
+// a row. W is read in place whatever its type: no planes, no copies.
+template <typename T>
+struct FewVec;
+template <>
+struct FewVec<float> {
+    static constexpr int N = 4;
+    __device__ static void load(const float *p, float (&v)[4]) {
+        const float4 q = __ldcs(reinterpret_cast<const float4 *>(p));
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    }
+};
+template <>
+struct FewVec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    __device__ static void load(const __nv_bfloat16 *p, float (&v)[8]) {
+        const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {              // bf16 is the upper half of an f32
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+// Entries a warp takes at a time, 16-byte steps of K in flight for each, and CTAs per SM
+constexpr int few_entries(int R) { return R == 1 ? 2 : 4; }
+constexpr int few_ahead(int R) { return R == 1 ? 4 : 2; }
+constexpr int few_ctas(int R) { return R == 1 ? 4 : R == 4 ? 2 : 1; }
+
+template <typename T, int R>
+__global__ void __launch_bounds__(256, few_ctas(R))
+    few_kernel(const T *H, int64_t ldh, int rows, int dim, const T *W, int64_t ldw, int vocab, const int64_t *target,
+               float2 *part, int64_t part_ld, float *picked) {
+    constexpr int N = FewVec<T>::N, E = few_entries(R), AHEAD = few_ahead(R);
+    extern __shared__ __align__(16) float few_h[];           // [R][dim]
+    __shared__ float2 joined[8][R];
+    pdl_release();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < R * dim; i += 256) {
+        const int r = i / dim, k = i - r * dim;
+        few_h[i] = r < rows ? static_cast<float>(H[r * ldh + k]) : 0.f;
+    }
+    int64_t at[R];
+    float top[R], sum[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        at[r] = r < rows ? target[r] : -1;
+        top[r] = -INFINITY;
+        sum[r] = 0.f;
+    }
+    __syncthreads();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * E;
+    for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * E; v0 < vocab; v0 += step) {
+        float acc[E][R];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[e][r] = 0.f;
+        const T *w[E];                                       // past the last entry: the last one again, dropped below
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] = W + min(v0 + e, static_cast<int64_t>(vocab) - 1) * ldw;
+#pragma unroll AHEAD
+        for (int k = lane * N; k < dim; k += 32 * N) {
+            float x[E][N];
+#pragma unroll
+            for (int e = 0; e < E; ++e) FewVec<T>::load(w[e] + k, x[e]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 *const h = reinterpret_cast<const float4 *>(few_h + r * dim + k);
+#pragma unroll
+                for (int q = 0; q < N / 4; ++q) {
+                    const float4 y = h[q];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        acc[e][r] = fmaf(x[e][4 * q], y.x, acc[e][r]);
+                        acc[e][r] = fmaf(x[e][4 * q + 1], y.y, acc[e][r]);
+                        acc[e][r] = fmaf(x[e][4 * q + 2], y.z, acc[e][r]);
+                        acc[e][r] = fmaf(x[e][4 * q + 3], y.w, acc[e][r]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                float s = acc[e][r];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                acc[e][r] = v0 + e < vocab ? s : -INFINITY;
+                if (lane == 0 && v0 + e == at[r] && at[r] < vocab) picked[r] = s;
+            }
+            float m = top[r];
+#pragma unroll
+            for (int e = 0; e < E; ++e) m = fmaxf(m, acc[e][r]);
+            const float ref = m == -INFINITY ? 0.f : m;
+            float t = sum[r] * expf(top[r] - ref);
+#pragma unroll
+            for (int e = 0; e < E; ++e) t += expf(acc[e][r] - ref);
+            sum[r] = t;
+            top[r] = m;
+        }
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) joined[warp][r] = make_float2(top[r], sum[r]);
+    }
+    __syncthreads();
+    if (threadIdx.x < rows) {
+        float m = -INFINITY, t = 0.f;
+        for (int q = 0; q < 8; ++q) m = fmaxf(m, joined[q][threadIdx.x].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        for (int q = 0; q < 8; ++q) t += joined[q][threadIdx.x].y * expf(joined[q][threadIdx.x].x - ref);
+        part[threadIdx.x * part_ld + blockIdx.x] = make_float2(m, t);
+    }
+}
+
 __device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
 __device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
@@ -249,6 +372,7 @@ struct Plan {
     int ctas;                 // that share a tile
     int groups;               // CTAs or pairs that the device's SMs hold
     bool copy_h, copy_w, compact, grad;
+    int few;                  // rows of the kernel for few rows (0: the tiled products)
     int64_t rows, dim, vocab;
     int64_t tiled;            // rows of the copy of H and of P: whole tiles
     int64_t seen;             // of them, those that tensor maps see: the rest reads as zero without being read
@@ -265,6 +389,18 @@ struct Plan {
 
 bool for_tma(const void *p, int64_t ld, int64_t elem) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * elem % 16 == 0;
+}
+
+// The rows that the kernel for few rows takes (1, 4 or 8), or 0 where the tiled products are used:
+// where W's rows are no whole 16-byte vectors, H does not fit shared memory, or there are too many
+// rows. Measured, loss over a vocabulary of 32000 and dim 1024, this kernel against the tiles: bf16
+// 1 row 15.7 us against 19.5, 2 rows 22 against 19.6; f32 1, 4, 8 rows 25.5, 29.5, 45 us against 106 (the
+// tiles' copies of W), 16 rows would be two times 45.
+int few_rows(int dtype, int64_t rows, int64_t dim, const void *W, int64_t ldw) {
+    const int64_t elem = dtype == BL_F32 ? 4 : 2;
+    if (rows > (dtype == BL_F32 ? 8 : 1) || !for_tma(W, ldw, elem) || dim * elem % 16 != 0) return 0;
+    const int r = rows <= 1 ? 1 : rows <= 4 ? 4 : 8;
+    return r * dim * 4 <= 44 * 1024 ? r : 0;
 }
 
 Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw,
@@ -305,6 +441,15 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
         if (t == q.wide || cost < least) q.tile_n = t, least = cost;
     }
     q.part_ld = 2 * cdiv(vocab, q.tile_n);
+    if (!grad) {
+        q.few = few_rows(dtype, rows, dim, W, ldw);
+        if (q.few) {
+            q.part_ld = std::min<int64_t>(cdiv(vocab, 8 * few_entries(q.few)), static_cast<int64_t>(sms) * few_ctas(q.few));
+            q.copy_h = q.copy_w = false;
+            q.pieces = 1;
+            q.piece = up(vocab, kTileN);
+        }
+    }
     q.ldo = up(dim, 32);
     // dH's partial sums: room for as many parts as are wanted if every row counts, and up to six (256 MB)
     // for the case that few do
@@ -482,6 +627,18 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     if (q.compact)
         BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept,
                           Cut{q.ctas, dim, q.wide, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.loss, c.lse));
+    if (q.few) {
+        auto kernel = few_kernel<T, 1>;
+        if constexpr (PLANES == 3) kernel = q.few == 1 ? kernel : q.few == 4 ? few_kernel<T, 4> : few_kernel<T, 8>;
+        float2 *const part = reinterpret_cast<float2 *>(c.ws + q.part);
+        float *const picked = reinterpret_cast<float *>(c.ws + q.picked);
+        BL_TRY(launch_pdl(kernel, static_cast<unsigned>(q.part_ld), 256, static_cast<size_t>(q.few) * c.dim * 4, c.s,
+                          static_cast<const T *>(c.H), c.ldh, rows, dim, static_cast<const T *>(c.W), c.ldw,
+                          static_cast<int>(c.vocab), c.target, part, q.part_ld, picked));
+        BL_TRY(launch_pdl(loss_kernel, 1, 256, 0, c.s, part, q.part_ld, picked, c.target, c.vocab, rows, nullptr, nullptr, flags, 0,
+                          c.loss, c.lse));
+        return BL_SUCCESS;
+    }
     const Columns in_place{64, 0, 1}, in_panels{0, 1, static_cast<int>(q.panels)};
     CUtensorMap h_k;
     Copy copy_h{};

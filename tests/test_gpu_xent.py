@@ -248,3 +248,22 @@ def test_refusals():
     assert raw.bl_xent(bl.BL_BF16, 8, 16, 32, H.data_ptr(), 16, W.data_ptr(), 16, t.data_ptr(), lse.data_ptr(),
                        lse.data_ptr(), ws.data_ptr(), ws.numel(), None) == 1
     assert b"workspace" in raw.bl_last_error()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 7, 8, 9])
+@pytest.mark.parametrize("dim,vocab,pad_w", [(8, 1, 0), (24, 31, 8), (1024, 4099, 0), (1408, 100, 16), (5632, 777, 0), (12000, 300, 0), (1001, 500, 0)])
+def test_loss_of_few_rows(kind, rows, dim, vocab, pad_w):
+    """Around the bounds of the kernel for few rows: its most rows, its longest rows, rows of W that
+    are no whole vectors, fewer entries than a CTA takes; one row without a target, holding NaN."""
+    torch, bl = torch_cuda(), lib()
+    H, W, t, g = make(rows, dim, vocab, kind, seed=rows * dim, pad_h=3, pad_w=pad_w)
+    if rows > 2:
+        t[1] = -5
+        H[1] = float("nan")
+    ref = reference(H, W, t, g, kind)
+    loss, lse = bl.xent(H, W, t)
+    check(lse, ref, "lse")
+    check(loss, ref, "loss")
+    again = bl.xent(H, W, t)
+    assert torch.equal(loss, again[0]) and torch.equal(lse, again[1])
