@@ -1,5 +1,7 @@
 /*
- * bl.h -- batched Cholesky factorisation and positive-definite solve for GB300 (sm_103a).
+ * bl.h -- batched Cholesky factorisation and positive-definite solve for GB300 (sm_103a), and
+ * the training operators around them (softmax cross entropy with its gradient, gradient norm and
+ * clipping).
  *
  * C ABI of libbl.so. All matrices are column-major: element (i, j) of item b of a batch lives
  * at  base + b*stride + j*ld + i  (in elements of the dtype; complex elements are interleaved
@@ -177,7 +179,7 @@ bl_status bl_xent(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, cons
  *   workspace at least bl_xent_workspace(..., grad = 1) bytes.
  * P is formed piece by piece of the vocabulary and rounded to bf16 for bf16 operands (relative
  * 2^-9 an element, what the gradients themselves are rounded to); f32 operands keep it in f32.
- * A kernel that gave up waiting makes dH NaN. Other arguments as bl_xent.
+ * A kernel that gave up waiting makes dH NaN; dW is undefined then. Other arguments as bl_xent.
  */
 bl_status bl_xent_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
                        const void *W, int64_t ldw, const int64_t *target, const float *lse, const float *g,

@@ -1,4 +1,5 @@
-"""Batched Cholesky factorisation (potrf) and SPD solves (posv, potrs) on GB300.
+"""Batched Cholesky factorisation (potrf) and SPD solves (posv, potrs) on GB300, and the
+operators of a training step around them (xent, xent_grad, gnorm, gclip).
 
 Thin ctypes binding over ``libbl.so`` (the C ABI in ``include/bl.h``). This module only
 marshals arguments: every step of the computation runs in the library's CUDA kernels. There is

@@ -561,7 +561,7 @@ const char *bl_status_string(bl_status s) {
 
 const char *bl_last_error(void) { return t_error.c_str(); }
 const char *bl_last_choice(void) { return t_choice.c_str(); }
-int bl_version(void) { return 100; }
+int bl_version(void) { return 200; }
 
 // Thread-local route pin, overriding BL_<OP>_ROUTE for this thread. op is "potrf", "posv" or
 // "potrs"; spelling NULL or "" clears the pin, "auto" selects by table. Returns BL_SUCCESS, or

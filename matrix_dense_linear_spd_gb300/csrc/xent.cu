@@ -212,6 +212,7 @@ struct FewVec<__nv_bfloat16> {
 constexpr int few_entries(int R) { return R == 1 ? 2 : 4; }
 constexpr int few_ahead(int R) { return R == 1 ? 4 : 2; }
 constexpr int few_ctas(int R) { return R == 1 ? 4 : R == 4 ? 2 : 1; }
+constexpr int few_smem(int R) { return 200 * 1024 / few_ctas(R); }      // H's share of the SM's shared memory
 
 template <typename T, int R>
 __global__ void __launch_bounds__(256, few_ctas(R))
@@ -400,7 +401,7 @@ int few_rows(int dtype, int64_t rows, int64_t dim, const void *W, int64_t ldw) {
     const int64_t elem = dtype == BL_F32 ? 4 : 2;
     if (rows > (dtype == BL_F32 ? 8 : 1) || !for_tma(W, ldw, elem) || dim * elem % 16 != 0) return 0;
     const int r = rows <= 1 ? 1 : rows <= 4 ? 4 : 8;
-    return r * dim * 4 <= 44 * 1024 ? r : 0;
+    return r * dim * 4 <= few_smem(r) ? r : 0;
 }
 
 Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw,
@@ -573,6 +574,19 @@ cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUte
                      : launch_tiles<MODE, PLANES, 2>(ma, mb, mo, a, flags, sms, s);
 }
 
+// Raise a kernel's dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (bit & done.load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
 template <typename T>
 Copy copy_of(const void *src, int64_t ld, int64_t rows, int64_t dim, const int64_t *target, int64_t vocab, const int *order,
              const int *kept, int tile, void *dst, int64_t height, int sms) {
@@ -632,6 +646,8 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         if constexpr (PLANES == 3) kernel = q.few == 1 ? kernel : q.few == 4 ? few_kernel<T, 4> : few_kernel<T, 8>;
         float2 *const part = reinterpret_cast<float2 *>(c.ws + q.part);
         float *const picked = reinterpret_cast<float *>(c.ws + q.picked);
+        static std::atomic<unsigned long long> allowed[3];
+        BL_TRY(allow_smem(kernel, few_smem(q.few), allowed[q.few / 4]));
         BL_TRY(launch_pdl(kernel, static_cast<unsigned>(q.part_ld), 256, static_cast<size_t>(q.few) * c.dim * 4, c.s,
                           static_cast<const T *>(c.H), c.ldh, rows, dim, static_cast<const T *>(c.W), c.ldw,
                           static_cast<int>(c.vocab), c.target, part, q.part_ld, picked));

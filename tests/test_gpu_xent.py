@@ -252,7 +252,7 @@ def test_refusals():
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 7, 8, 9])
-@pytest.mark.parametrize("dim,vocab,pad_w", [(8, 1, 0), (24, 31, 8), (1024, 4099, 0), (1408, 100, 16), (5632, 777, 0), (12000, 300, 0), (1001, 500, 0)])
+@pytest.mark.parametrize("dim,vocab,pad_w", [(8, 1, 0), (24, 31, 8), (1024, 4099, 0), (1408, 100, 16), (5632, 777, 0), (12000, 300, 0), (6400, 130, 0), (1001, 500, 0)])
 def test_loss_of_few_rows(kind, rows, dim, vocab, pad_w):
     """Around the bounds of the kernel for few rows: its most rows, its longest rows, rows of W that
     are no whole vectors, fewer entries than a CTA takes; one row without a target, holding NaN."""
@@ -267,3 +267,32 @@ def test_loss_of_few_rows(kind, rows, dim, vocab, pad_w):
     check(loss, ref, "loss")
     again = bl.xent(H, W, t)
     assert torch.equal(loss, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("kind,rows,dim,vocab,ignored", [
+    ("bf16", 1, 64, 300, 0.0), ("bf16", 5, 72, 300, 0.5), ("bf16", 130, 72, 333, 0.9), ("bf16", 300, 129, 1000, 0.4),
+    ("f32", 3, 64, 300, 0.3), ("f32", 40, 68, 301, 0.3), ("f32", 200, 131, 700, 0.97), ("f32", 40, 16392, 7000, 0.2)])
+def test_nothing_is_read_from_the_workspace_before_it_is_written(kind, rows, dim, vocab, ignored):
+    """A workspace of all ones (NaN in every float type) gives the bits that any other gives."""
+    torch, bl = torch_cuda(), lib()
+    H, W, t, g = make(rows, dim, vocab, kind, seed=23, ignored=ignored)
+    want = run_all(H, W, t, g)
+    raw, code = bl.get_lib(), bl.BL_F32 if kind == "f32" else bl.BL_BF16
+    s = torch.cuda.current_stream().cuda_stream
+
+    def scratch(grad):
+        need = raw.bl_xent_workspace(code, rows, dim, vocab, H.data_ptr(), dim, W.data_ptr(), dim, grad)
+        return torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    ws = scratch(0)
+    assert raw.bl_xent(code, rows, dim, vocab, H.data_ptr(), dim, W.data_ptr(), dim, t.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                       ws.data_ptr(), ws.numel() - 256, s) == 0
+    assert bool((ws[-256:] == 255).all()), "wrote past the workspace"
+    ws = scratch(1)
+    dH, dW = torch.full_like(H, float("nan")), torch.full_like(W, float("nan"))
+    assert raw.bl_xent_grad(code, rows, dim, vocab, H.data_ptr(), dim, W.data_ptr(), dim, t.data_ptr(), lse.data_ptr(), g.data_ptr(),
+                            dH.data_ptr(), dim, dW.data_ptr(), dim, ws.data_ptr(), ws.numel() - 256, s) == 0
+    torch.cuda.synchronize()
+    assert bool((ws[-256:] == 255).all()), "wrote past the workspace"
+    for name, v in (("loss", loss), ("lse", lse), ("dH", dH), ("dW", dW)):
+        assert torch.equal(want[name], v), name
