@@ -185,10 +185,13 @@ __global__ void __launch_bounds__(256)
 // shared-memory reads of H above. A warp takes four vocabulary entries
 // at a time, its lanes share K; H waits in shared memory as f32. Each CTA leaves one maximum and sum
 // a row. W is read in place whatever its type: no planes, no copies.
-template <typename T>
-struct FewVec;
+template <typename T, bool VEC>
+struct FewVec {                                    // rows that start anywhere: value by value
+    static constexpr int N = 1;
+    __device__ static void load(const T *p, float (&v)[1]) { v[0] = static_cast<float>(__ldcs(p)); }
+};
 template <>
-struct FewVec<float> {
+struct FewVec<float, true> {
     static constexpr int N = 4;
     __device__ static void load(const float *p, float (&v)[4]) {
         const float4 q = __ldcs(reinterpret_cast<const float4 *>(p));
@@ -196,7 +199,7 @@ struct FewVec<float> {
     }
 };
 template <>
-struct FewVec<__nv_bfloat16> {
+struct FewVec<__nv_bfloat16, true> {
     static constexpr int N = 8;
     __device__ static void load(const __nv_bfloat16 *p, float (&v)[8]) {
         const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(p));
@@ -208,17 +211,17 @@ struct FewVec<__nv_bfloat16> {
         }
     }
 };
-// Entries a warp takes at a time, 16-byte steps of K in flight for each, and CTAs per SM
+// Entries a warp takes at a time, steps of K in flight for each, and CTAs per SM
 constexpr int few_entries(int R) { return R == 1 ? 2 : 4; }
-constexpr int few_ahead(int R) { return R == 1 ? 4 : 2; }
+constexpr int few_ahead(int R, bool vec) { return (R == 1 ? 4 : 2) * (vec ? 1 : 2); }
 constexpr int few_ctas(int R) { return R == 1 ? 4 : R == 4 ? 2 : 1; }
 constexpr int few_smem(int R) { return 200 * 1024 / few_ctas(R); }      // H's share of the SM's shared memory
 
-template <typename T, int R>
+template <typename T, int R, bool VEC>
 __global__ void __launch_bounds__(256, few_ctas(R))
     few_kernel(const T *H, int64_t ldh, int rows, int dim, const T *W, int64_t ldw, int vocab, const int64_t *target,
                float2 *part, int64_t part_ld, float *picked) {
-    constexpr int N = FewVec<T>::N, E = few_entries(R), AHEAD = few_ahead(R);
+    constexpr int N = FewVec<T, VEC>::N, E = few_entries(R), AHEAD = few_ahead(R, VEC);
     extern __shared__ __align__(16) float few_h[];           // [R][dim]
     __shared__ float2 joined[8][R];
     pdl_release();
@@ -251,21 +254,24 @@ __global__ void __launch_bounds__(256, few_ctas(R))
         for (int k = lane * N; k < dim; k += 32 * N) {
             float x[E][N];
 #pragma unroll
-            for (int e = 0; e < E; ++e) FewVec<T>::load(w[e] + k, x[e]);
+            for (int e = 0; e < E; ++e) FewVec<T, VEC>::load(w[e] + k, x[e]);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float4 *const h = reinterpret_cast<const float4 *>(few_h + r * dim + k);
+                const float *const h = few_h + r * dim + k;
+                float y[N];
+                if constexpr (VEC) {
 #pragma unroll
-                for (int q = 0; q < N / 4; ++q) {
-                    const float4 y = h[q];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        acc[e][r] = fmaf(x[e][4 * q], y.x, acc[e][r]);
-                        acc[e][r] = fmaf(x[e][4 * q + 1], y.y, acc[e][r]);
-                        acc[e][r] = fmaf(x[e][4 * q + 2], y.z, acc[e][r]);
-                        acc[e][r] = fmaf(x[e][4 * q + 3], y.w, acc[e][r]);
+                    for (int q = 0; q < N; q += 4) {
+                        const float4 t = *reinterpret_cast<const float4 *>(h + q);
+                        y[q] = t.x, y[q + 1] = t.y, y[q + 2] = t.z, y[q + 3] = t.w;
                     }
+                } else {
+                    y[0] = h[0];
                 }
+#pragma unroll
+                for (int q = 0; q < N; ++q)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e][r] = fmaf(x[e][q], y[q], acc[e][r]);
             }
         }
 #pragma unroll
@@ -363,7 +369,10 @@ __global__ void __launch_bounds__(256)
 
 // K is added in tensor memory over so many 64-deep steps at a time where the result is f32
 constexpr int kChunkF32 = 2, kChunkLoss = 16, kWhole = 1 << 30;
-constexpr int64_t kPieceBytes = int64_t(512) << 20;     // of P, and of a piece's copy of W
+// Bytes of P, and of a piece's copy of W, that a piece of the vocabulary may take. Steps of 4096 x 4096 x
+// 131072 in bf16 and 1024 x 1024 x 32000 in f32 at 64, 128, 512 and 2048 MB: 11.04, 10.84, 10.66, 10.65 ms
+// and 1.22, 1.13, 1.04, 1.04 ms
+constexpr int64_t kPieceBytes = int64_t(512) << 20;
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t cdiv(int64_t v, int64_t by) { return (v + by - 1) / by; }
@@ -393,13 +402,14 @@ bool for_tma(const void *p, int64_t ld, int64_t elem) {
 }
 
 // The rows that the kernel for few rows takes (1, 4 or 8), or 0 where the tiled products are used:
-// where W's rows are no whole 16-byte vectors, H does not fit shared memory, or there are too many
-// rows. Measured, loss over a vocabulary of 32000 and dim 1024, this kernel against the tiles: bf16
-// 1 row 15.7 us against 19.5, 2 rows 22 against 19.6; f32 1, 4, 8 rows 25.5, 29.5, 45 us against 106 (the
-// tiles' copies of W), 16 rows would be two times 45.
+// where there are too many rows, or H does not fit shared memory. Measured, loss over a vocabulary of
+// 32000, this kernel against the tiles: dim 1024, bf16 1 row 15.7 us against 19.5, 2 rows 22 against 19.6;
+// f32 1, 4, 8 rows 25.5, 29.5, 45 us against 106 (the tiles' copies of W); dim 1021, whose rows start off the
+// vectors and which the tiles copy, bf16 1, 4, 8 rows 29, 37, 64 us against 43, f32 35, 42, 69 against 116.
+bool few_vec(const void *W, int64_t ldw, int64_t dim, int64_t elem) { return for_tma(W, ldw, elem) && dim * elem % 16 == 0; }
 int few_rows(int dtype, int64_t rows, int64_t dim, const void *W, int64_t ldw) {
-    const int64_t elem = dtype == BL_F32 ? 4 : 2;
-    if (rows > (dtype == BL_F32 ? 8 : 1) || !for_tma(W, ldw, elem) || dim * elem % 16 != 0) return 0;
+    const bool vec = few_vec(W, ldw, dim, dtype == BL_F32 ? 4 : 2);
+    if (rows > (dtype == BL_F32 ? 8 : vec ? 1 : 4)) return 0;
     const int r = rows <= 1 ? 1 : rows <= 4 ? 4 : 8;
     return r * dim * 4 <= few_smem(r) ? r : 0;
 }
@@ -410,6 +420,8 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     q.planes = dtype == BL_F32 ? 3 : 1;
     q.pairs = dtype == BL_F32 ? 6 : 1;
     q.compact = rows > kTileM;
+    // pairs of CTAs above one row tile: steps at dim 1024, vocabulary 32000 on single CTAs against pairs: bf16
+    // 64 rows 75 us, 93; 128 rows 78, 93; 200 rows 111, 108; f32 64 rows 319, 358; 200 rows 467, 398
     q.ctas = rows > kTileM ? 2 : 1;
     q.groups = std::max(1, sms / q.ctas);
     q.wide = q.ctas == 1 && q.planes == 3 ? Ring<1, 3>::kTile : kTileN;
@@ -642,12 +654,16 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept,
                           Cut{q.ctas, dim, q.wide, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.loss, c.lse));
     if (q.few) {
-        auto kernel = few_kernel<T, 1>;
-        if constexpr (PLANES == 3) kernel = q.few == 1 ? kernel : q.few == 4 ? few_kernel<T, 4> : few_kernel<T, 8>;
+        const bool vec = few_vec(c.W, c.ldw, c.dim, sizeof(T));
+        auto kernel = q.few == 1 ? (vec ? few_kernel<T, 1, true> : few_kernel<T, 1, false>) : few_kernel<T, 4, false>;
+        if constexpr (PLANES == 3) {
+            if (q.few == 4 && vec) kernel = few_kernel<T, 4, true>;
+            if (q.few == 8) kernel = vec ? few_kernel<T, 8, true> : few_kernel<T, 8, false>;
+        }
         float2 *const part = reinterpret_cast<float2 *>(c.ws + q.part);
         float *const picked = reinterpret_cast<float *>(c.ws + q.picked);
-        static std::atomic<unsigned long long> allowed[3];
-        BL_TRY(allow_smem(kernel, few_smem(q.few), allowed[q.few / 4]));
+        static std::atomic<unsigned long long> allowed[6];
+        BL_TRY(allow_smem(kernel, few_smem(q.few), allowed[q.few / 4 + 3 * vec]));
         BL_TRY(launch_pdl(kernel, static_cast<unsigned>(q.part_ld), 256, static_cast<size_t>(q.few) * c.dim * 4, c.s,
                           static_cast<const T *>(c.H), c.ldh, rows, dim, static_cast<const T *>(c.W), c.ldw,
                           static_cast<int>(c.vocab), c.target, part, q.part_ld, picked));

@@ -19,7 +19,14 @@
 // The tensor cores' f32 accumulation cuts where f32 would round, so a long chain of products is
 // biased towards zero, by about 2^-25 of the sum a step. Where the result is f32 (the loss; every
 // product of f32 operands) the chain is cut into chunks of K, whose sums are added in registers.
-// Measured at rows 1024, dim 1024, vocabulary 32000, f32: dH 9.6e-6 off without chunks.
+// Measured at rows 1024, dim 1024, vocabulary 32000, f32: dH 9.6e-6 off without chunks, 4.2e-7 with
+// chunks of 128 (9.2e-7 with 256, 2.5% faster); the bf16 loss of 4096 x 4096 x 16384 with chunks of 512,
+// 1024, 2048 and none: 317, 301, 294, 291 us.
+//
+// What bounds it: the operands' way into shared memory. A bf16 stage brings 32 KB for the 512 cycles of
+// its products, 64 bytes a cycle, and the tensor pipe is 83 to 86% busy (303 to 312 us for each of the four
+// products at 4096 x 4096 x 16384, 1,760 to 1,810 TFLOP/s); an f32 stage brings half of that a cycle, and
+// the pipe is 93 to 96% busy. Then the power cap: back to back the clock falls from 1.9 to 1.65 GHz.
 //
 // P and the copies of H and W are stored in panels of 64 columns ([plane][panel][row][64]), so that
 // every operand tile is one contiguous piece of memory in either direction of use.
@@ -328,7 +335,8 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
             v[i] = r.counted && n0 + c0 + i < a.n ? r.g * e : 0.f;      // panels are whole: zero to their end
         }
     }
-    const bool there = row0 < r.m;      // P has whole row tiles as well: rows that do not count are zero
+    // where the rows that count are copied together P has whole row tiles: dW multiplies their zeros
+    const bool there = row0 < r.m || (MODE == PROBS && a.kept != nullptr);
     if constexpr (MODE == DH || PLANES == 3) {
         if constexpr (MODE == PROBS) {
             // three planes of 32 values: 64 bytes a line each
@@ -346,7 +354,7 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
                     *reinterpret_cast<uint4 *>(stage + (threadIdx.x & 31) * 64 + ((j ^ ((threadIdx.x >> 1) & 3)) << 4)) =
                         make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
                 }
-                lines_store(map, stage, c0 & 32, row0, pl * a.p_panels + (n0 + c0) / 64, false);
+                if (there) lines_store(map, stage, c0 & 32, row0, pl * a.p_panels + (n0 + c0) / 64, false);
             }
         } else {
             lines_free();
@@ -362,7 +370,7 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
         put_bf16(stage, c0, v);
         if ((c0 & 32) || c0 + 32 >= cols) {
             if (MODE == DW && a.out) lines_copy<__nv_bfloat16>(a, stage, row0, n0 + (c0 & ~63));
-            else if (MODE == PROBS) lines_store(map, stage, 0, row0, (n0 + c0) / 64, false);
+            else if (there && MODE == PROBS) lines_store(map, stage, 0, row0, (n0 + c0) / 64, false);
             else if (there) lines_store(map, stage, n0 + (c0 & ~63), row0, 0, false);
         }
     }
