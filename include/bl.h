@@ -177,8 +177,9 @@ bl_status bl_xent(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, cons
  *   dH, dW    the gradients, laid out as H and W (lddh, lddw >= dim), overwritten. Either may be
  *             NULL: that product is skipped. They overlap no input.
  *   workspace at least bl_xent_workspace(..., grad = 1) bytes.
- * P is formed piece by piece of the vocabulary and rounded to bf16 for bf16 operands (relative
- * 2^-9 an element, what the gradients themselves are rounded to); f32 operands keep it in f32.
+ * P is formed piece by piece of the vocabulary, in units of the largest |g| of a row that counts, and
+ * rounded to bf16 for bf16 operands (relative 2^-8 an element, as the gradients themselves are);
+ * f32 operands keep it in f32.
  * A kernel that gave up waiting makes dH NaN; dW is undefined then. Other arguments as bl_xent.
  */
 bl_status bl_xent_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,

@@ -35,15 +35,17 @@ __device__ __forceinline__ bool has_target(const int64_t *target, int64_t row, i
 }
 
 // One block: the rows that count, in order; each row's place among them (-1: does not count); how
-// many they are, and the parts of dH's K axis. The rows that do not count get the results they have (loss, lse: or null).
+// many they are, the parts of dH's K axis, and the unit of P (g: or null). The rows that do not count get the results they have (loss, lse: or null).
 __global__ void __launch_bounds__(1024)
-    index_kernel(const int64_t *target, int64_t vocab, int rows, int *order, int *place, int *kept, Cut cut, float *loss,
-                 float *lse) {
+    index_kernel(const int64_t *target, int64_t vocab, int rows, int *order, int *place, int *kept, Cut cut,
+                 const float *g, float *unit, float *loss, float *lse) {
     __shared__ int sums[2][32];
+    __shared__ float most[32];
     pdl_release();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int before = 0;
+    float m = 0.f;
     for (int r0 = 0, turn = 0; r0 < rows; r0 += 1024, turn ^= 1) {
         const int row = r0 + threadIdx.x;
         const bool in = row < rows, counts = in && has_target(target, row, vocab);
@@ -61,13 +63,21 @@ __global__ void __launch_bounds__(1024)
         before += __shfl_sync(0xffffffffu, upto, 31);
         if (in) {
             place[row] = counts ? at : -1;
+            if (counts && g) m = fmaxf(m, fabsf(g[row]));
             if (counts) order[at] = row;
             else if (loss) loss[row] = lse[row] = 0.f;
         }
     }
-    if (threadIdx.x == 0) {
-        kept[0] = before;
-        kept[1] = parts_for(cut, before);
+    m = warp_max(m);
+    if (lane == 0) most[warp] = m;
+    __syncthreads();
+    if (warp == 0) {
+        m = warp_max(most[lane]);
+        if (lane == 0) {
+            kept[0] = before;
+            kept[1] = parts_for(cut, before);
+            if (g) *unit = unit_from(m);
+        }
     }
 }
 
@@ -86,6 +96,8 @@ struct Copy {
     int panels;
     int64_t height;
     int vec, blocks;
+    const float *g;           // of the gradient's rows in their places: the unit of P is found on the way
+    float *unit;
 };
 // Two copies in one launch, H's and the first piece's of W (either may be without blocks).
 template <typename T, int PLANES>
@@ -95,6 +107,10 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ Copy 
     const bool second = static_cast<int>(blockIdx.x) >= one.blocks;
     const int block = second ? blockIdx.x - one.blocks : blockIdx.x;
     const Copy &w = second ? two : one;
+    if (w.g && block == 0 && threadIdx.x < 32) {
+        const float u = unit_of_rows(w.g, w.target, w.vocab, static_cast<int>(w.rows));
+        if (threadIdx.x == 0) *w.unit = u;
+    }
     const int64_t count = w.kept ? *w.kept : w.rows, filled = max((count + w.tile - 1) / w.tile, int64_t(1)) * w.tile;
     const int64_t per_row = w.panels * 8, all = filled * per_row, plane = w.panels * w.height * 64;
     for (int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x; i < all;
@@ -314,18 +330,20 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
 }
 
-// dH from the parts' sums, four columns a thread; rows without a target are zero. A product that
+// dH from the parts' sums, four columns a thread, times the unit of P; rows without a target are zero. A product that
 // gave up makes it NaN. With SHARE = 8 eight lanes of a warp add every eighth part each (many parts
 // mean few results: 64 rows x 1024 in 38 parts took 14 us with one thread a result).
 template <typename T, int SHARE>
 __global__ void __launch_bounds__(256)
     dh_kernel(const float *part, int all_parts, int64_t rows, int64_t ldo, int dim, const int64_t *target, int64_t vocab,
-              const int *place, const int *kept_rows, const int32_t *flags, int flag_count, T *dh, int64_t ld, int vec) {
+              const int *place, const int *kept_rows, const float *unit_of_p, const int32_t *flags, int flag_count,
+              T *dh, int64_t ld, int vec) {
     constexpr int SIDE = 32 / SHARE;                // results that a warp works on at once
     pdl_release();
     pdl_wait();
     const bool bad = __syncthreads_or(flags_seen(flags, flag_count)) != 0;
     const int kept = kept_rows ? kept_rows[0] : static_cast<int>(rows), splits = kept_rows ? kept_rows[1] : all_parts;
+    const float unit = *unit_of_p;
     const int64_t height = part_rows(kept), part_step = SHARE * height * (ldo / 4);
     const int lane = threadIdx.x & 31, mine = SHARE == 1 ? 0 : lane / SIDE;
     const int64_t per_row = (dim + 3) / 4, all = rows * per_row, step = static_cast<int64_t>(gridDim.x) * 256 / SHARE;
@@ -351,6 +369,7 @@ __global__ void __launch_bounds__(256)
             v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
             v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
         }
+        v.x *= unit, v.y *= unit, v.z *= unit, v.w *= unit;
         if (bad) v = make_float4(NAN, NAN, NAN, NAN);
         if (i >= all || mine != 0) continue;
         T *const d = dh + row * ld + c;
@@ -394,7 +413,7 @@ struct Plan {
     int first_kb;             // 64-deep steps of the first piece
     int64_t slab_rows;        // of dH's partial sums, all parts together
     int64_t ldo;              // row length of dH's partial sums
-    int64_t flags, kept, order, place, h, w, part, picked, p, dh, bytes;   // offsets into the workspace
+    int64_t flags, kept, unit, order, place, h, w, part, picked, p, dh, bytes;   // offsets into the workspace
 };
 
 bool for_tma(const void *p, int64_t ld, int64_t elem) {
@@ -480,6 +499,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     };
     q.flags = take(q.pieces * 3 * sms * 4);
     q.kept = take(8);
+    q.unit = take(4);
     if (q.compact) {
         q.order = take(rows * 4);
         q.place = take(rows * 4);
@@ -648,11 +668,12 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     int *const kept = q.compact ? reinterpret_cast<int *>(c.ws + q.kept) : nullptr;
     int *const order = q.compact ? reinterpret_cast<int *>(c.ws + q.order) : nullptr;
     int *const place = q.compact ? reinterpret_cast<int *>(c.ws + q.place) : nullptr;
+    float *const unit = reinterpret_cast<float *>(c.ws + q.unit);
     int32_t *const flags = reinterpret_cast<int32_t *>(c.ws + q.flags);
     int flag_count = 0;
     if (q.compact)
         BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept,
-                          Cut{q.ctas, dim, q.wide, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.loss, c.lse));
+                          Cut{q.ctas, dim, q.wide, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.g, unit, c.loss, c.lse));
     if (q.few) {
         const bool vec = few_vec(c.W, c.ldw, c.dim, sizeof(T));
         auto kernel = q.few == 1 ? (vec ? few_kernel<T, 1, true> : few_kernel<T, 1, false>) : few_kernel<T, 4, false>;
@@ -676,6 +697,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     Copy copy_h{};
     if (q.copy_h) {
         copy_h = copy_of<T>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, order, kept, q.ctas * kTileM, c.ws + q.h, q.tiled, c.sms);
+        if (!q.compact) copy_h.g = c.g, copy_h.unit = unit;
         BL_MAP(map_panels(&h_k, c.ws + q.h, q.seen, q.tiled, PLANES * q.panels, kTileM));
     } else {
         BL_MAP(map_bf16(&h_k, c.H, c.dim, c.rows, 1, c.ldh, c.ldh, kTileM));
@@ -688,6 +710,8 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     base.chunk = PLANES == 3 ? kChunkF32 : kWhole;
     base.target = c.target;
     base.vocab = c.vocab;
+    base.g = c.g;
+    base.unit = unit;
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t v0 = i * q.piece, n = std::min(q.piece, c.vocab - v0);
         const char *const w_at = static_cast<const char *>(c.W) + v0 * c.ldw * static_cast<int64_t>(sizeof(T));
@@ -730,7 +754,6 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         BL_MAP(map_panels(&p_out, pp, q.seen, q.tiled, PLANES * p_panels, 32, PLANES == 1 ? 128 : 64));
         a.p_panels = static_cast<int>(p_panels);
         a.lse = c.lse_in;
-        a.g = c.g;
         BL_TRY((launch_gemm<PROBS, PLANES>(h_k, w_k, p_out, a, q.ctas, flag_count, c.sms, c.s)));
         if (c.dH) {
             CUtensorMap p_k, sums;
@@ -782,8 +805,8 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         const int64_t es = sizeof(T);
         const int vec = reinterpret_cast<uintptr_t>(c.dH) % (4 * es) == 0 && c.lddh % 4 == 0;
         BL_TRY(launch_pdl(share == 8 ? dh_kernel<T, 8> : dh_kernel<T, 1>, static_cast<unsigned>(blocks), 256, 0, c.s,
-                          reinterpret_cast<const float *>(c.ws + q.dh), q.parts, c.rows, q.ldo, dim, c.target, c.vocab, place, kept, flags,
-                          flag_count, static_cast<T *>(c.dH), c.lddh, vec));
+                          reinterpret_cast<const float *>(c.ws + q.dh), q.parts, c.rows, q.ldo, dim, c.target, c.vocab, place, kept, unit,
+                          flags, flag_count, static_cast<T *>(c.dH), c.lddh, vec));
     }
     return BL_SUCCESS;
 }

@@ -98,6 +98,7 @@ struct GemmArgs {
     int64_t part_ld;
     float *picked;             // LOGITS: the target's logit of each row
     const float *lse, *g;      // PROBS
+    const float *unit;         // PROBS, DW: the scale of P, below
     int p_panels;              // of a plane of P
     void *out;                 // DW: the result, where its rows do not start on 16-byte boundaries
     int64_t ldo;
@@ -209,6 +210,24 @@ __device__ __forceinline__ void split3(float x, float &x0, float &x1, float &x2)
     x2 = fine ? __bfloat162float(__float2bfloat16_rn(r - x1)) : 0.f;
 }
 
+// P is kept in units of the largest |g| of a row that counts, and dH and dW are multiplied by it in f32
+// at the end: where all rows weigh the same, as in a mean, g then rounds nothing. (P_rv is close to
+// -g at the targets of unsure rows, so g's own rounding to bf16, up to 2^-8, would be the same for all of
+// them: gradients of 1279 rows of equal weight were up to 3.1e-3 off, rounded to bf16 themselves 1.7e-3.)
+__device__ __forceinline__ float unit_from(float most) { return most > 0.f && most < INFINITY ? most : 1.f; }
+__device__ __forceinline__ float warp_max(float m) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+// By all lanes of a warp, for rows in their places (at most a row tile).
+__device__ __forceinline__ float unit_of_rows(const float *g, const int64_t *target, int64_t vocab, int rows) {
+    float m = 0.f;
+    for (int r = threadIdx.x & 31; r < rows; r += 32)
+        if (target[r] >= 0 && target[r] < vocab) m = fmaxf(m, fabsf(g[r]));
+    return unit_from(warp_max(m));
+}
+
 // ---- epilogues. A warp owns 32 rows (a lane each) and 128 columns, in blocks of 32 columns.
 
 struct Row {              // what an epilogue keeps of its row
@@ -217,6 +236,7 @@ struct Row {              // what an epilogue keeps of its row
     bool counted;
     float top, sum, picked;    // LOGITS
     float lse, ref, g;         // PROBS
+    float unit;                // PROBS, DW
 };
 
 template <int MODE>
@@ -234,7 +254,7 @@ __device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s,
         r.sum = r.picked = 0.f;
         if constexpr (MODE == PROBS) {
             r.lse = r.counted ? a.lse[src] : 0.f;
-            r.g = r.counted ? a.g[src] : 0.f;
+            r.g = r.counted ? a.g[src] / r.unit : 0.f;
             r.ref = r.lse * kLog2e;
         }
     }
@@ -334,6 +354,10 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
             if (i == r.at - c0) e -= 1.f;
             v[i] = r.counted && n0 + c0 + i < a.n ? r.g * e : 0.f;      // panels are whole: zero to their end
         }
+    }
+    if constexpr (MODE == DW) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= r.unit;
     }
     // where the rows that count are copied together P has whole row tiles: dW multiplies their zeros
     const bool there = row0 < r.m || (MODE == PROBS && a.kept != nullptr);
@@ -545,6 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = warp & 3, half = (warp - 4) >> 2;  // a warp may read its quarter of the lanes
         unsigned char *const stage = staging + (warp - 4) * kStageBytes;
         const Shape sh = shape_of<MODE, CTAS>(a);
+        float unit = 1.f;
+        if constexpr (MODE == PROBS || MODE == DW) unit = *a.unit;
         uint32_t done = 0;
         bool ok = true;
         for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
@@ -553,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (MODE == PROBS) cols = (cols + 63) & ~63;
             cols = min(cols, (half + 1) * kHalf);
             Row r;
+            r.unit = unit;
             begin<MODE>(r, a, sh, k, (k.tm * CTAS + rank) * kTileM + quad * 32 + lane);
             float v[SUMS ? kHalf / 32 : 1][32];
             if constexpr (SUMS) {

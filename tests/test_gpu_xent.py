@@ -296,3 +296,21 @@ def test_nothing_is_read_from_the_workspace_before_it_is_written(kind, rows, dim
     assert bool((ws[-256:] == 255).all()), "wrote past the workspace"
     for name, v in (("loss", loss), ("lse", lse), ("dH", dH), ("dW", dW)):
         assert torch.equal(want[name], v), name
+
+
+@pytest.mark.parametrize("rows", [100, 1000])
+def test_equal_weights_round_nothing(rows):
+    """Unsure rows of one weight g that lies halfway between two bf16 values: P is -g at the targets
+    and g / vocab elsewhere. In units of g that is -(1 - 2^-12), 2^-11 off at most in bf16, so what is
+    left is the rounding of dH and dW themselves, uniform within 2^-8: a relative 2-norm of at most
+    2^-8 / sqrt(3) + 2^-11 over many values (g itself would be 2^-8 off)."""
+    torch, bl = torch_cuda(), lib()
+    H, W, t, _ = make(rows, 512, 4096, "bf16", seed=29)
+    W.mul_(2.0 ** -10)
+    g = torch.full((rows,), (1 + 2.0 ** -8) * 2.0 ** -10, device="cuda")
+    ref = reference(H, W, t, g, "bf16")
+    _, lse = bl.xent(H, W, t)
+    dH, dW = bl.xent_grad(H, W, t, lse, g)
+    for name, v in (("dH", dH), ("dW", dW)):
+        off = (v.double() - ref[name][0]).norm() / ref[name][0].norm()
+        assert off < 2.0 ** -8 / math.sqrt(3) + 2.0 ** -11, (name, float(off))

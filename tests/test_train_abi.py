@@ -74,3 +74,17 @@ def test_matrix_ops_refuse_the_training_types(bl):
     for dtype in (bl.BL_BF16, bl.BL_F16):
         assert lib.bl_potrf(0, dtype, 4, 1, F, 4, 16, F, None) == 1
     assert lib.bl_xent_workspace(1, 8, 16, 32, F, 16, F, 16, 0) == -1
+
+
+def test_the_tensor_binding_refuses_on_the_host(bl):
+    """Wrong types and CPU tensors raise before anything is allocated on a GPU."""
+    import torch
+    x, t = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)
+    for call in (lambda: bl.gnorm(3), lambda: bl.gnorm([1]), lambda: bl.gnorm([x.int()]), lambda: bl.gclip([x], "1"),
+                 lambda: bl.xent(x.double(), x.double(), t), lambda: bl.xent(x, None, t)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: bl.gnorm([x]), lambda: bl.gclip([x], 1.0), lambda: bl.xent(x, x, t),
+                 lambda: bl.xent_grad(x, x, t, x[0], x[0])):
+        with pytest.raises(ValueError):
+            call()
