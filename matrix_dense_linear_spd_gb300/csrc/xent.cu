@@ -13,7 +13,8 @@
 // included) reaches no result. How many they are is known on the device only; the products read it
 // there. Up to one tile of rows there is nothing to gain: rows keep their places, and the loss reads
 // H itself if TMA can. W is read in place if it is bf16 and its rows start on 16-byte boundaries;
-// otherwise each piece is copied (f32: as planes) before its products.
+// otherwise each piece is copied (f32: as planes) before its products. The loss of a few rows has a
+// kernel of its own (few_kernel), which reads H and W as they are.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,7 +36,8 @@ __device__ __forceinline__ bool has_target(const int64_t *target, int64_t row, i
 }
 
 // One block: the rows that count, in order; each row's place among them (-1: does not count); how
-// many they are, the parts of dH's K axis, and the unit of P (g: or null). The rows that do not count get the results they have (loss, lse: or null).
+// many they are, the parts of dH's K axis, and the unit of P (g: or null). The rows that do not count
+// get the results they have (loss, lse: or null).
 __global__ void __launch_bounds__(1024)
     index_kernel(const int64_t *target, int64_t vocab, int rows, int *order, int *place, int *kept, Cut cut,
                  const float *g, float *unit, float *loss, float *lse) {
