@@ -94,7 +94,12 @@ struct Ref {
 };
 
 PyObject *grads(PyObject *list, bool clip, double max_norm, PyObject *out, PyObject *stream) {
+    // Both lists are held to the end of the call: a generator's tensors may have no other owner, and the
+    // norm and the workspace must not be given their memory. Iterating over one may also run anything, the
+    // other list's own changes among it, so the items are looked at after that.
     Ref seq(PySequence_Fast(list, "a list of tensors is wanted"));
+    const bool given = clip && out != Py_None;
+    Ref outs(given ? PySequence_Fast(out, "out must be a list of tensors") : PyTuple_New(0));
     const int64_t n = PySequence_Fast_GET_SIZE(seq.o);
     PyObject **items = PySequence_Fast_ITEMS(seq.o);
     std::vector<int32_t> kinds(n + 1);
@@ -114,8 +119,7 @@ PyObject *grads(PyObject *list, bool clip, double max_norm, PyObject *out, PyObj
         x[i] = t.data_ptr();
         y[i] = t.data_ptr();
     }
-    if (clip && out != Py_None) {
-        Ref outs(PySequence_Fast(out, "out must be a list of tensors"));
+    if (given) {
         if (PySequence_Fast_GET_SIZE(outs.o) != n) refuse(PyExc_ValueError, "out must have as many tensors");
         for (int64_t i = 0; i < n; ++i) {
             const at::Tensor &t = THPVariable_Unpack(items[i]), &o = tensor(PySequence_Fast_GET_ITEM(outs.o, i), "every output");
