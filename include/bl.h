@@ -131,7 +131,8 @@ bl_status bl_gnorm(int64_t count, const int32_t *dtypes, const void *const *x, c
  * finite c is 1 as well: the caller sees it in `norm` and skips the step.
  *
  *   y         HOST array of device pointers to the results, of x's types and sizes. y[i] may be
- *             x[i] (in place; left untouched where c = 1) but overlaps no other input or output.
+ *             x[i] (in place; left untouched where c = 1) but overlaps no other input or output: such a
+ *             call (one tensor listed twice in place, say) is refused.
  *   max_norm  >= 0, infinity allowed (copies).
  *   norm      receives the norm BEFORE scaling. c is computed in f64 and rounded to f32 for f32,
  *             bf16 and f16 tensors, whose products are rounded once to their type.

@@ -274,8 +274,9 @@ def gnorm(tensors, stream=None):
 
 def gclip(tensors, max_norm, out=None, stream=None):
     """Scale the tensors to a global norm of at most max_norm, in place or into the tensors of
-    `out` (same types, shapes and strides). A norm that is not finite leaves the values as they
-    are. Returns the norm before scaling, a 0-dim f32 tensor."""
+    `out` (same types, shapes and strides). No result may overlap another tensor of the call (a
+    tensor that is listed twice in place is refused). A norm that is not finite leaves the values as
+    they are. Returns the norm before scaling, a 0-dim f32 tensor."""
     return (_binding or _training()).gclip(tensors, max_norm, out, _raw(stream))
 
 

@@ -30,6 +30,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <new>
+#include <vector>
 
 #include "host.h"
 #include "pdl.cuh"
@@ -329,13 +331,41 @@ bl_status check(const char *op, int64_t count, const int32_t *dtypes, const void
             return fail(BL_ERR_INVALID_ARGUMENT, "%s: tensor %lld is NULL or not aligned to its element", op, (long long)i);
         if (clip && (!y[i] || reinterpret_cast<uintptr_t>(y[i]) % es != 0))
             return fail(BL_ERR_INVALID_ARGUMENT, "%s: output %lld is NULL or not aligned to its element", op, (long long)i);
-        if (clip && x[i] != y[i]) {
-            const uintptr_t a = reinterpret_cast<uintptr_t>(x[i]), b = reinterpret_cast<uintptr_t>(y[i]);
-            const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * es;
-            if (a < b + bytes && b < a + bytes)
-                return fail(BL_ERR_INVALID_ARGUMENT, "%s: output %lld overlaps its input without being it", op, (long long)i);
-        }
     }
+    return BL_SUCCESS;
+}
+
+// Every result lies in memory of its own: it may be its input, but meets no other tensor of the call
+// (the same tensor listed twice in place would be scaled by two CTAs at once). Inputs that are only read
+// may meet one another. One walk over both lists in the order of addresses, in which most lists already are (the
+// refusal of 400 tensors whose last two meet, with all other checks: 3.7 us in place, 4.8 with outputs, 7.8 of
+// the host's time if they are in no order; 60 tensors 1.5 to 2).
+bl_status check_overlap(const char *op, int64_t count, const int32_t *dtypes, const void *const *x, void *const *y,
+                        const int64_t *sizes) {
+    const auto below = [](const Range &a, const Range &b) { return a.lo < b.lo; };
+    std::vector<Range> written, read;
+    written.reserve(count);
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const int64_t bytes = sizes[i] * host_bytes(dtypes[i]);
+        written.push_back(range_of(y[i], bytes));
+        if (x[i] != y[i]) read.push_back(range_of(x[i], bytes));
+    }
+    if (!std::is_sorted(written.begin(), written.end(), below)) std::sort(written.begin(), written.end(), below);
+    if (!std::is_sorted(read.begin(), read.end(), below)) std::sort(read.begin(), read.end(), below);
+    uintptr_t written_to = 0, read_to = 0;               // what has been passed ends there
+    size_t r = 0;
+    for (const Range &w : written) {
+        for (; r < read.size() && read[r].lo <= w.lo; ++r) {
+            if (read[r].lo < written_to) return fail(BL_ERR_INVALID_ARGUMENT, "%s: an output overlaps an input that it is not the result of", op);
+            read_to = std::max(read_to, read[r].hi);
+        }
+        if (w.lo < read_to) return fail(BL_ERR_INVALID_ARGUMENT, "%s: an output overlaps an input that it is not the result of", op);
+        if (w.lo < written_to) return fail(BL_ERR_INVALID_ARGUMENT, "%s: two outputs overlap", op);
+        written_to = w.hi;
+    }
+    if (r < read.size() && read[r].lo < written_to)
+        return fail(BL_ERR_INVALID_ARGUMENT, "%s: an output overlaps an input that it is not the result of", op);
     return BL_SUCCESS;
 }
 
@@ -407,7 +437,14 @@ cudaError_t run(int64_t count, const int32_t *dtypes, const void *const *x, void
 bl_status entry(const char *op, int64_t count, const int32_t *dtypes, const void *const *x, void *const *y, bool clip,
                 const int64_t *sizes, double max_norm, float *norm, void *ws, int64_t ws_bytes, bl_stream_t stream) {
     clear_error();
-    const bl_status st = check(op, count, dtypes, x, y, clip, sizes, max_norm, norm, ws, ws_bytes);
+    bl_status st = check(op, count, dtypes, x, y, clip, sizes, max_norm, norm, ws, ws_bytes);
+    if (st == BL_SUCCESS && clip) {
+        try {
+            st = check_overlap(op, count, dtypes, x, y, sizes);
+        } catch (const std::bad_alloc &) {
+            st = fail(BL_ERR_INTERNAL, "%s: out of host memory", op);
+        }
+    }
     if (st != BL_SUCCESS) return st;
     const int sms = sm_count();
     if (sms <= 0) return fail(BL_ERR_CUDA, "%s: cannot query the current CUDA device", op);

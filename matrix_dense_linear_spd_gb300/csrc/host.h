@@ -1,6 +1,8 @@
 // Host-side helpers shared by the C entry points.
 #pragma once
 
+#include <cstdint>
+
 #include "../../include/bl.h"
 
 namespace bl {
@@ -11,5 +13,14 @@ bl_status fail(bl_status st, const char *fmt, ...);
 void clear_error();
 // SMs of the current device (cached per device); 0 if it cannot be queried.
 int sm_count();
+
+// Bytes [lo, hi) of memory that a call reads or writes.
+struct Range {
+    uintptr_t lo, hi;
+};
+inline Range range_of(const void *p, int64_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return {a, a + static_cast<uintptr_t>(bytes)};
+}
 
 }  // namespace bl
