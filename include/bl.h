@@ -158,7 +158,7 @@ int64_t bl_gnorm_workspace(int64_t count);
  *             where W and its columns start on 16-byte boundaries, and copied otherwise.
  *   target    device int64[rows]. A target outside [0, vocab) marks a row that does not count: its
  *             loss and lse are 0 and its column of H, whatever it holds, reaches no result.
- *   loss, lse device float[rows].
+ *   loss, lse device float[rows]; they overlap nothing else of the call.
  *   workspace device memory of at least bl_xent_workspace(..., grad = 0) bytes, 256-byte aligned,
  *             free again once the call's work has completed on the stream.
  * The same call gives the same bits every time. A kernel that gave up waiting for an asynchronous
@@ -176,7 +176,8 @@ bl_status bl_xent(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, cons
  *   g         device float[rows]: the gradient of what is minimised with respect to each row's
  *             loss (1/rows for a mean). Not looked at where a row does not count.
  *   dH, dW    the gradients, laid out as H and W (lddh, lddw >= dim), overwritten. Either may be
- *             NULL: that product is skipped. They overlap no input.
+ *             NULL: that product is skipped. They overlap no input and not each other (a call where they
+ *             do is refused; rows that lie in the gaps of another matrix's rows do not overlap it).
  *   workspace at least bl_xent_workspace(..., grad = 1) bytes.
  * P is formed piece by piece of the vocabulary, in units of the largest |g| of a row that counts, and
  * rounded to bf16 for bf16 operands (relative 2^-8 an element, as the gradients themselves are);

@@ -289,5 +289,6 @@ def xent(H, W, target, stream=None):
 
 def xent_grad(H, W, target, lse, g, dH=None, dW=None, stream=None):
     """Gradients of sum_r g_r loss_r: (dH, dW) in H's and W's type, given xent's lse. dH and dW
-    may be tensors to write to; False leaves that gradient out (None is returned for it)."""
+    may be tensors to write to, which overlap no other tensor of the call; False leaves that
+    gradient out (None is returned for it)."""
     return (_binding or _training()).xent_grad(H, W, target, lse, g, dH, dW, _raw(stream))

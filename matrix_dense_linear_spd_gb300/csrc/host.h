@@ -22,5 +22,6 @@ inline Range range_of(const void *p, int64_t bytes) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     return {a, a + static_cast<uintptr_t>(bytes)};
 }
+inline bool meet(const Range &a, const Range &b) { return a.lo < b.hi && b.lo < a.hi; }
 
 }  // namespace bl

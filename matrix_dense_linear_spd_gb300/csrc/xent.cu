@@ -836,6 +836,46 @@ bl_status check_matrix(const char *op, const char *name, const void *p, int64_t 
     return BL_SUCCESS;
 }
 
+// The bytes of rows of `dim` values, ld apart, that a matrix consists of.
+struct Rows {
+    uintptr_t at;
+    uintptr_t step, length;
+    int64_t rows;
+    Range all() const { return {at, at + static_cast<uintptr_t>(rows - 1) * step + length}; }
+};
+Rows rows_at(const void *p, int64_t rows, int64_t dim, int64_t ld, int64_t es) {
+    return {reinterpret_cast<uintptr_t>(p), static_cast<uintptr_t>(ld * es), static_cast<uintptr_t>(dim * es), rows};
+}
+// Whether two matrices share a byte. One may lie in the gaps of the other: as another column range of one
+// buffer, or in some other way, for which every row of the shorter one is looked up.
+bool meet(const Rows &a, const Rows &b) {
+    if (!bl::meet(a.all(), b.all())) return false;
+    if (a.rows > b.rows) return meet(b, a);
+    if (a.step == b.step && a.rows > 1) {
+        const uintptr_t d = (b.at - a.at + (a.at > b.at ? (a.at - b.at + a.step - 1) / a.step * a.step : 0)) % a.step;
+        if (d >= a.length && d + b.length <= a.step) return false;
+    }
+    for (int64_t r = 0; r < a.rows; ++r) {
+        const uintptr_t lo = a.at + static_cast<uintptr_t>(r) * a.step, hi = lo + a.length;
+        // the first row of b that ends past lo
+        const uintptr_t j = b.at + b.length > lo ? 0 : (lo - b.at - b.length) / b.step + 1;
+        if (j < static_cast<uintptr_t>(b.rows) && b.at + j * b.step < hi) return true;
+    }
+    return false;
+}
+struct Named {
+    const char *name;
+    Rows rows;
+};
+// No result overlaps another tensor of the call. The first `written` of the list are results or scratch.
+bl_status check_apart(const char *op, const Named *t, int written, int count) {
+    for (int i = 0; i < written; ++i)
+        for (int j = i + 1; j < count; ++j)
+            if (t[i].rows.at && t[j].rows.at && meet(t[i].rows, t[j].rows))
+                return fail(BL_ERR_INVALID_ARGUMENT, "%s: %s overlaps %s", op, t[i].name, t[j].name);
+    return BL_SUCCESS;
+}
+
 bl_status check_vector(const char *op, const char *name, const void *p, int align) {
     if (!p || reinterpret_cast<uintptr_t>(p) % align != 0)
         return fail(BL_ERR_INVALID_ARGUMENT, "%s: %s is NULL or not %d-byte aligned", op, name, align);
@@ -866,6 +906,18 @@ bl_status entry(const char *op, int dtype, Call &c, bool grad, void *ws, int64_t
     if (ws_bytes < q.bytes)
         return fail(BL_ERR_INVALID_ARGUMENT, "%s: workspace of %lld bytes is smaller than %lld", op, (long long)ws_bytes,
                     (long long)q.bytes);
+    const auto vector = [&](const void *p, int64_t bytes) { return rows_at(p, 1, bytes, bytes, 1); };
+    const int64_t es = dtype == BL_F32 ? 4 : 2;
+    Named all[8] = {{"dH", rows_at(c.dH, c.rows, c.dim, c.lddh, es)}, {"dW", rows_at(c.dW, c.vocab, c.dim, c.lddw, es)},
+                    {"the workspace", vector(ws, q.bytes)},           {"H", rows_at(c.H, c.rows, c.dim, c.ldh, es)},
+                    {"W", rows_at(c.W, c.vocab, c.dim, c.ldw, es)},   {"target", vector(c.target, c.rows * 8)},
+                    {"lse", vector(c.lse_in, c.rows * 4)},            {"g", vector(c.g, c.rows * 4)}};
+    if (!grad) {
+        all[0] = {"loss", vector(c.loss, c.rows * 4)};
+        all[1] = {"lse", vector(c.lse, c.rows * 4)};
+    }
+    st = check_apart(op, all, 3, grad ? 8 : 6);
+    if (st != BL_SUCCESS) return st;
     c.ws = static_cast<char *>(ws);
     c.s = reinterpret_cast<cudaStream_t>(stream);
     return dtype == BL_F32 ? run<float, 3>(op, q, c) : run<__nv_bfloat16, 1>(op, q, c);
