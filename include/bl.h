@@ -162,7 +162,8 @@ int64_t bl_gnorm_workspace(int64_t count);
  *   workspace device memory of at least bl_xent_workspace(..., grad = 0) bytes, 256-byte aligned,
  *             free again once the call's work has completed on the stream.
  * The same call gives the same bits every time. A kernel that gave up waiting for an asynchronous
- * copy or product (a device fault, not a numerical result) makes every loss NaN.
+ * copy or product (a device fault, not a numerical result) makes the loss and lse of every row that
+ * counts NaN.
  */
 bl_status bl_xent(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
                   const void *W, int64_t ldw, const int64_t *target, float *loss, float *lse,
@@ -182,7 +183,7 @@ bl_status bl_xent(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, cons
  * P is formed piece by piece of the vocabulary, in units of the largest |g| of a row that counts, and
  * rounded to bf16 for bf16 operands (relative 2^-8 an element, as the gradients themselves are);
  * f32 operands keep it in f32.
- * A kernel that gave up waiting makes dH NaN; dW is undefined then. Other arguments as bl_xent.
+ * A kernel that gave up waiting makes all of dH and dW NaN. Other arguments as bl_xent.
  */
 bl_status bl_xent_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
                        const void *W, int64_t ldw, const int64_t *target, const float *lse, const float *g,
@@ -251,6 +252,13 @@ const char *bl_select_debug(int op, bl_dtype dtype, bl_uplo uplo, int64_t n, int
  */
 bl_status bl_debug_tc_tile_f32(const float *A, const float *B, float *C, int32_t *status,
                                bl_stream_t stream);
+
+/*
+ * Diagnostic: with on != 0 the calling thread's bl_xent and bl_xent_grad report, from then on, that
+ * one of their matrix products gave up waiting, although none did: what a caller sees of it can be
+ * tested. on = 0 ends that. (bl_xent's kernel for few rows waits for nothing and reports nothing.)
+ */
+bl_status bl_debug_xent_gave_up(int on);
 
 /*
  * Diagnostic: arithmetic-peak microbenchmarks, so that roofline fractions can be taken against

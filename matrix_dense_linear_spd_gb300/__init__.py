@@ -26,7 +26,7 @@ STATUS = {0: "success", 1: "invalid argument", 2: "no route", 3: "CUDA error", 4
 EXPORTED = ("bl_potrf", "bl_posv", "bl_potrs", "bl_status_string", "bl_last_error", "bl_last_choice",
             "bl_version", "bl_set_route", "bl_num_routes", "bl_route_name", "bl_route_capacity",
             "bl_select_debug", "bl_debug_tc_tile_f32", "bl_debug_peak", "bl_gnorm", "bl_gclip",
-            "bl_gnorm_workspace", "bl_xent", "bl_xent_grad", "bl_xent_workspace")
+            "bl_gnorm_workspace", "bl_xent", "bl_xent_grad", "bl_xent_workspace", "bl_debug_xent_gave_up")
 
 
 class BLError(RuntimeError):
@@ -77,6 +77,8 @@ def _load():
     lib.bl_xent.restype = ctypes.c_int
     lib.bl_xent_grad.argtypes = [ctypes.c_int, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp]
     lib.bl_xent_grad.restype = ctypes.c_int
+    lib.bl_debug_xent_gave_up.argtypes = [ctypes.c_int]
+    lib.bl_debug_xent_gave_up.restype = ctypes.c_int
     lib.bl_xent_workspace.argtypes = [ctypes.c_int, i64, i64, i64, vp, i64, vp, i64, ctypes.c_int]
     lib.bl_xent_workspace.restype = i64
     return lib

@@ -332,18 +332,39 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
 }
 
+// What the gradient writes where a product gave up: NaN over all of dW (dw null: none is wanted).
+template <typename T>
+struct Spoiled {
+    T *dw;
+    int64_t ld, rows;
+    int dim;
+    __device__ void fill() const {
+        if (!dw) return;
+        for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+            for (int c = threadIdx.x; c < dim; c += blockDim.x) put(dw + r * ld + c, NAN);
+    }
+};
+// The last kernel of a gradient without dH: all that is left to do is to look at the flags.
+template <typename T>
+__global__ void __launch_bounds__(256) spoil_kernel(const int32_t *flags, int flag_count, const Spoiled<T> dw) {
+    pdl_release();
+    pdl_wait();
+    if (__syncthreads_or(flags_seen(flags, flag_count))) dw.fill();
+}
+
 // dH from the parts' sums, four columns a thread, times the unit of P; rows without a target are zero. A product that
-// gave up makes it NaN. With SHARE = 8 eight lanes of a warp add every eighth part each (many parts
+// gave up makes it NaN, and dW. With SHARE = 8 eight lanes of a warp add every eighth part each (many parts
 // mean few results: 64 rows x 1024 in 38 parts took 14 us with one thread a result).
 template <typename T, int SHARE>
 __global__ void __launch_bounds__(256)
     dh_kernel(const float *part, int all_parts, int64_t rows, int64_t ldo, int dim, const int64_t *target, int64_t vocab,
               const int *place, const int *kept_rows, const float *unit_of_p, const int32_t *flags, int flag_count,
-              T *dh, int64_t ld, int vec) {
+              T *dh, int64_t ld, int vec, const Spoiled<T> dw) {
     constexpr int SIDE = 32 / SHARE;                // results that a warp works on at once
     pdl_release();
     pdl_wait();
     const bool bad = __syncthreads_or(flags_seen(flags, flag_count)) != 0;
+    if (bad) dw.fill();
     const int kept = kept_rows ? kept_rows[0] : static_cast<int>(rows), splits = kept_rows ? kept_rows[1] : all_parts;
     const float unit = *unit_of_p;
     const int64_t height = part_rows(kept), part_step = SHARE * height * (ldo / 4);
@@ -635,6 +656,8 @@ Copy copy_of(const void *src, int64_t ld, int64_t rows, int64_t dim, const int64
     return w;
 }
 
+thread_local bool t_gave_up = false;       // bl_debug_xent_gave_up
+
 struct Call {
     int64_t rows, dim, vocab;
     const void *H;
@@ -797,6 +820,8 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             BL_TRY((launch_gemm<DW, PLANES>(p_mn, h_mn, to, d, q.ctas, flag_count, c.sms, c.s)));
         }
     }
+    if (t_gave_up) BL_TRY(cudaMemsetAsync(flags, 1, 4, c.s));
+    const Spoiled<T> spoiled{static_cast<T *>(c.dW), c.lddw, c.vocab, dim};
     if (!q.grad) {
         BL_TRY(launch_pdl(loss_kernel, static_cast<unsigned>(cdiv(c.rows, 8)), 256, 0, c.s,
                           reinterpret_cast<const float2 *>(c.ws + q.part), q.part_ld, reinterpret_cast<const float *>(c.ws + q.picked),
@@ -808,7 +833,9 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         const int vec = reinterpret_cast<uintptr_t>(c.dH) % (4 * es) == 0 && c.lddh % 4 == 0;
         BL_TRY(launch_pdl(share == 8 ? dh_kernel<T, 8> : dh_kernel<T, 1>, static_cast<unsigned>(blocks), 256, 0, c.s,
                           reinterpret_cast<const float *>(c.ws + q.dh), q.parts, c.rows, q.ldo, dim, c.target, c.vocab, place, kept, unit,
-                          flags, flag_count, static_cast<T *>(c.dH), c.lddh, vec));
+                          flags, flag_count, static_cast<T *>(c.dH), c.lddh, vec, spoiled));
+    } else {
+        BL_TRY(launch_pdl(spoil_kernel<T>, static_cast<unsigned>(c.sms), 256, 0, c.s, flags, flag_count, spoiled));
     }
     return BL_SUCCESS;
 }
@@ -961,6 +988,12 @@ bl_status bl_xent_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab,
     c.lse_in = lse, c.g = g;
     c.dH = dH, c.lddh = lddh, c.dW = dW, c.lddw = lddw;
     return bl::xent::entry("xent_grad", dtype, c, true, workspace, workspace_bytes, stream);
+}
+
+bl_status bl_debug_xent_gave_up(int on) {
+    bl::clear_error();
+    bl::xent::t_gave_up = on != 0;
+    return BL_SUCCESS;
 }
 
 }  // extern "C"
