@@ -235,7 +235,7 @@ struct Row {              // what an epilogue keeps of its row
     int part_rows;        // DH
     bool counted;
     float top, sum, picked;    // LOGITS
-    float lse, ref, g;         // PROBS
+    float lse, g;              // PROBS
     float unit;                // PROBS, DW
 };
 
@@ -255,7 +255,6 @@ __device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s,
         if constexpr (MODE == PROBS) {
             r.lse = r.counted ? a.lse[src] : 0.f;
             r.g = r.counted ? a.g[src] / r.unit : 0.f;
-            r.ref = r.lse * kLog2e;
         }
     }
 }
@@ -274,10 +273,12 @@ __device__ __forceinline__ void block_logits(Row &r, const GemmArgs &a, const Wo
         if (hit >> i & 1) r.picked = v[i];
         m = fmaxf(m, v[i]);
     }
-    const float ref = m == -INFINITY ? 0.f : m * kLog2e;      // a row of -inf: every term is 0
-    r.sum *= exp2f(fmaf(r.top, kLog2e, -ref));
+    // The difference comes before the product: m * log2(e) overflows for logits near the type's lowest value
+    // (a mask), and its rounding would move the sum by |m| 2^-24 against the exp(m) that it stands beside.
+    const float ref = m == -INFINITY ? 0.f : m;               // a row of -inf: every term is 0
+    r.sum *= exp2f((r.top - ref) * kLog2e);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) r.sum += exp2f(fmaf(v[i], kLog2e, -ref));
+    for (int i = 0; i < 32; ++i) r.sum += exp2f((v[i] - ref) * kLog2e);
     r.top = m;
 }
 
@@ -348,9 +349,8 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
     if constexpr (MODE == PROBS) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            // the f32 form keeps s - lse exact where it can; the bf16 form rounds the result to 8
-            // bits anyway
-            float e = PLANES == 1 ? exp2f(fmaf(v[i], kLog2e, -r.ref)) : expf(v[i] - r.lse);
+            // the difference first, as in block_logits; the bf16 form rounds the result to 8 bits anyway
+            float e = PLANES == 1 ? exp2f((v[i] - r.lse) * kLog2e) : expf(v[i] - r.lse);
             if (i == r.at - c0) e -= 1.f;
             v[i] = r.counted && n0 + c0 + i < a.n ? r.g * e : 0.f;      // panels are whole: zero to their end
         }
