@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(256)
         for (int64_t i = lane + 32 * HELD; i < part_ld; i += 32) sum += p[i].y * expf(p[i].x - ref);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        // not s - chosen: s has been rounded, by up to |s| 2^-24, and a sure row's loss is less than that. Both
+        // terms are exact or small, and neither is negative.
         s = ref + logf(sum);
-        l = s - chosen;
+        l = (ref - chosen) + logf(sum);
     }
     if (bad) l = s = NAN;
     if (lane == 0) {

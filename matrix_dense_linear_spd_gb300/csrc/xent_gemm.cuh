@@ -278,7 +278,13 @@ __device__ __forceinline__ void block_logits(Row &r, const GemmArgs &a, const Wo
     const float ref = m == -INFINITY ? 0.f : m;               // a row of -inf: every term is 0
     r.sum *= exp2f((r.top - ref) * kLog2e);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) r.sum += exp2f((v[i] - ref) * kLog2e);
+    for (int i = 0; i < 32; ++i) v[i] = exp2f((v[i] - ref) * kLog2e);
+    // pairwise: beside a sure row's 1 each addition may round 2^-24 of its loss away
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) v[i] += v[i + o];
+    r.sum += v[0];
     r.top = m;
 }
 

@@ -48,3 +48,28 @@ def test_masked_entries_have_no_share(kind, rows, value, sign):
         check(dH[:, :-1], {"dH": [x[:, :-1] for x in ref["dH"]]}, "dH")
         if value == "lowest":
             assert bool((dH[:, -1] == 0).all()), name
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 100, 300])
+def test_a_mask_that_leaves_nothing(kind, rows):
+    """Every entry at the lowest value: they share the row evenly, so the loss is log(vocab), within f32's rounding
+    of the sum and the logarithm; lse is the lowest value to f32's precision. With minus infinity there
+    is no softmax: NaN. Either way other rows are as they are without it."""
+    torch, bl = torch_cuda(), lib()
+    H, W, t, g = make(rows, 64, VOCAB, kind, seed=1)
+    H[:, -1] = 0
+    H[0] = 0
+    H[0, -1] = 1
+    low = torch.finfo(W.dtype).min
+    W[:, -1] = low
+    loss, lse = bl.xent(H, W, t)
+    assert abs(float(loss[0]) / math.log(VOCAB) - 1) < 2.0 ** -18
+    assert abs(float(lse[0]) / low - 1) < 2.0 ** -22
+    if rows > 1:
+        rest = reference(H[1:], torch.cat([W[:, :-1], torch.zeros_like(W[:, :1])], 1), t[1:], g[1:], kind)
+        check(loss[1:], rest, "loss")
+        check(lse[1:], rest, "lse")
+    W[:, -1] = -math.inf
+    H[1:, -1] = 1
+    assert bool(bl.xent(H, W, t)[0].isnan().all())
