@@ -159,6 +159,8 @@ int64_t bl_gnorm_workspace(int64_t count);
  *   target    device int64[rows]. A target outside [0, vocab) marks a row that does not count: its
  *             loss and lse are 0 and its column of H, whatever it holds, reaches no result.
  *   loss, lse device float[rows]; they overlap nothing else of the call.
+ *             A logit of minus infinity has no share in its row (a mask; the type's lowest value does as
+ *             well); one of plus infinity or NaN, or a row with minus infinity only, gives NaN.
  *   workspace device memory of at least bl_xent_workspace(..., grad = 0) bytes, 256-byte aligned,
  *             free again once the call's work has completed on the stream.
  * The same call gives the same bits every time. A kernel that gave up waiting for an asynchronous

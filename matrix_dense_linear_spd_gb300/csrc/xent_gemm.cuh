@@ -199,15 +199,16 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&t);
 }
 
-// x = x0 + x1 + x2 in bf16. A value that rounds past the largest bf16 is cut instead; what is
-// not finite stays in x0 alone.
+// x = x0 + x1 + x2 in bf16. A value that rounds past the largest bf16 is cut instead. NaN stays in x0
+// alone. An infinity is its sign in x0 and itself in x2, the plane that meets the other operand's x0 only: in
+// x0 it would meet that operand's x1 and x2 as well, which are mostly zero, and 0 * inf is NaN.
 __device__ __forceinline__ void split3(float x, float &x0, float &x1, float &x2) {
+    const bool fine = fabsf(x) <= 3.4028235e38f, infinite = isinf(x);
     x0 = __bfloat162float(__float2bfloat16_rn(x));
-    if (isinf(x0) && !isinf(x)) x0 = __bfloat162float(__float2bfloat16_rz(x));
+    if (isinf(x0)) x0 = infinite ? copysignf(1.f, x) : __bfloat162float(__float2bfloat16_rz(x));
     const float r = x - x0;
-    const bool fine = fabsf(x) <= 3.4028235e38f;
     x1 = fine ? __bfloat162float(__float2bfloat16_rn(r)) : 0.f;
-    x2 = fine ? __bfloat162float(__float2bfloat16_rn(r - x1)) : 0.f;
+    x2 = fine ? __bfloat162float(__float2bfloat16_rn(r - x1)) : infinite ? x : 0.f;
 }
 
 // P is kept in units of the largest |g| of a row that counts, and dH and dW are multiplied by it in f32

@@ -25,7 +25,7 @@ def masks(torch):
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", [1, 8, 100, 300])
-@pytest.mark.parametrize("value", ["lowest"])
+@pytest.mark.parametrize("value", ["lowest", "-inf"])
 @pytest.mark.parametrize("sign", [1, -1])
 def test_masked_entries_have_no_share(kind, rows, value, sign):
     torch, bl = torch_cuda(), lib()
