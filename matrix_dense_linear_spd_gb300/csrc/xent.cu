@@ -411,8 +411,10 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ plan
 
-// K is added in tensor memory over so many 64-deep steps at a time where the result is f32
-constexpr int kChunkF32 = 2, kChunkLoss = 16, kWhole = 1 << 30;
+// K is added in tensor memory over so many 64-deep steps at a time where the result is f32: f32 operands, the
+// logits of bf16 operands, and those of P where the loss of few rows has added them in f32 (W's way from memory
+// hides it: step of 1 row x 4096 x 32000 216 us, 212 with the chain uncut)
+constexpr int kChunkF32 = 2, kChunkLoss = 16, kChunkFew = 1, kWhole = 1 << 30;
 // Bytes of P, and of a piece's copy of W, that a piece of the vocabulary may take. Steps of 4096 x 4096 x
 // 131072 in bf16 and 1024 x 1024 x 32000 in f32 at 64, 128, 512 and 2048 MB: 11.04, 10.84, 10.66, 10.65 ms
 // and 1.22, 1.13, 1.04, 1.04 ms
@@ -427,6 +429,7 @@ struct Plan {
     int groups;               // CTAs or pairs that the device's SMs hold
     bool copy_h, copy_w, compact, grad;
     int few;                  // rows of the kernel for few rows (0: the tiled products)
+    bool few_loss;            // the gradient's lse comes from that kernel
     int64_t rows, dim, vocab;
     int64_t tiled;            // rows of the copy of H and of P: whole tiles
     int64_t seen;             // of them, those that tensor maps see: the rest reads as zero without being read
@@ -498,8 +501,10 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
         if (t == q.wide || cost < least) q.tile_n = t, least = cost;
     }
     q.part_ld = 2 * cdiv(vocab, q.tile_n);
+    const int few = few_rows(dtype, rows, dim, W, ldw);
+    q.few_loss = grad && few;
     if (!grad) {
-        q.few = few_rows(dtype, rows, dim, W, ldw);
+        q.few = few;
         if (q.few) {
             q.part_ld = std::min<int64_t>(cdiv(vocab, 8 * few_entries(q.few)), static_cast<int64_t>(sms) * few_ctas(q.few));
             q.copy_h = q.copy_w = false;
@@ -766,8 +771,8 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         a.v0 = static_cast<int>(v0);
         a.ca = cols_h;
         a.cb = cols_w;
+        if (PLANES == 1) a.chunk = q.few_loss ? kChunkFew : kChunkLoss;
         if (!q.grad) {
-            if (PLANES == 1) a.chunk = kChunkLoss;
             a.part = reinterpret_cast<float2 *>(c.ws + q.part) + 2 * (v0 / q.tile_n);
             a.part_ld = q.part_ld;
             a.picked = reinterpret_cast<float *>(c.ws + q.picked);

@@ -17,8 +17,10 @@
 // smallest first. That costs as much tensor time as three tf32 products and is closer to f32.
 //
 // The tensor cores' f32 accumulation cuts where f32 would round, so a long chain of products is
-// biased towards zero, by about 2^-25 of the sum a step. Where the result is f32 (the loss; every
-// product of f32 operands) the chain is cut into chunks of K, whose sums are added in registers.
+// biased towards zero, by about 2^-25 of the sum a step. Where the result is f32 (the logits; every
+// product of f32 operands) the chain is cut into chunks of K, whose sums are added in registers. The loss and P
+// cut theirs alike, so that both form the same logits: exp(s - lse) - 1 at the target of a row that is sure of it
+// shows every difference (dim 4096, logits of 57, p = 0.9999: with P's chain uncut several times P's size).
 // Measured at rows 1024, dim 1024, vocabulary 32000, f32: dH 9.6e-6 off without chunks, 4.2e-7 with
 // chunks of 128 (9.2e-7 with 256, 2.5% faster); the bf16 loss of 4096 x 4096 x 16384 with chunks of 512,
 // 1024, 2048 and none: 317, 301, 294, 291 us.
@@ -356,7 +358,8 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
     if constexpr (MODE == PROBS) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            // the difference first, as in block_logits; the bf16 form rounds the result to 8 bits anyway
+            // the difference first, as in block_logits; the bf16 form rounds the result to 8 bits anyway. What the
+            // exponential is off by where it is near 1 (2^-22) is no more than what lse's own rounding leaves.
             float e = PLANES == 1 ? exp2f((v[i] - r.lse) * kLog2e) : expf(v[i] - r.lse);
             if (i == r.at - c0) e -= 1.f;
             v[i] = r.counted && n0 + c0 + i < a.n ? r.g * e : 0.f;      // panels are whole: zero to their end
@@ -421,7 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     using R = Ring<CTAS, PLANES>;
     constexpr int kBytesA = R::kBytesA, kBytesB = R::kBytesB, kStageA = R::kStageA, kStageB = R::kStageB, kStages = R::kStages;
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DH || MODE == DW;
-    constexpr bool SUMS = MODE == LOGITS || PLANES == 3;      // chunks are added in registers
+    // Chunks of K are added in registers (SUMS). Where one chunk is all there is, the bf16 results go out block by
+    // block as they leave tensor memory instead (DIRECT).
+    constexpr bool SUMS = MODE == LOGITS || MODE == PROBS || PLANES == 3, DIRECT = MODE != LOGITS && PLANES == 1;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kStageA;
@@ -588,8 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             Row r;
             r.unit = unit;
             begin<MODE>(r, a, sh, k, (k.tm * CTAS + rank) * kTileM + quad * 32 + lane);
+            const bool direct = DIRECT && (!SUMS || k.kb1 - k.kb0 <= a.chunk);
             float v[SUMS ? kHalf / 32 : 1][32];
-            if constexpr (SUMS) {
+            if (SUMS && !direct) {
 #pragma unroll
                 for (int b = 0; b < kHalf / 32; ++b)
 #pragma unroll
@@ -601,7 +607,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc::fence_after_sync();
                 const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
-                if constexpr (SUMS) {
+                if (direct) {
+                    if constexpr (DIRECT) {
+#pragma unroll 1
+                        for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
+                            __syncwarp();
+                            tc::tmem_ld32(acc + c0, v[0]);
+                            block<MODE, PLANES>(r, a, k, c0, cols, v[0], &map_out, stage);
+                        }
+                    }
+                } else if constexpr (SUMS) {
 #pragma unroll
                     for (int b = 0; b < kHalf / 32; ++b) {
                         const int c0 = half * kHalf + 32 * b;
@@ -611,13 +626,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[b][i] += x[i];
                         }
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
-                        __syncwarp();
-                        tc::tmem_ld32(acc + c0, v[0]);
-                        block<MODE, PLANES>(r, a, k, c0, cols, v[0], &map_out, stage);
                     }
                 }
                 __syncwarp();
@@ -632,11 +640,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) gave_up = 1;
                 break;
             }
-            if constexpr (SUMS) {
+            if (SUMS && !direct) {
+                // One copy of the code for the four blocks, whose sums move up: a CTA with one tile fetches it
+                // once, and fetching is what four copies cost (P of 64 rows x 2048 x 32000 32 us instead of
+                // 28, the loss of 64 rows x 1024 x 32000 17.7 us instead of 17.0)
+#pragma unroll 1
+                for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
+                    block<MODE, PLANES>(r, a, k, c0, cols, v[0], &map_out, stage);
 #pragma unroll
-                for (int b = 0; b < kHalf / 32; ++b)
-                    if (half * kHalf + 32 * b < cols)
-                        block<MODE, PLANES>(r, a, k, half * kHalf + 32 * b, cols, v[b], &map_out, stage);
+                    for (int b = 0; b + 1 < (SUMS ? kHalf / 32 : 1); ++b)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[b][i] = v[b + 1][i];
+                }
                 __syncwarp();
             }
             end<MODE>(r, a, k, half);

@@ -60,3 +60,37 @@ def test_loss_of_sure_rows(kind, rows, level):
     assert float(want.median()) < 1e-2 and bool((loss >= 0).all())
     assert bool(((loss.double() - want).abs() <= want * (2 * ds).expm1() + 2.0 ** -18 * want + 4 * U).all())
     assert bool(((lse.double() - (want + s[range(rows), t])).abs() <= ds + 2 * U * (1 + lse.abs())).all())
+
+
+@pytest.mark.parametrize("kind,rows,dim,level", [("bf16", 1, 4096, 20.0), ("bf16", 100, 4096, 40.0), ("bf16", 300, 4096, 40.0),
+                                                 ("bf16", 300, 16384, 40.0), ("f32", 1, 4096, 40.0), ("f32", 100, 4096, 40.0),
+                                                 ("f32", 300, 4096, 40.0)])
+def test_gradient_of_sure_rows(kind, rows, dim, level):
+    """P at the target is g (p - 1), p within 1e-2 of 1. Loss and gradient form the same logits, so ds moves p - 1 by
+    (1 - p) expm1(2 ds) only; what is left of s - lse is lse's rounding, d = u |lse| + 2^-21, and, where
+    the loss of few rows has been summed by another kernel, both kernels' sums: 16 u sum |HW| at most. Elsewhere |dP| <= g p
+    expm1(2 ds + d). Then P's own rounding, dW's sum and dW's rounding."""
+    torch, bl = torch_cuda(), lib()
+    vocab = 2000
+    H, W, t, g = sure_rows(rows, dim, vocab, kind, level, 17.0, seed=dim + rows)
+    s, loss, ds = exact(H, W, t)
+    assert 1e-6 < float(loss.median()) < 1e-2
+    h, w, gd, at = H.double(), W.double(), g.double(), (range(rows), t)
+    lse_exact = s[at] + loss
+    d = U * lse_exact.abs() + 2.0 ** -21
+    if rows <= 8:
+        d = d + 16 * U * (h.abs() @ w.abs().T).amax(1)
+    p = (s - lse_exact[:, None]).exp()
+    P, e_p = p.clone(), p * (2 * ds + d)[:, None].expm1()
+    P[at] = (-loss).expm1()
+    e_p[at] = -P[at] * (2 * ds).expm1() + d
+    P, e_p = P * gd[:, None], e_p * gd[:, None]
+    u_p = 2.0 ** -8 if kind == "bf16" else 2.0 ** -20
+    e_p = e_p + u_p * P.abs()
+    want = P.T @ h
+    bound = e_p.T @ h.abs() + (rows + 8) * 2 * U * (P.abs().T @ h.abs()) + u_p * want.abs()
+    _, lse = bl.xent(H, W, t)
+    dH, dW = bl.xent_grad(H, W, t, lse, g)
+    over = (dW.double() - want).abs() - bound
+    worst = (dW.double() - want)[t].norm() / want[t].norm()
+    assert float(over.amax()) <= 0, f"targets' rows of dW are {float(worst):.2e} off"
