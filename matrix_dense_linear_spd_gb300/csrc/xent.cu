@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(256)
 
 // K is added in tensor memory over so many 64-deep steps at a time where the result is f32: f32 operands, the
 // logits of bf16 operands, and those of P where the loss of few rows has added them in f32 (W's way from memory
-// hides it: step of 1 row x 4096 x 32000 216 us, 212 with the chain uncut)
-constexpr int kChunkF32 = 2, kChunkLoss = 16, kChunkFew = 1, kWhole = 1 << 30;
+// hides it: step of 1 row x 4096 x 32000 216 us, 212 with the chain uncut). bf16 results, dH and dW, have long chunks.
+constexpr int kChunkF32 = 2, kChunkLoss = 16, kChunkFew = 1, kChunkBf16 = 256;
 // Bytes of P, and of a piece's copy of W, that a piece of the vocabulary may take. Steps of 4096 x 4096 x
 // 131072 in bf16 and 1024 x 1024 x 32000 in f32 at 64, 128, 512 and 2048 MB: 11.04, 10.84, 10.66, 10.65 ms
 // and 1.22, 1.13, 1.04, 1.04 ms
@@ -739,7 +739,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     base.kept = kept;
     base.order = order;
     base.flags = flags;
-    base.chunk = PLANES == 3 ? kChunkF32 : kWhole;
+    base.chunk = PLANES == 3 ? kChunkF32 : kChunkBf16;
     base.target = c.target;
     base.vocab = c.vocab;
     base.g = c.g;

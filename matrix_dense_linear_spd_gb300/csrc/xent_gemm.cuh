@@ -17,10 +17,12 @@
 // smallest first. That costs as much tensor time as three tf32 products and is closer to f32.
 //
 // The tensor cores' f32 accumulation cuts where f32 would round, so a long chain of products is
-// biased towards zero, by about 2^-25 of the sum a step. Where the result is f32 (the logits; every
+// biased towards zero: by about 2^-25 of the sum a step in these products, by up to 2^-23.4 where all terms have one
+// sign (dW over 2^21 equal rows in one chain: 1.2e-2 low). Where the result is f32 (the logits; every
 // product of f32 operands) the chain is cut into chunks of K, whose sums are added in registers. The loss and P
 // cut theirs alike, so that both form the same logits: exp(s - lse) - 1 at the target of a row that is sure of it
 // shows every difference (dim 4096, logits of 57, p = 0.9999: with P's chain uncut several times P's size).
+// bf16 results are cut every 16384 of K, 1e-4 of the sum at most, where their own rounding is 4e-3.
 // Measured at rows 1024, dim 1024, vocabulary 32000, f32: dH 9.6e-6 off without chunks, 4.2e-7 with
 // chunks of 128 (9.2e-7 with 256, 2.5% faster); the bf16 loss of 4096 x 4096 x 16384 with chunks of 512,
 // 1024, 2048 and none: 317, 301, 294, 291 us.
@@ -424,9 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     using R = Ring<CTAS, PLANES>;
     constexpr int kBytesA = R::kBytesA, kBytesB = R::kBytesB, kStageA = R::kStageA, kStageB = R::kStageB, kStages = R::kStages;
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DH || MODE == DW;
-    // Chunks of K are added in registers (SUMS). Where one chunk is all there is, the bf16 results go out block by
-    // block as they leave tensor memory instead (DIRECT).
-    constexpr bool SUMS = MODE == LOGITS || MODE == PROBS || PLANES == 3, DIRECT = MODE != LOGITS && PLANES == 1;
+    constexpr int BLOCKS = kHalf / 32;                        // a warp's columns
+    // Chunks of K are added in registers. Where one chunk is all there is, the results of bf16 operands go out block
+    // by block as they leave tensor memory instead.
+    constexpr bool MAY_BE_DIRECT = MODE != LOGITS && PLANES == 1;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kStageA;
@@ -593,11 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             Row r;
             r.unit = unit;
             begin<MODE>(r, a, sh, k, (k.tm * CTAS + rank) * kTileM + quad * 32 + lane);
-            const bool direct = DIRECT && (!SUMS || k.kb1 - k.kb0 <= a.chunk);
-            float v[SUMS ? kHalf / 32 : 1][32];
-            if (SUMS && !direct) {
+            const bool direct = MAY_BE_DIRECT && k.kb1 - k.kb0 <= a.chunk;
+            float v[BLOCKS][32];
+            if (!direct) {
 #pragma unroll
-                for (int b = 0; b < kHalf / 32; ++b)
+                for (int b = 0; b < BLOCKS; ++b)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[b][i] = 0.f;
             }
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after_sync();
                 const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
                 if (direct) {
-                    if constexpr (DIRECT) {
+                    if constexpr (MAY_BE_DIRECT) {
 #pragma unroll 1
                         for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
                             __syncwarp();
@@ -616,9 +619,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             block<MODE, PLANES>(r, a, k, c0, cols, v[0], &map_out, stage);
                         }
                     }
-                } else if constexpr (SUMS) {
+                } else {
 #pragma unroll
-                    for (int b = 0; b < kHalf / 32; ++b) {
+                    for (int b = 0; b < BLOCKS; ++b) {
                         const int c0 = half * kHalf + 32 * b;
                         if (c0 < cols) {
                             float x[32];
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) gave_up = 1;
                 break;
             }
-            if (SUMS && !direct) {
+            if (!direct) {
                 // One copy of the code for the four blocks, whose sums move up: a CTA with one tile fetches it
                 // once, and fetching is what four copies cost (P of 64 rows x 2048 x 32000 32 us instead of
                 // 28, the loss of 64 rows x 1024 x 32000 17.7 us instead of 17.0)
@@ -648,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
                     block<MODE, PLANES>(r, a, k, c0, cols, v[0], &map_out, stage);
 #pragma unroll
-                    for (int b = 0; b + 1 < (SUMS ? kHalf / 32 : 1); ++b)
+                    for (int b = 0; b + 1 < BLOCKS; ++b)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[b][i] = v[b + 1][i];
                 }

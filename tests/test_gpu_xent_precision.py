@@ -94,3 +94,19 @@ def test_gradient_of_sure_rows(kind, rows, dim, level):
     over = (dW.double() - want).abs() - bound
     worst = (dW.double() - want)[t].norm() / want[t].norm()
     assert float(over.amax()) <= 0, f"targets' rows of dW are {float(worst):.2e} off"
+
+
+@pytest.mark.parametrize("rows", [1 << 17, 1 << 21])
+def test_dW_of_many_rows_is_not_biased(rows):
+    """Logits of zero: every p is 1 / 300, P is its rounding to bf16, and an entry that is nobody's target gets the sum of as
+    many equal terms as there are rows. Cut towards zero in one chain, 2^21 rows would lose 2^-25 a step of
+    16, 2^-8 of the sum; chains of 65536 at most lose 2^-13, which leaves dW's own rounding of 2^-9."""
+    torch, bl = torch_cuda(), lib()
+    H = torch.full((rows, 8), 1 + 2.0 ** -7, device="cuda", dtype=torch.bfloat16)
+    W = torch.zeros(300, 8, device="cuda", dtype=torch.bfloat16)
+    t, g = torch.zeros(rows, dtype=torch.int64, device="cuda"), torch.ones(rows, device="cuda")
+    _, lse = bl.xent(H, W, t)
+    _, dW = bl.xent_grad(H, W, t, lse, g, dH=False)
+    p = float(torch.tensor(1 / 300).bfloat16())
+    want = rows * p * (1 + 2.0 ** -7)
+    assert float((dW[1:].double() / want - 1).abs().amax()) <= 2.0 ** -9 + 2.0 ** -12
