@@ -128,7 +128,7 @@ bl_status bl_gnorm(int64_t count, const int32_t *dtypes, const void *const *x, c
 /*
  * bl_gclip -- scale `count` tensors so that their global norm is at most max_norm:
  * y_ij = c * x_ij with c = max_norm / norm where norm > max_norm, else 1. Where the norm is not
- * finite c is 1 as well: the caller sees it in `norm` and skips the step.
+ * finite, or beyond f32's range, c is 1 as well: the caller sees infinity or NaN in `norm` and skips the step.
  *
  *   y         HOST array of device pointers to the results, of x's types and sizes. y[i] may be
  *             x[i] (in place; left untouched where c = 1) but overlaps no other input or output: such a

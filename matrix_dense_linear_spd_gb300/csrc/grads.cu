@@ -2,7 +2,7 @@
 //
 //   norm = sqrt(sum_i sum_j x_ij^2),   y_ij = c * x_ij,   c = norm > max_norm ? max_norm / norm : 1
 //
-// (c = 1 too where the norm is not finite.) The norm reads every element once and does one
+// (c = 1 too where the norm is not finite, or not in f32.) The norm reads every element once and does one
 // multiply-add each, so HBM bandwidth bounds it; clipping reads every element twice and writes it
 // once. Two launches whatever the number of tensors (up to kMany per launch): the sum kernel
 // leaves one f64 partial sum per CTA, and every CTA of the second kernel adds those partials in
@@ -221,8 +221,9 @@ __device__ __forceinline__ void scale_by(const Entry &e, int64_t k, double c, in
     else if (e.dtype == BL_F16) chunk_scale<__half>(s, e.x, e.y, c, tid);
     else chunk_scale<double>(s, e.x, e.y, c, tid);
 }
+// A norm that the caller sees as not finite, in the f32 that it gets, changes nothing.
 __device__ __forceinline__ double factor(double norm, double max_norm) {
-    return norm > max_norm && isfinite(norm) ? max_norm / norm : 1.0;
+    return norm > max_norm && isfinite(static_cast<float>(norm)) ? max_norm / norm : 1.0;
 }
 
 template <int MAXT>
