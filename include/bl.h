@@ -134,8 +134,8 @@ bl_status bl_gnorm(int64_t count, const int32_t *dtypes, const void *const *x, c
  *             x[i] (in place; left untouched where c = 1) but overlaps no other input or output: such a
  *             call (one tensor listed twice in place, say) is refused.
  *   max_norm  >= 0, infinity allowed (copies).
- *   norm      receives the norm BEFORE scaling. c is computed in f64 and rounded to f32 for f32,
- *             bf16 and f16 tensors, whose products are rounded once to their type.
+ *   norm      receives the norm BEFORE scaling. c is computed in f64 and rounded to 24 bits
+ *             for f32, bf16 and f16 tensors, whose products are rounded once to their type.
  * Other arguments as bl_gnorm.
  */
 bl_status bl_gclip(int64_t count, const int32_t *dtypes, const void *const *x, void *const *y,

@@ -158,9 +158,21 @@ __device__ __forceinline__ double chunk_sum(const Span &s, int tid) {
     return static_cast<double>(acc);
 }
 
+// The factor, for f64 values and for the others. One near the end of f32's range (norms of 1e30 and more) has
+// few bits there or none: it is `single` times `rest`, and the product with `rest` is exact.
+struct Factor {
+    double whole;
+    float single, rest;
+    __device__ static Factor of(double c) {
+        const bool tiny = c < 0x1p-100;
+        return {c, static_cast<float>(tiny ? c * 0x1p64 : c), tiny ? 0x1p-64f : 1.f};
+    }
+};
+__device__ __forceinline__ float scaled(float v, const Factor &c) { return v * c.single * c.rest; }
+__device__ __forceinline__ double scaled(double v, const Factor &c) { return v * c.whole; }
+
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const Span &s, const void *x, void *y, double c, int tid) {
-    const typename Elem<T>::Wide cw = static_cast<typename Elem<T>::Wide>(c);
+__device__ __forceinline__ void chunk_scale(const Span &s, const void *x, void *y, const Factor &c, int tid) {
     const intptr_t shift = reinterpret_cast<intptr_t>(y) - reinterpret_cast<intptr_t>(x);
     const bool together = (shift & 15) == 0;
     Vec<T> v[kVecs];
@@ -170,7 +182,7 @@ __device__ __forceinline__ void chunk_scale(const Span &s, const void *x, void *
     for (int u = 0; u < kVecs; ++u) {
         const uintptr_t a = s.base + (u * kThreads + tid) * 16;
 #pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) v[u].e[i] = Elem<T>::down(Elem<T>::up(v[u].e[i]) * cw);
+        for (int i = 0; i < Vec<T>::N; ++i) v[u].e[i] = Elem<T>::down(scaled(Elem<T>::up(v[u].e[i]), c));
         if (together && a >= s.lo && a + 16 <= s.hi) {
             __stcs(reinterpret_cast<uint4 *>(a + shift), v[u].q);
         } else {
@@ -214,7 +226,7 @@ __device__ __forceinline__ double sum_of(const Entry &e, int64_t k, int tid) {
     if (e.dtype == BL_F16) return chunk_sum<__half>(s, tid);
     return chunk_sum<double>(s, tid);
 }
-__device__ __forceinline__ void scale_by(const Entry &e, int64_t k, double c, int tid) {
+__device__ __forceinline__ void scale_by(const Entry &e, int64_t k, const Factor &c, int tid) {
     const Span s = span_of(e.x, e.n * elem_bytes(e.dtype), k);
     if (e.dtype == BL_F32) chunk_scale<float>(s, e.x, e.y, c, tid);
     else if (e.dtype == BL_BF16) chunk_scale<__nv_bfloat16>(s, e.x, e.y, c, tid);
@@ -271,7 +283,7 @@ template <int MAXT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     grads_scale_kernel(const __grid_constant__ Tensors<MAXT> t, const double *partials, int count, double max_norm,
                        float *norm) {
-    __shared__ double shared_factor;
+    __shared__ Factor shared_factor;
     pdl_release();
     const int64_t chunks = t.entry[t.count].first;
     const int k0 = static_cast<int>(chunks * blockIdx.x / gridDim.x);
@@ -282,15 +294,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (threadIdx.x == 0) {
         const double all = sqrt(sum);
         if (norm && blockIdx.x == 0) *norm = static_cast<float>(all);
-        shared_factor = factor(all, max_norm);
+        shared_factor = Factor::of(factor(all, max_norm));
     }
     __syncthreads();
-    const double c = shared_factor;
+    const Factor c = shared_factor;
     // backwards: what the sum kernel read last is what L2 still holds
     for (int k = k1 - 1; k >= k0; --i) {
         const Entry e = t.entry[i];
         const int stop = max(e.first, k0);
-        if (c == 1.0 && e.x == e.y) k = stop - 1;           // in place and nothing to change
+        if (c.whole == 1.0 && e.x == e.y) k = stop - 1;           // in place and nothing to change
         for (; k >= stop; --k) scale_by(e, k - e.first, c, threadIdx.x);
     }
 }
