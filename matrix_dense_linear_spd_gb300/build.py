@@ -1,6 +1,7 @@
 """Build libbl.so in-tree: nvcc for sm_103a, one translation unit per dtype compiled in
-parallel, plus the host dispatcher; and _torch_binding.so, the training operators' binding to
-torch tensors, with the host compiler against the installed torch's headers. The tuned selection tables (tuned/*.txt) are embedded as
+parallel, plus the host dispatcher; then, where torch is installed, _torch_binding.so, the training
+operators' binding to torch tensors, with the host compiler against torch's headers. libbl.so needs
+neither and is in place before the binding is looked at. The tuned selection tables (tuned/*.txt) are embedded as
 string literals so the library needs no data files at run time (BL_TUNED_DIR still overrides).
 
 Usage: python -m matrix_dense_linear_spd_gb300.build [--force] [--jobs N]
@@ -178,16 +179,18 @@ def build(force: bool = False, jobs: int | None = None) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
     jobs = jobs or max(1, min(len(srcs), os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(jobs) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if importlib.util.find_spec("torch") else None
         objs = list(ex.map(_compile, srcs))
-        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xlinker", "--no-undefined", "-Xlinker", "-soname=libbl.so"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    if binding is None:
+        print("torch is not installed: the training operators' binding to its tensors is not built", file=sys.stderr)
+    else:
+        _link_binding(binding.result())
     return LIB
 
 

@@ -9,3 +9,10 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (GB300, sm_103a)")
     config.addinivalue_line("markers", "slow: long-running CPU case")
+
+
+def pytest_sessionstart(session):
+    """A tree whose library was built before the tensor binding existed, or without it, is built again."""
+    from matrix_dense_linear_spd_gb300 import build
+    if os.path.exists(build.LIB) and not os.path.exists(build.BINDING):
+        build.build()
