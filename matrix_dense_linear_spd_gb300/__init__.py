@@ -245,6 +245,9 @@ def potrs(A, B, uplo="L", stream=None):
 #
 # Checks, allocation and the C call are in csrc/binding/torch_binding.cpp: these operators take
 # lists of hundreds of tensors and run for microseconds, where ctypes costs more than the GPU does.
+#
+# None of them records anything for autograd: their results carry no graph, whatever their inputs
+# require. Tensors that they write to count as changed in place.
 
 _binding = None
 
@@ -270,7 +273,8 @@ def _raw(stream):
 
 def gnorm(tensors, stream=None):
     """Global norm sqrt(sum of all squares) of a list of f32, f64, bf16 or f16 tensors, in any
-    mix and any memory order (no gaps, no overlaps). Returns a 0-dim f32 tensor on their device."""
+    mix and any memory order (no gaps, no overlaps). Returns a 0-dim f32 tensor on their device,
+    which carries no autograd graph."""
     return (_binding or _training()).gnorm(tensors, _raw(stream))
 
 
@@ -278,19 +282,22 @@ def gclip(tensors, max_norm, out=None, stream=None):
     """Scale the tensors to a global norm of at most max_norm, in place or into the tensors of
     `out` (same types, shapes and strides). No result may overlap another tensor of the call (a
     tensor that is listed twice in place is refused). A norm that is not finite leaves the values as
-    they are. Returns the norm before scaling, a 0-dim f32 tensor."""
+    they are. Returns the norm before scaling, a 0-dim f32 tensor. Not recorded by autograd."""
     return (_binding or _training()).gclip(tensors, max_norm, out, _raw(stream))
 
 
 def xent(H, W, target, stream=None):
     """Softmax cross entropy of the tokens H (rows, dim) over the vocabulary W (vocab, dim), both
     bf16 or both f32, for int64 targets: (loss, lse), f32 tensors of one value a row. A row whose
-    target lies outside [0, vocab) does not count: 0, 0. The logits are never stored."""
+    target lies outside [0, vocab) does not count: 0, 0. The logits are never stored.
+
+    The losses carry no autograd graph, also where H or W require gradients: backward() through them does
+    nothing. xent_grad gives the gradients; hand them on with H.backward(dH) and W.grad."""
     return (_binding or _training()).xent(H, W, target, _raw(stream))
 
 
 def xent_grad(H, W, target, lse, g, dH=None, dW=None, stream=None):
     """Gradients of sum_r g_r loss_r: (dH, dW) in H's and W's type, given xent's lse. dH and dW
     may be tensors to write to, which overlap no other tensor of the call; False leaves that
-    gradient out (None is returned for it)."""
+    gradient out (None is returned for it). Not recorded by autograd."""
     return (_binding or _training()).xent_grad(H, W, target, lse, g, dH, dW, _raw(stream))

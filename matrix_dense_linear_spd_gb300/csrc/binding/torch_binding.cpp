@@ -68,6 +68,11 @@ c10::DataPtr scratch(int64_t bytes) {
     return c10::cuda::CUDACachingAllocator::get()->allocate(static_cast<size_t>(bytes));
 }
 
+// The call has written to a tensor of the caller's: autograd then knows that what it saved of it is gone.
+void written(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 at::Tensor floats(at::IntArrayRef shape, c10::Device d) {
     return at::empty(shape, at::TensorOptions().dtype(at::kFloat).device(d));
 }
@@ -140,6 +145,10 @@ PyObject *grads(PyObject *list, bool clip, double max_norm, PyObject *out, PyObj
     const int st = clip ? bl_gclip(n, kinds.data(), x.data(), y.data(), sizes.data(), max_norm, to, ws.get(), need, on.bl())
                         : bl_gnorm(n, kinds.data(), x.data(), sizes.data(), to, ws.get(), need, on.bl());
     if (st != BL_SUCCESS) failed(st);
+    if (clip) {
+        PyObject **const results = given ? PySequence_Fast_ITEMS(outs.o) : items;
+        for (int64_t i = 0; i < n; ++i) written(THPVariable_Unpack(results[i]));
+    }
     return THPVariable_Wrap(std::move(norm));
 }
 
@@ -235,6 +244,8 @@ PyObject *do_xent_grad(PyObject *const *a) {
                                 dh.defined() ? dh.data_ptr() : nullptr, lddh, dw.defined() ? dw.data_ptr() : nullptr, lddw,
                                 ws.get(), need, on.bl());
     if (st != BL_SUCCESS) failed(st);
+    if (dh.defined()) written(dh);
+    if (dw.defined()) written(dw);
     return pair(wrapped(dh), wrapped(dw));
 }
 
