@@ -110,3 +110,25 @@ def test_dW_of_many_rows_is_not_biased(rows):
     p = float(torch.tensor(1 / 300).bfloat16())
     want = rows * p * (1 + 2.0 ** -7)
     assert float((dW[1:].double() / want - 1).abs().amax()) <= 2.0 ** -9 + 2.0 ** -12
+
+
+@pytest.mark.parametrize("rows,vocab", [(64, 3000), (1024, 4000)])
+def test_f32_products_are_f32(rows, vocab):
+    """Single CTAs and pairs, f32. Three planes and sums cut every 128 of K leave a relative error of about 4e-7 in the
+    2-norm, of which f32's own rounding is 1e-7; two planes (2^-17 an element) or uncut sums (1e-5 at K = 32000, 1e-6
+    at 4000) would not stay below 1e-6. A vocabulary of one entry shows the logits: lse = s."""
+    torch, bl = torch_cuda(), lib()
+    H, W, t, g = make(rows, 1024, vocab, "f32", seed=rows, scale=1.0)
+    g = g.abs() + 0.5
+    for v in (0, 7):
+        _, s = bl.xent(H, W[v:v + 1], torch.zeros_like(t))
+        want = H.double() @ W[v].double()
+        assert float((s.double() - want).norm() / want.norm()) < 1e-6
+    _, lse = bl.xent(H, W, t)
+    dH, dW = bl.xent_grad(H, W, t, lse, g)
+    P = torch.softmax(H.double() @ W.double().T, 1)
+    P[range(rows), t] -= 1
+    P *= g.double()[:, None]
+    for name, got, want in (("dH", dH, P @ W.double()), ("dW", dW, P.T @ H.double())):
+        off = float((got.double() - want).norm() / want.norm())
+        assert off < 1e-6, (name, off)
