@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(256)
 // logits of bf16 operands, and those of P where the loss of few rows has added them in f32 (W's way from memory
 // hides it: step of 1 row x 4096 x 32000 216 us, 212 with the chain uncut). bf16 results, dH and dW, have long chunks.
 constexpr int kChunkF32 = 2, kChunkLoss = 16, kChunkFew = 1, kChunkBf16 = 256;
-// Bytes of P, and of a piece's copy of W, that a piece of the vocabulary may take. Steps of 4096 x 4096 x
+// Bytes of P, and of a piece's copy of W, that a piece of the vocabulary may take (4096 entries may take more: 8 KB of P
+// a row in bf16, 24 KB in f32). Steps of 4096 x 4096 x
 // 131072 in bf16 and 1024 x 1024 x 32000 in f32 at 64, 128, 512 and 2048 MB: 11.04, 10.84, 10.66, 10.65 ms
 // and 1.22, 1.13, 1.04, 1.04 ms
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
@@ -452,7 +453,8 @@ bool for_tma(const void *p, int64_t ld, int64_t elem) {
 // where there are too many rows, or H does not fit shared memory. Measured, loss over a vocabulary of
 // 32000, this kernel against the tiles: dim 1024, bf16 1 row 15.7 us against 19.5, 2 rows 22 against 19.6;
 // f32 1, 4, 8 rows 25.5, 29.5, 45 us against 106 (the tiles' copies of W); dim 1021, whose rows start off the
-// vectors and which the tiles copy, bf16 1, 4, 8 rows 29, 37, 64 us against 43, f32 35, 42, 69 against 116.
+// vectors and which the tiles copy, bf16 1, 4, 8 rows 29, 37, 64 us against 43, f32 35, 42, 69 against 116. (Of a W
+// far larger than L2 only one row was measured: dim 4096, vocabulary 131072, bf16 153 us against 216.)
 bool few_vec(const void *W, int64_t ldw, int64_t dim, int64_t elem) { return for_tma(W, ldw, elem) && dim * elem % 16 == 0; }
 int few_rows(int dtype, int64_t rows, int64_t dim, const void *W, int64_t ldw) {
     const bool vec = few_vec(W, ldw, dim, dtype == BL_F32 ? 4 : 2);

@@ -28,8 +28,8 @@
 // 1024, 2048 and none: 317, 301, 294, 291 us.
 //
 // What bounds it: the operands' way into shared memory. A bf16 stage brings 32 KB for the 512 cycles of
-// its products, 64 bytes a cycle, and the tensor pipe is 83 to 86% busy (303 to 312 us for each of the four
-// products at 4096 x 4096 x 16384, 1,760 to 1,810 TFLOP/s); an f32 stage brings half of that a cycle, and
+// its products, 64 bytes a cycle, and the tensor pipe is 80 to 86% busy (307 to 317 us for each of the four
+// products at 4096 x 4096 x 16384, 1,740 to 1,790 TFLOP/s; P, uncut, 303); an f32 stage brings half of that a cycle, and
 // the pipe is 93 to 96% busy. Then the power cap: back to back the clock falls from 1.9 to 1.65 GHz.
 //
 // P and the copies of H and W are stored in panels of 64 columns ([plane][panel][row][64]), so that
