@@ -183,8 +183,8 @@ bl_status bl_xent(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, cons
  *             do is refused; rows that lie in the gaps of another matrix's rows do not overlap it).
  *   workspace at least bl_xent_workspace(..., grad = 1) bytes.
  * P is formed piece by piece of the vocabulary, in units of the largest |g| of a row that counts, and
- * rounded to bf16 for bf16 operands (relative 2^-8 an element, as the gradients themselves are);
- * f32 operands keep it in f32. Before that rounding an element is g exp(s - lse) times an error of
+ * rounded to bf16 for bf16 operands (relative 2^-8 an element, as the gradients themselves are), up to
+ * 16 rows to two bf16 parts (2^-16); f32 operands keep it in f32. Before that rounding an element is g exp(s - lse) times an error of
  * 2^-24 |lse| from lse's own rounding, and of the sums of s; at the target of a row that is sure of it, where P
  * is g (exp(s - lse) - 1), the former is left in absolute terms.
  * A kernel that gave up waiting makes all of dH and dW NaN. Other arguments as bl_xent.

@@ -424,8 +424,16 @@ constexpr int64_t kPieceBytes = int64_t(512) << 20;
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t cdiv(int64_t v, int64_t by) { return (v + by - 1) / by; }
 
+// P of bf16 operands takes two planes up to so many rows, so that a sum over few of them does not show its
+// rounding: errors of dH and dW against 64 bits, in units of those with P in f32, over sizes and seeds, at worst: 1
+// row 1.6 and 2.0, 2 rows 1.4 and 1.7, 5 and 8 rows 1.5, 16 rows 1.25, 64 rows and more 1.3 (1.2 on average). The
+// second plane costs what the doubled products do not hide behind W's way from memory: step of 8 rows x 1024 x 32000
+// 80 us instead of 71, of 32 rows x 4096 x 32000 223 instead of 207.
+constexpr int kTwoPlaneRows = 16;
+
 struct Plan {
     int planes, pairs;
+    int p_planes;             // of P
     int ctas;                 // that share a tile
     int groups;               // CTAs or pairs that the device's SMs hold
     bool copy_h, copy_w, compact, grad;
@@ -468,12 +476,13 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     Plan q{};
     q.planes = dtype == BL_F32 ? 3 : 1;
     q.pairs = dtype == BL_F32 ? 6 : 1;
+    q.p_planes = dtype == BL_F32 ? 3 : rows <= kTwoPlaneRows ? 2 : 1;
     q.compact = rows > kTileM;
     // pairs of CTAs above one row tile: steps at dim 1024, vocabulary 32000 on single CTAs against pairs: bf16
     // 64 rows 75 us, 93; 128 rows 78, 93; 200 rows 111, 108; f32 64 rows 319, 358; 200 rows 467, 398
     q.ctas = rows > kTileM ? 2 : 1;
     q.groups = std::max(1, sms / q.ctas);
-    q.wide = q.ctas == 1 && q.planes == 3 ? Ring<1, 3>::kTile : kTileN;
+    q.wide = q.ctas == 1 && q.planes == 3 ? Ring<1, 3, 3>::kTile : kTileN;
     // a row without a target may hold anything: only the loss of uncopied rows ignores it
     q.copy_h = dtype == BL_F32 || grad || q.compact || !for_tma(H, ldh, 2);
     q.copy_w = dtype == BL_F32 || !for_tma(W, ldw, 2);
@@ -487,7 +496,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     // a piece: what keeps P and the copy of W within their size, but 4096 entries at least, so
     // that a piece's products fill the GPU; pieces of one size
     int64_t most = up(vocab, kTileN);
-    if (grad) most = std::min(most, kPieceBytes / (q.tiled * 2 * q.planes));
+    if (grad) most = std::min(most, kPieceBytes / (q.tiled * 2 * q.p_planes));
     if (q.copy_w) most = std::min(most, kPieceBytes / (q.panels * 128 * q.planes));
     most = std::max<int64_t>(most / kTileN * kTileN, 4096);
     q.pieces = cdiv(vocab, most);
@@ -542,7 +551,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
         q.part = take(rows * q.part_ld * 8);
         q.picked = take(rows * 4);
     } else {
-        q.p = take(q.planes * q.tiled * q.piece * 2);
+        q.p = take(q.p_planes * q.tiled * q.piece * 2);
         q.dh = take(q.slab_rows * q.ldo * 4);
     }
     q.bytes = at;
@@ -597,7 +606,7 @@ bool map_f32(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, in
 template <int MODE, int PLANES, int CTAS>
 cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, GemmArgs &a, int &flags, int sms,
                          cudaStream_t s) {
-    constexpr int kSmem = Ring<CTAS, PLANES>::kSmem;
+    constexpr int kSmem = RingOf<MODE, PLANES, CTAS>::kSmem;
     const auto kernel = gemm_kernel<MODE, PLANES, CTAS>;
     static std::atomic<int> groups[64];         // CTAs, or pairs of CTAs, that the device runs at once
     int dev = 0;
@@ -636,6 +645,14 @@ cudaError_t launch_gemm(const CUtensorMap &ma, const CUtensorMap &mb, const CUte
                         int sms, cudaStream_t s) {
     return ctas == 1 ? launch_tiles<MODE, PLANES, 1>(ma, mb, mo, a, flags, sms, s)
                      : launch_tiles<MODE, PLANES, 2>(ma, mb, mo, a, flags, sms, s);
+}
+// One of the products that make P or take it. Two planes of it only ever meet single CTAs.
+template <int MODE, int PLANES>
+cudaError_t launch_with_p(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, GemmArgs &a, const Plan &q, int &flags,
+                          int sms, cudaStream_t s) {
+    if constexpr (PLANES == 1)
+        if (q.p_planes == 2) return launch_tiles<MODE, 2, 1>(ma, mb, mo, a, flags, sms, s);
+    return launch_gemm<MODE, PLANES>(ma, mb, mo, a, q.ctas, flags, sms, s);
 }
 
 // Raise a kernel's dynamic shared memory, once per device.
@@ -785,13 +802,13 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         const int64_t p_panels = cdiv(n, 64);
         const Columns cols_p{0, 1, static_cast<int>(p_panels)};
         CUtensorMap p_out;
-        BL_MAP(map_panels(&p_out, pp, q.seen, q.tiled, PLANES * p_panels, 32, PLANES == 1 ? 128 : 64));
+        BL_MAP(map_panels(&p_out, pp, q.seen, q.tiled, q.p_planes * p_panels, 32, q.p_planes == 1 ? 128 : 64));
         a.p_panels = static_cast<int>(p_panels);
         a.lse = c.lse_in;
-        BL_TRY((launch_gemm<PROBS, PLANES>(h_k, w_k, p_out, a, q.ctas, flag_count, c.sms, c.s)));
+        BL_TRY((launch_with_p<PROBS, PLANES>(h_k, w_k, p_out, a, q, flag_count, c.sms, c.s)));
         if (c.dH) {
             CUtensorMap p_k, sums;
-            BL_MAP(map_panels(&p_k, pp, q.seen, q.tiled, PLANES * p_panels, kTileM));
+            BL_MAP(map_panels(&p_k, pp, q.seen, q.tiled, q.p_planes * p_panels, kTileM));
             BL_MAP(map_f32(&sums, c.ws + q.dh, c.dim, q.slab_rows, 1, q.ldo, q.ldo));
             GemmArgs d = base;
             d.m = rows;
@@ -803,11 +820,11 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             d.accumulate = i > 0;
             d.ca = cols_p;
             d.cb = cols_w;
-            BL_TRY((launch_gemm<DH, PLANES>(p_k, w_mn, sums, d, q.ctas, flag_count, c.sms, c.s)));
+            BL_TRY((launch_with_p<DH, PLANES>(p_k, w_mn, sums, d, q, flag_count, c.sms, c.s)));
         }
         if (c.dW) {
             CUtensorMap p_mn, h_mn, to;
-            BL_MAP(map_panels(&p_mn, pp, q.seen, q.tiled, PLANES * p_panels, kTileK));
+            BL_MAP(map_panels(&p_mn, pp, q.seen, q.tiled, q.p_planes * p_panels, kTileK));
             BL_MAP(map_panels(&h_mn, c.ws + q.h, q.seen, q.tiled, PLANES * q.panels, kTileK));      // the gradient always copies H
             GemmArgs d = base;
             d.m = static_cast<int>(n);
@@ -826,7 +843,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             } else {
                 BL_MAP(map_f32(&to, out, c.dim, n, 1, c.lddw, c.lddw));
             }
-            BL_TRY((launch_gemm<DW, PLANES>(p_mn, h_mn, to, d, q.ctas, flag_count, c.sms, c.s)));
+            BL_TRY((launch_with_p<DW, PLANES>(p_mn, h_mn, to, d, q, flag_count, c.sms, c.s)));
         }
     }
     if (t_gave_up) BL_TRY(cudaMemsetAsync(flags, 1, 4, c.s));

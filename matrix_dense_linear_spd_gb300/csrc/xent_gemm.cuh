@@ -35,6 +35,9 @@
 // P and the copies of H and W are stored in panels of 64 columns ([plane][panel][row][64]), so that
 // every operand tile is one contiguous piece of memory in either direction of use.
 //
+// bf16 operands have P in one bf16 plane, or in two where few rows add up to little averaging of its roundings
+// (PLANES = 2: LOGITS and PROBS take one plane of H and W, DH and DW two of P and one of the other operand).
+//
 // Every wait is bounded: a role that gives up marks its CTA's flag, waits (bounded) for its own
 // copies and products in flight, and leaves; the others then run out of time too.
 #pragma once
@@ -59,14 +62,19 @@ constexpr int kStageBytes = 32 * 128;                           // an epilogue w
 // every plane of both, so that f32 operands cross the chip once for their six products (copied again
 // for each product: 1024 x 1024 x 32000 1.12 ms a step instead of 1.03, 20 rows x 3918 x 3275 137 us
 // instead of 86). A single CTA has room for the planes of 128 columns of B only.
-template <int CTAS, int PLANES>
+template <int CTAS, int PLANES_A, int PLANES_B>
 struct Ring {
-    static constexpr int kTile = CTAS == 1 && PLANES == 3 ? kTileN / 2 : kTileN;       // columns of a tile, at most
+    static constexpr int kTile = CTAS == 1 && PLANES_B == 3 ? kTileN / 2 : kTileN;     // columns of a tile, at most
     static constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTile / CTAS * kTileK * 2;     // of a plane
-    static constexpr int kStageA = PLANES * kBytesA, kStageB = PLANES * kBytesB;
-    static constexpr int kStages = PLANES == 3 ? 2 : CTAS == 1 ? 4 : 6;                // 192 KB
+    static constexpr int kStageA = PLANES_A * kBytesA, kStageB = PLANES_B * kBytesB;
+    static constexpr int kStages = PLANES_A == 3 ? 2 : PLANES_A == 2 ? 3 : CTAS == 1 ? 4 : 6;                // 192 KB
     static constexpr int kSmem = kStages * (kStageA + kStageB) + kEpilogueWarps * kStageBytes + 1024;
 };
+// Planes of a product's operands
+__host__ __device__ constexpr int planes_a(int mode, int planes) { return planes == 3 || mode == DH || mode == DW ? planes : 1; }
+__host__ __device__ constexpr int planes_b(int planes) { return planes == 3 ? 3 : 1; }
+template <int MODE, int PLANES, int CTAS>
+using RingOf = Ring<CTAS, planes_a(MODE, PLANES), planes_b(PLANES)>;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;             // producers, issuer (and an idle warp), epilogue
 // 384 threads start with 168 registers each; the first four warps give most of theirs to the
 // epilogue, whose rows hold 128 sums: 128 * 56 + 256 * 224 = 384 * 168.
@@ -108,9 +116,12 @@ struct GemmArgs {
     int64_t ldo;
 };
 
-// The products of planes that f32 operands take, smallest first.
-__host__ __device__ constexpr int pair_a(int q) { return q == 1 ? 2 : q == 0 || q == 3 ? 1 : 0; }
-__host__ __device__ constexpr int pair_b(int q) { return q == 2 ? 2 : q == 0 || q == 4 ? 1 : 0; }
+// The products of planes, smallest first: all where only A has several, six of nine for f32 operands.
+__host__ __device__ constexpr int pairs_of(int pa, int pb) { return pb == 3 ? 6 : pa; }
+__host__ __device__ constexpr int pair_a(int q, int pairs) {
+    return pairs < 6 ? pairs - 1 - q : q == 1 ? 2 : q == 0 || q == 3 ? 1 : 0;
+}
+__host__ __device__ constexpr int pair_b(int q, int pairs) { return pairs < 6 ? 0 : q == 2 ? 2 : q == 0 || q == 4 ? 1 : 0; }
 
 // DH has few tiles and a long K axis, so K is cut into parts that have partial sums of their own:
 // as many as make the least of the rounds that the device needs, times a part's steps (and 4 to
@@ -360,9 +371,9 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
     if constexpr (MODE == PROBS) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            // the difference first, as in block_logits; the bf16 form rounds the result to 8 bits anyway. What the
+            // the difference first, as in block_logits; the bf16 form rounds the result to 8 or 16 bits anyway. What the
             // exponential is off by where it is near 1 (2^-22) is no more than what lse's own rounding leaves.
-            float e = PLANES == 1 ? exp2f((v[i] - r.lse) * kLog2e) : expf(v[i] - r.lse);
+            float e = PLANES == 3 ? expf(v[i] - r.lse) : exp2f((v[i] - r.lse) * kLog2e);
             if (i == r.at - c0) e -= 1.f;
             v[i] = r.counted && n0 + c0 + i < a.n ? r.g * e : 0.f;      // panels are whole: zero to their end
         }
@@ -373,11 +384,11 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
     }
     // where the rows that count are copied together P has whole row tiles: dW multiplies their zeros
     const bool there = row0 < r.m || (MODE == PROBS && a.kept != nullptr);
-    if constexpr (MODE == DH || PLANES == 3) {
+    if constexpr (MODE == DH || PLANES == 3 || (MODE == PROBS && PLANES == 2)) {
         if constexpr (MODE == PROBS) {
-            // three planes of 32 values: 64 bytes a line each
+            // planes of 32 values: 64 bytes a line each
 #pragma unroll
-            for (int pl = 0; pl < 3; ++pl) {
+            for (int pl = 0; pl < PLANES; ++pl) {
                 lines_free();
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -423,13 +434,14 @@ template <int MODE, int PLANES, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_out, const __grid_constant__ GemmArgs a) {
-    using R = Ring<CTAS, PLANES>;
+    using R = RingOf<MODE, PLANES, CTAS>;
+    constexpr int PA = planes_a(MODE, PLANES), PB = planes_b(PLANES), PAIRS = pairs_of(PA, PB);
     constexpr int kBytesA = R::kBytesA, kBytesB = R::kBytesB, kStageA = R::kStageA, kStageB = R::kStageB, kStages = R::kStages;
     constexpr bool A_MN = MODE == DW, B_MN = MODE == DH || MODE == DW;
     constexpr int BLOCKS = kHalf / 32;                        // a warp's columns
     // Chunks of K are added in registers. Where one chunk is all there is, the results of bf16 operands go out block
     // by block as they leave tensor memory instead.
-    constexpr bool MAY_BE_DIRECT = MODE != LOGITS && PLANES == 1;
+    constexpr bool MAY_BE_DIRECT = MODE != LOGITS && PLANES != 3;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kStageA;
@@ -482,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int part = cols_of<B_MN, CTAS>(k.tn, a) / CTAS;       // this CTA's columns of B
                 const int m0 = (k.tm * CTAS + rank) * kTileM, n0 = k.tn * a.tile_n + rank * part;
                 const int groups_b = (part + 63) >> 6;
-                const uint32_t bytes = CTAS * PLANES * (kBytesA + (B_MN ? groups_b * (kTileK * 128) : a.tile_n / CTAS * 128));
+                const uint32_t bytes = CTAS * (PA * kBytesA + PB * (B_MN ? groups_b * (kTileK * 128) : a.tile_n / CTAS * 128));
                 for (int kb = k.kb0; kb < k.kb1; ++kb) {
                     if (!tc::mbar_wait(&empty[s], phase ^ 1, kPolls)) {
                         ok = false;
@@ -491,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (announce) tc::mbar_expect_tx(&full[s], bytes);
                     const uint32_t bar = bar0 + 8 * s;
 #pragma unroll 1
-                    for (int p = 0; p < PLANES; ++p) {
+                    for (int p = 0; p < (for_a ? PA : PB); ++p) {
                         if (for_a) {
                             unsigned char *const d = tiles_a + s * kStageA + p * kBytesA;
                             const int z = p * a.ca.plane;
@@ -556,10 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc::fence_after_sync();
                         const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (kStageB >> 4);
-                        constexpr int PAIRS = PLANES == 1 ? 1 : 6;
 #pragma unroll
                         for (int q = 0; q < PAIRS; ++q) {
-                            const int pa = PLANES == 1 ? 0 : pair_a(q), pb = PLANES == 1 ? 0 : pair_b(q);
+                            const int pa = pair_a(q, PAIRS), pb = pair_b(q, PAIRS);
 #pragma unroll
                             for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
                                 tc::mma_f16<CTAS>(acc, da + pa * (kBytesA >> 4) + j * (A_MN ? 2048 / 16 : 2),

@@ -132,3 +132,22 @@ def test_f32_products_are_f32(rows, vocab):
     for name, got, want in (("dH", dH, P @ W.double()), ("dW", dW, P.T @ H.double())):
         off = float((got.double() - want).norm() / want.norm())
         assert off < 1e-6, (name, off)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5, 32])
+def test_gradients_of_few_rows_are_rounded_once(rows):
+    """P of one row, or of few, scales whole rows of the results: rounded to 8 bits it would put up to 2^-8 on top of
+    the results' own rounding. That is uniform within 2^-8 of a value, or less: a relative 2-norm of 2^-8 / sqrt(3) over many
+    values, whose mantissas are not all 1; 2^-11 is left for everything else."""
+    torch, bl = torch_cuda(), lib()
+    for seed in range(24):
+        H, W, t, g = make(rows, 512, 2000, "bf16", seed=100 * rows + seed)
+        H.add_(W[t] * torch.linspace(0, 10, rows + 24, device="cuda")[seed:seed + rows, None])           # some rows are sure, most are not
+        _, lse = bl.xent(H, W, t)
+        dH, dW = bl.xent_grad(H, W, t, lse, g)
+        P = torch.softmax(H.double() @ W.double().T, 1)
+        P[range(rows), t] -= 1
+        P *= g.double()[:, None]
+        for name, got, want in (("dH", dH, P @ W.double()), ("dW", dW, P.T @ H.double())):
+            off = float((got.double() - want).norm() / want.norm())
+            assert off < 2.0 ** -8 / math.sqrt(3) + 2.0 ** -11, (name, seed, off)
