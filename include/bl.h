@@ -200,6 +200,48 @@ bl_status bl_xent_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab,
 int64_t bl_xent_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
                           const void *W, int64_t ldw, int grad);
 
+/*
+ * bl_score -- scores of given tokens: their log probabilities, the entropy of the distribution that each was
+ * drawn from, and its likeliest tokens. With s and lse as in bl_xent and p_rv = exp(s_rv - lse_r):
+ *     logp_r = s_r,target(r) - lse_r,   entropy_r = -sum_v p_rv log p_rv,
+ *     the `top` largest s_rv of a row, largest first, of equal ones the lowest v first
+ * The logits are not kept, but for blocks of 32 that may hold one of the likeliest.
+ *
+ *   top       0 .. 32 (and at most vocab) alternatives for each row.
+ *   logp, entropy, lse   device float[rows].
+ *   top_logp, top_id     device float[rows*top] (s - lse) and int64[rows*top] (v), row after row; not looked
+ *             at where top is 0.
+ *   workspace at least bl_score_workspace(...) bytes, 256-byte aligned. With alternatives up to 2 GB of it, or
+ *             16 KB a row if that is more, are for logits, and few of them are written.
+ * A row whose target does not count has logp, entropy, lse and top_logp 0 and top_id -1. Where bl_xent gives
+ * NaN all floats of the row are NaN and top_id is -1. A logit of minus infinity has no share in the entropy, and
+ * its place among the alternatives, after all others. No result overlaps another tensor of the call. Other
+ * arguments, and what holds beside that, as bl_xent.
+ */
+bl_status bl_score(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, int64_t top, const void *H, int64_t ldh,
+                   const void *W, int64_t ldw, const int64_t *target, float *logp, float *entropy, float *lse,
+                   float *top_logp, int64_t *top_id, void *workspace, int64_t workspace_bytes, bl_stream_t stream);
+
+/*
+ * bl_score_grad -- the gradients of sum_r g_r logp_r + e_r entropy_r: with x = s - lse,
+ *     P_rv = g_r ([v = target(r)] - p_rv) - e_r p_rv (x_rv + entropy_r),   dH = P W,   dW = P^T H
+ *
+ *   lse, entropy   device float[rows], as bl_score gave them for the same H, W and target.
+ *   g, e      device float[rows]. Not looked at where a row does not count.
+ *   workspace at least bl_xent_workspace(..., grad = 1) bytes.
+ * P is kept in units of the largest |g| or |e| of a row that counts. Other arguments, and what holds beside
+ * that, as bl_xent_grad.
+ */
+bl_status bl_score_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh,
+                        const void *W, int64_t ldw, const int64_t *target, const float *lse, const float *entropy,
+                        const float *g, const float *e, void *dH, int64_t lddh, void *dW, int64_t lddw,
+                        void *workspace, int64_t workspace_bytes, bl_stream_t stream);
+
+/* Bytes of workspace that bl_score needs on the current device for these arguments; -1 if they are invalid
+ * (see bl_last_error()). Of H and W only the addresses are looked at. */
+int64_t bl_score_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, int64_t top, const void *H,
+                           int64_t ldh, const void *W, int64_t ldw);
+
 /* Static, human-readable name of a status code. */
 const char *bl_status_string(bl_status status);
 
@@ -258,9 +300,10 @@ bl_status bl_debug_tc_tile_f32(const float *A, const float *B, float *C, int32_t
                                bl_stream_t stream);
 
 /*
- * Diagnostic: with on != 0 the calling thread's bl_xent and bl_xent_grad report, from then on, that
- * one of their matrix products gave up waiting, although none did: what a caller sees of it can be
- * tested. on = 0 ends that. (bl_xent's kernel for few rows waits for nothing and reports nothing.)
+ * Diagnostic: with on != 0 the calling thread's bl_xent, bl_xent_grad, bl_score and bl_score_grad report,
+ * from then on, that one of their matrix products gave up waiting, although none did: what a caller sees of it
+ * can be tested. on = 0 ends that. (The kernel for few rows of the first and third waits for nothing and
+ * reports nothing.)
  */
 bl_status bl_debug_xent_gave_up(int on);
 

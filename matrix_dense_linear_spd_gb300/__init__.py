@@ -1,5 +1,5 @@
 """Batched Cholesky factorisation (potrf) and SPD solves (posv, potrs) on GB300, and the
-operators of a training step around them (xent, xent_grad, gnorm, gclip).
+operators of a training step around them (xent, xent_grad, score, score_grad, gnorm, gclip).
 
 Thin ctypes binding over ``libbl.so`` (the C ABI in ``include/bl.h``). This module only
 marshals arguments: every step of the computation runs in the library's CUDA kernels. There is
@@ -26,7 +26,8 @@ STATUS = {0: "success", 1: "invalid argument", 2: "no route", 3: "CUDA error", 4
 EXPORTED = ("bl_potrf", "bl_posv", "bl_potrs", "bl_status_string", "bl_last_error", "bl_last_choice",
             "bl_version", "bl_set_route", "bl_num_routes", "bl_route_name", "bl_route_capacity",
             "bl_select_debug", "bl_debug_tc_tile_f32", "bl_debug_peak", "bl_gnorm", "bl_gclip",
-            "bl_gnorm_workspace", "bl_xent", "bl_xent_grad", "bl_xent_workspace", "bl_debug_xent_gave_up")
+            "bl_gnorm_workspace", "bl_xent", "bl_xent_grad", "bl_xent_workspace", "bl_debug_xent_gave_up",
+            "bl_score", "bl_score_grad", "bl_score_workspace")
 
 
 class BLError(RuntimeError):
@@ -81,6 +82,12 @@ def _load():
     lib.bl_debug_xent_gave_up.restype = ctypes.c_int
     lib.bl_xent_workspace.argtypes = [ctypes.c_int, i64, i64, i64, vp, i64, vp, i64, ctypes.c_int]
     lib.bl_xent_workspace.restype = i64
+    lib.bl_score.argtypes = [ctypes.c_int, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.bl_score.restype = ctypes.c_int
+    lib.bl_score_grad.argtypes = [ctypes.c_int, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.bl_score_grad.restype = ctypes.c_int
+    lib.bl_score_workspace.argtypes = [ctypes.c_int, i64, i64, i64, i64, vp, i64, vp, i64]
+    lib.bl_score_workspace.restype = i64
     return lib
 
 
@@ -301,3 +308,19 @@ def xent_grad(H, W, target, lse, g, dH=None, dW=None, stream=None):
     may be tensors to write to, which overlap no other tensor of the call; False leaves that
     gradient out (None is returned for it). Not recorded by autograd."""
     return (_binding or _training()).xent_grad(H, W, target, lse, g, dH, dW, _raw(stream))
+
+
+def score(H, W, target, top=0, stream=None):
+    """Scores of the tokens `target` under the distributions softmax(H W^T), for tensors as xent takes them:
+    (logp, entropy, lse, top_logp, top_id). logp, entropy and lse are f32, one value a row; top_logp (f32) and
+    top_id (int64) are (rows, top): each row's `top` (0 to 32) likeliest tokens, the likeliest first and of equal
+    ones the lowest first. A row whose target lies outside [0, vocab) does not count: 0, and -1 in top_id. A row
+    with a logit that is infinite or NaN has NaN, and -1 in top_id. The results carry no autograd graph; score_grad
+    gives the gradients of logp and entropy."""
+    return (_binding or _training()).score(H, W, target, top, _raw(stream))
+
+
+def score_grad(H, W, target, lse, entropy, g, e, dH=None, dW=None, stream=None):
+    """Gradients of sum_r g_r logp_r + e_r entropy_r: (dH, dW) in H's and W's type, given score's lse and
+    entropy; g and e are f32, one value a row. dH and dW as in xent_grad. Not recorded by autograd."""
+    return (_binding or _training()).score_grad(H, W, target, lse, entropy, g, e, dH, dW, _raw(stream))

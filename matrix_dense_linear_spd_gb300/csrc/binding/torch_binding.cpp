@@ -249,6 +249,49 @@ PyObject *do_xent_grad(PyObject *const *a) {
     return pair(wrapped(dh), wrapped(dw));
 }
 
+// ------------------------------------------------------------------ score, score_grad
+
+PyObject *do_score(PyObject *const *a) {
+    const Xent c(a[0], a[1], a[2]);
+    const int64_t top = PyLong_AsLongLong(a[3]);
+    if (top == -1 && PyErr_Occurred()) throw Refused();
+    On on(c.h.device(), a[4]);
+    const int64_t need = bl_score_workspace(c.code, c.rows, c.dim, c.vocab, top, c.h.data_ptr(), c.ldh, c.w.data_ptr(), c.ldw);
+    if (need < 0) failed(BL_ERR_INVALID_ARGUMENT);
+    const c10::Device d = c.h.device();
+    at::Tensor logp = floats({c.rows}, d), entropy = floats({c.rows}, d), lse = floats({c.rows}, d), top_logp = floats({c.rows, top}, d);
+    at::Tensor top_id = at::empty({c.rows, top}, at::TensorOptions().dtype(at::kLong).device(d));
+    const c10::DataPtr ws = scratch(need);
+    const int st = bl_score(c.code, c.rows, c.dim, c.vocab, top, c.h.data_ptr(), c.ldh, c.w.data_ptr(), c.ldw, c.target,
+                            logp.mutable_data_ptr<float>(), entropy.mutable_data_ptr<float>(), lse.mutable_data_ptr<float>(),
+                            top_logp.mutable_data_ptr<float>(), top_id.mutable_data_ptr<int64_t>(), ws.get(), need, on.bl());
+    if (st != BL_SUCCESS) failed(st);
+    Ref r0(THPVariable_Wrap(std::move(logp))), r1(THPVariable_Wrap(std::move(entropy))), r2(THPVariable_Wrap(std::move(lse)));
+    Ref r3(THPVariable_Wrap(std::move(top_logp))), r4(THPVariable_Wrap(std::move(top_id)));
+    return PyTuple_Pack(5, r0.o, r1.o, r2.o, r3.o, r4.o);
+}
+
+PyObject *do_score_grad(PyObject *const *a) {
+    const Xent c(a[0], a[1], a[2]);
+    const float *const lse = values_of<const float>(tensor(a[3], "lse"), "lse", at::kFloat, c.h);
+    const float *const entropy = values_of<const float>(tensor(a[4], "entropy"), "entropy", at::kFloat, c.h);
+    const float *const g = values_of<const float>(tensor(a[5], "g"), "g", at::kFloat, c.h);
+    const float *const e = values_of<const float>(tensor(a[6], "e"), "e", at::kFloat, c.h);
+    if (a[7] == Py_False && a[8] == Py_False) refuse(PyExc_ValueError, "dH and dW are both left out");
+    On on(c.h.device(), a[9]);
+    const int64_t need = c.need(1);
+    int64_t lddh, lddw;
+    at::Tensor dh = gradient(a[7], "dH", c.h, &lddh), dw = gradient(a[8], "dW", c.w, &lddw);
+    const c10::DataPtr ws = scratch(need);
+    const int st = bl_score_grad(c.code, c.rows, c.dim, c.vocab, c.h.data_ptr(), c.ldh, c.w.data_ptr(), c.ldw, c.target, lse,
+                                 entropy, g, e, dh.defined() ? dh.data_ptr() : nullptr, lddh,
+                                 dw.defined() ? dw.data_ptr() : nullptr, lddw, ws.get(), need, on.bl());
+    if (st != BL_SUCCESS) failed(st);
+    if (dh.defined()) written(dh);
+    if (dw.defined()) written(dw);
+    return pair(wrapped(dh), wrapped(dw));
+}
+
 // ------------------------------------------------------------------ the module
 
 template <typename F>
@@ -293,9 +336,18 @@ PyObject *py_xent_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 8, [&] { return do_xent_grad(a); });
 }
 
+// score(H, W, target, top, stream)
+PyObject *py_score(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 5, [&] { return do_score(a); });
+}
+// score_grad(H, W, target, lse, entropy, g, e, dH, dW, stream)
+PyObject *py_score_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 10, [&] { return do_score_grad(a); });
+}
+
 #define BL_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {{"init", py_init, METH_O, nullptr}, BL_METHOD(gnorm), BL_METHOD(gclip), BL_METHOD(xent),
-                         BL_METHOD(xent_grad), {nullptr, nullptr, 0, nullptr}};
+                         BL_METHOD(xent_grad), BL_METHOD(score), BL_METHOD(score_grad), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,236 @@
+// Token scores: what follows the products of logits in bl_score.
+//
+//   logp_r = s_r,t(r) - lse_r,   entropy_r = -sum_v p_rv log p_rv,   the `top` largest of s_r, lowest index first
+//
+// Every part of a row (a tile's 128 columns, or a CTA's entries for few rows) leaves its maximum m, the sum S of
+// exp(s - m) and the sum T of exp(s - m) (s - m). Joined, entropy = log S - T / S: neither term is negative, so
+// that nothing cancels for a row that is sure of its token. (S is 1 and more and rounded to 24 bits: the entropies of such
+// rows, as their losses, are exact to a few 2^-24, and -T / S, their larger part, to a relative 2^-18.)
+//
+// The alternatives come from the largest logits of 32-wide blocks: one of the `top` largest logits of a row lies
+// in one of its `top` first blocks, in the order of (largest logit, lower index). Only those blocks' logits are
+// read; the products keep a block's logits only where they may be among them (block_scores).
+#pragma once
+
+#include "xent_gemm.cuh"
+
+namespace bl {
+namespace xent {
+
+constexpr int kMostTop = 32;                      // a warp holds a row's list, a lane each
+
+// (value, index) as one whole number: the larger is the likelier, of equal values the one with the lower index.
+// 0 stands for none.
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t index) {
+    const uint32_t order = static_cast<uint32_t>(in_order(__float_as_int(v + 0.f))) ^ 0x80000000u;     // -0 is +0
+    return v != v ? 0ull : (static_cast<uint64_t>(order) << 32) | (0xffffffffu - index);
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+    return __int_as_float(in_order(static_cast<int32_t>(static_cast<uint32_t>(key >> 32) ^ 0x80000000u)));
+}
+__device__ __forceinline__ uint32_t index_of(uint64_t key) { return 0xffffffffu - static_cast<uint32_t>(key); }
+
+// A warp's list, sorted: lane i holds the i-th. Every lane offers a key (0: none); `top` of the list count.
+struct List {
+    uint64_t mine, least;                         // least: the last that counts
+    __device__ __forceinline__ void start(uint64_t key, int top) {
+        mine = key;
+        least = __shfl_sync(0xffffffffu, mine, top - 1);
+    }
+    __device__ __forceinline__ void offer(uint64_t key, int top) {
+        const int lane = threadIdx.x & 31;
+        uint32_t votes = __ballot_sync(0xffffffffu, key > least);
+        while (votes) {
+            const uint64_t k = __shfl_sync(0xffffffffu, key, __ffs(votes) - 1);
+            votes &= votes - 1;
+            if (k <= least) continue;
+            const int at = __ffs(__ballot_sync(0xffffffffu, k > mine)) - 1;
+            const uint64_t above = __shfl_up_sync(0xffffffffu, mine, 1);
+            mine = lane > at ? above : lane == at ? k : mine;
+            least = __shfl_sync(0xffffffffu, mine, top - 1);
+        }
+    }
+};
+
+// The largest logit of every 32, where the logits come from the kernel for few rows. A warp takes 32 blocks.
+__global__ void __launch_bounds__(256) block_max_kernel(const float *logits, int64_t block_ld, int64_t vocab, int64_t groups,
+                                                        int64_t all, float *block_max) {
+    pdl_release();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (w >= all) return;
+    const int64_t row = w / groups, first = (w - row * groups) * 32;             // the warp's first block
+    const float *const p = logits + row * block_ld * 32;
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t c = first * 32 + i * 128 + lane * 4;
+        v[i] = c < block_ld * 32 ? *reinterpret_cast<const float4 *>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c >= vocab) v[i].x = -INFINITY;
+        if (c + 1 >= vocab) v[i].y = -INFINITY;
+        if (c + 2 >= vocab) v[i].z = -INFINITY;
+        if (c + 3 >= vocab) v[i].w = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float m = fmaxf(fmaxf(v[i].x, v[i].y), fmaxf(v[i].z, v[i].w));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int64_t block = first + i * 4 + lane / 8;
+        if (lane % 8 == 0 && block < block_ld) block_max[row * block_ld + block] = m;
+    }
+}
+
+// The floors of the rows start at minus infinity. (Words that fill a line up to slot_ld stay out of the way.)
+__global__ void __launch_bounds__(256) slots_kernel(int32_t *slots, int64_t count, int top, int slot_ld) {
+    pdl_release();
+    pdl_wait();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < count) slots[i] = i % slot_ld < top ? kLowest : 0x7fffffff;
+}
+
+struct Scores {
+    const int64_t *target;
+    int64_t vocab;
+    int rows;
+    const int *place;             // each row's place among those that count; null: its own
+    // alternatives, of the piece of the vocabulary that starts at v0
+    int top;
+    const float *block_max, *logits;
+    int64_t block_ld, v0, n;
+    uint64_t *best;               // [row][top]: the list so far, where there are several pieces
+    bool first, last;
+    // the last piece: what is left of the rows
+    const float2 *part;
+    const float *part_t, *picked;
+    int64_t part_ld;
+    const int32_t *flags;
+    int flag_count;
+    float *logp, *entropy, *lse, *top_logp;
+    int64_t *top_id;
+};
+
+// WARPS warps share a row: 8 where rows are few, else 1.
+template <int WARPS>
+__global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Scores a) {
+    constexpr int ROWS = 8 / WARPS, HELD = 8;
+    __shared__ uint64_t lists[8][kMostTop];
+    pdl_release();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % WARPS;
+    const int row = blockIdx.x * ROWS + warp / WARPS, top = a.top;
+    const bool bad = a.last && __syncthreads_or(flags_seen(a.flags, a.flag_count)) != 0;
+    int64_t j = -1;
+    if (row < a.rows) j = a.place ? a.place[row] : has_target(a.target, row, a.vocab) ? row : -1;
+    const bool counts = j >= 0;
+    List list;
+    list.start(0, 1);
+    if (top > 0) {
+        uint64_t before = 0;
+        if (counts && !a.first && share == 0 && lane < top) before = a.best[j * top + lane];
+        // blocks: what the list holds already comes first among equals and is no block
+        list.start(before ? before | 0xffffffffull : 0, top);
+        const int64_t blocks = counts ? (a.n + 31) / 32 : 0;
+        const float *const most = a.block_max + (counts ? j : 0) * a.block_ld;
+        for (int64_t b0 = share * 32; b0 < blocks; b0 += WARPS * 32 * HELD) {
+            float m[HELD];
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) {
+                const int64_t b = b0 + h * (WARPS * 32) + lane;
+                m[h] = b < blocks ? most[b] : NAN;
+            }
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) list.offer(key_of(m[h], static_cast<uint32_t>(b0 + h * (WARPS * 32) + lane) + 1), top);
+        }
+        const auto join = [&] {                              // all warps' lists into the first warp's, and back
+            if constexpr (WARPS > 1) {
+                lists[warp][lane] = list.mine;
+                __syncthreads();
+                if (share == 0)
+                    for (int w = 1; w < WARPS; ++w) list.offer(lane < top ? lists[w][lane] : 0, top);
+                __syncthreads();
+            }
+        };
+        join();
+        uint64_t chosen = lane < top ? list.mine : 0;
+        if constexpr (WARPS > 1) {
+            if (share == 0) lists[0][lane] = chosen;
+            __syncthreads();
+            chosen = lists[0][lane];
+            __syncthreads();
+        }
+        // their logits
+        list.start(before, top);
+        const float *const s = a.logits + (counts ? j : 0) * a.block_ld * 32;
+        for (int i0 = share; i0 < top; i0 += WARPS * HELD) {
+            float v[HELD];
+            int64_t at[HELD];
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) {
+                const int i = i0 + h * WARPS;
+                const uint64_t k = __shfl_sync(0xffffffffu, chosen, i & 31);
+                at[h] = i < top && k && index_of(k) ? static_cast<int64_t>(index_of(k) - 1) * 32 + lane : a.n;
+                v[h] = at[h] < a.n ? s[at[h]] : NAN;
+            }
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) list.offer(key_of(v[h], static_cast<uint32_t>(a.v0 + at[h])), top);
+        }
+        join();
+        if (!a.last && counts && share == 0 && lane < top) a.best[j * top + lane] = list.mine;
+    }
+    if (!a.last || row >= a.rows || share != 0) return;
+    float logp = 0.f, entropy = 0.f, lse = 0.f, ref = 0.f, log_sum = 0.f;
+    bool sound = false;
+    if (counts) {
+        const float2 *const p = a.part + j * a.part_ld;
+        const float *const pt = a.part_t + j * a.part_ld;
+        float2 v[HELD];
+        float t[HELD];
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) {
+            const bool in = lane + 32 * h < a.part_ld;
+            v[h] = in ? p[lane + 32 * h] : make_float2(-INFINITY, 0.f);
+            t[h] = in ? pt[lane + 32 * h] : 0.f;
+        }
+        const float picked = a.picked[j];
+        float most = -INFINITY, sum = 0.f, sum_t = 0.f;
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) most = fmaxf(most, v[h].x);
+        for (int64_t i = lane + 32 * HELD; i < a.part_ld; i += 32) most = fmaxf(most, p[i].x);
+        most = warp_max(most);
+        ref = most == -INFINITY ? 0.f : most;
+        const auto add = [&](float2 x, float xt) {
+            const float d = fmaxf(x.x - ref, -1e30f);
+            sum += x.y * expf(x.x - ref);                    // an infinite logit makes NaN here
+            sum_t += expf(d) * fmaf(d, x.y, xt);
+        };
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) add(v[h], t[h]);
+        for (int64_t i = lane + 32 * HELD; i < a.part_ld; i += 32) add(p[i], pt[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            sum_t += __shfl_xor_sync(0xffffffffu, sum_t, o);
+        }
+        log_sum = logf(sum);
+        sound = sum > 0.f && !bad;
+        lse = sound ? ref + log_sum : NAN;
+        // the difference of two logits first, as in the loss: lse has been rounded
+        logp = sound ? (picked - ref) - log_sum : NAN;
+        entropy = sound ? log_sum - sum_t / sum : NAN;
+    }
+    if (lane == 0) {
+        a.logp[row] = logp;
+        a.entropy[row] = entropy;
+        a.lse[row] = lse;
+    }
+    if (lane < top) {
+        const bool there = sound && list.mine != 0;
+        a.top_logp[static_cast<int64_t>(row) * top + lane] = there ? (value_of(list.mine) - ref) - log_sum : counts ? NAN : 0.f;
+        a.top_id[static_cast<int64_t>(row) * top + lane] = there ? static_cast<int64_t>(index_of(list.mine)) : -1;
+    }
+}
+
+}  // namespace xent
+}  // namespace bl

@@ -1,7 +1,10 @@
-// Softmax cross entropy over a large vocabulary and its gradients, without keeping the logits.
+// Softmax cross entropy over a large vocabulary and its gradients, without keeping the logits; and the scores of
+// given tokens (log probability, entropy, the likeliest alternatives) with the gradients of the first two.
 //
 //   s_rv = sum_k H_rk W_vk,  lse_r = log sum_v exp s_rv,  loss_r = lse_r - s_r,t(r)
 //   P_rv = g_r (exp(s_rv - lse_r) - [v = t(r)]),  dH = P W,  dW = P^T H
+//   scores:  logp_r = -loss_r,  entropy_r = -sum_v p_rv log p_rv,
+//            P_rv = g_r ([v = t(r)] - p_rv) - e_r p_rv (log p_rv + entropy_r)
 //
 // The loss is one product over the vocabulary whose tiles leave a maximum and a sum of exponentials
 // each. The gradient computes the logits again, piece of the vocabulary by piece: a piece's P (in
@@ -24,6 +27,7 @@
 
 #include "host.h"
 #include "pdl.cuh"
+#include "score.cuh"
 #include "xent_gemm.cuh"
 
 namespace bl {
@@ -31,16 +35,12 @@ namespace xent {
 
 // ------------------------------------------------------------------ elementwise kernels
 
-__device__ __forceinline__ bool has_target(const int64_t *target, int64_t row, int64_t vocab) {
-    return !target || (target[row] >= 0 && target[row] < vocab);
-}
-
 // One block: the rows that count, in order; each row's place among them (-1: does not count); how
-// many they are, the parts of dH's K axis, and the unit of P (g: or null). The rows that do not count
+// many they are, the parts of dH's K axis, and the unit of P (g, e: or null). The rows that do not count
 // get the results they have (loss, lse: or null).
 __global__ void __launch_bounds__(1024)
     index_kernel(const int64_t *target, int64_t vocab, int rows, int *order, int *place, int *kept, Cut cut,
-                 const float *g, float *unit, float *loss, float *lse) {
+                 const float *g, const float *e, float *unit, float *loss, float *lse) {
     __shared__ int sums[2][32];
     __shared__ float most[32];
     pdl_release();
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(1024)
         before += __shfl_sync(0xffffffffu, upto, 31);
         if (in) {
             place[row] = counts ? at : -1;
-            if (counts && g) m = fmaxf(m, fabsf(g[row]));
+            if (counts && g) m = fmaxf(m, e ? fmaxf(fabsf(g[row]), fabsf(e[row])) : fabsf(g[row]));
             if (counts) order[at] = row;
             else if (loss) loss[row] = lse[row] = 0.f;
         }
@@ -98,7 +98,7 @@ struct Copy {
     int panels;
     int64_t height;
     int vec, blocks;
-    const float *g;           // of the gradient's rows in their places: the unit of P is found on the way
+    const float *g, *e;       // of the gradient's rows in their places: the unit of P is found on the way
     float *unit;
 };
 // Two copies in one launch, H's and the first piece's of W (either may be without blocks).
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ Copy 
     const int block = second ? blockIdx.x - one.blocks : blockIdx.x;
     const Copy &w = second ? two : one;
     if (w.g && block == 0 && threadIdx.x < 32) {
-        const float u = unit_of_rows(w.g, w.target, w.vocab, static_cast<int>(w.rows));
+        const float u = unit_of_rows(w.g, w.e, w.target, w.vocab, static_cast<int>(w.rows));
         if (threadIdx.x == 0) *w.unit = u;
     }
     const int64_t count = w.kept ? *w.kept : w.rows, filled = max((count + w.tile - 1) / w.tile, int64_t(1)) * w.tile;
@@ -146,13 +146,6 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ Copy 
                                                                        bf16x2(p[q][4], p[q][5]), bf16x2(p[q][6], p[q][7]));
         }
     }
-}
-
-// Whether any CTA of the call's products gave up: this thread's share of the flags.
-__device__ __forceinline__ int flags_seen(const int32_t *flags, int count) {
-    int bad = 0;
-    for (int i = threadIdx.x; i < count; i += blockDim.x) bad |= flags[i];
-    return bad;
 }
 
 // One warp a row: join the tiles' maxima and sums. A product that gave up makes every loss NaN.
@@ -237,13 +230,15 @@ constexpr int few_ahead(int R, bool vec) { return (R == 1 ? 4 : 2) * (vec ? 1 : 
 constexpr int few_ctas(int R) { return R == 1 ? 4 : R == 4 ? 2 : 1; }
 constexpr int few_smem(int R) { return 200 * 1024 / few_ctas(R); }      // H's share of the SM's shared memory
 
-template <typename T, int R, bool VEC>
+// With SCORE it leaves the entropy's sums too, and the logits (or null).
+template <typename T, int R, bool VEC, bool SCORE>
 __global__ void __launch_bounds__(256, few_ctas(R))
     few_kernel(const T *H, int64_t ldh, int rows, int dim, const T *W, int64_t ldw, int vocab, const int64_t *target,
-               float2 *part, int64_t part_ld, float *picked) {
+               float2 *part, int64_t part_ld, float *picked, float *part_t, float *logits, int64_t logits_ld) {
     constexpr int N = FewVec<T, VEC>::N, E = few_entries(R), AHEAD = few_ahead(R, VEC);
     extern __shared__ __align__(16) float few_h[];           // [R][dim]
     __shared__ float2 joined[8][R];
+    __shared__ float joined_t[SCORE ? 8 : 1][R];
     pdl_release();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -252,12 +247,12 @@ __global__ void __launch_bounds__(256, few_ctas(R))
         few_h[i] = r < rows ? static_cast<float>(H[r * ldh + k]) : 0.f;
     }
     int64_t at[R];
-    float top[R], sum[R];
+    float top[R], sum[R], sum_t[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         at[r] = r < rows ? target[r] : -1;
         top[r] = -INFINITY;
-        sum[r] = 0.f;
+        sum[r] = sum_t[r] = 0.f;
     }
     __syncthreads();
     const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * E;
@@ -303,11 +298,19 @@ __global__ void __launch_bounds__(256, few_ctas(R))
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                 acc[e][r] = v0 + e < vocab ? s : -INFINITY;
                 if (lane == 0 && v0 + e == at[r] && at[r] < vocab) picked[r] = s;
+                if constexpr (SCORE)
+                    if (lane == 0 && logits && r < rows && v0 + e < vocab) logits[r * logits_ld + v0 + e] = s;
             }
             float m = top[r];
 #pragma unroll
             for (int e = 0; e < E; ++e) m = fmaxf(m, acc[e][r]);
             const float ref = m == -INFINITY ? 0.f : m;
+            if constexpr (SCORE) {                   // as in block_scores
+                const float d = fmaxf(top[r] - ref, -1e30f);
+                sum_t[r] = expf(d) * fmaf(d, sum[r], sum_t[r]);
+#pragma unroll
+                for (int e = 0; e < E; ++e) sum_t[r] += expf(acc[e][r] - ref) * fmaxf(acc[e][r] - ref, -1e30f);
+            }
             float t = sum[r] * expf(top[r] - ref);
 #pragma unroll
             for (int e = 0; e < E; ++e) t += expf(acc[e][r] - ref);
@@ -317,7 +320,10 @@ __global__ void __launch_bounds__(256, few_ctas(R))
     }
     if (lane == 0) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) joined[warp][r] = make_float2(top[r], sum[r]);
+        for (int r = 0; r < R; ++r) {
+            joined[warp][r] = make_float2(top[r], sum[r]);
+            if constexpr (SCORE) joined_t[warp][r] = sum_t[r];
+        }
     }
     __syncthreads();
     if (threadIdx.x < rows) {
@@ -326,6 +332,14 @@ __global__ void __launch_bounds__(256, few_ctas(R))
         const float ref = m == -INFINITY ? 0.f : m;
         for (int q = 0; q < 8; ++q) t += joined[q][threadIdx.x].y * expf(joined[q][threadIdx.x].x - ref);
         part[threadIdx.x * part_ld + blockIdx.x] = make_float2(m, t);
+        if constexpr (SCORE) {
+            float all = 0.f;
+            for (int q = 0; q < 8; ++q) {
+                const float d = fmaxf(joined[q][threadIdx.x].x - ref, -1e30f);
+                all += expf(d) * fmaf(d, joined[q][threadIdx.x].y, joined_t[q][threadIdx.x]);
+            }
+            part_t[threadIdx.x * part_ld + blockIdx.x] = all;
+        }
     }
 }
 
@@ -420,6 +434,8 @@ constexpr int kChunkF32 = 2, kChunkLoss = 16, kChunkFew = 1, kChunkBf16 = 256;
 // 131072 in bf16 and 1024 x 1024 x 32000 in f32 at 64, 128, 512 and 2048 MB: 11.04, 10.84, 10.66, 10.65 ms
 // and 1.22, 1.13, 1.04, 1.04 ms
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
+// Bytes of the logits that a piece's blocks may keep for the alternatives (few of them are written).
+constexpr int64_t kLogitBytes = int64_t(2) << 30;
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t cdiv(int64_t v, int64_t by) { return (v + by - 1) / by; }
@@ -437,6 +453,10 @@ struct Plan {
     int ctas;                 // that share a tile
     int groups;               // CTAs or pairs that the device's SMs hold
     bool copy_h, copy_w, compact, grad;
+    bool score;               // scores (with grad: their gradients)
+    int top;                  // alternatives of a row
+    int64_t block_ld;         // 32-wide blocks of a row's logits in a piece
+    int slot_ld;              // groups of tiles that a row's floor comes from, in whole lines (0: none)
     int few;                  // rows of the kernel for few rows (0: the tiled products)
     bool few_loss;            // the gradient's lse comes from that kernel
     int64_t rows, dim, vocab;
@@ -450,6 +470,7 @@ struct Plan {
     int first_kb;             // 64-deep steps of the first piece
     int64_t slab_rows;        // of dH's partial sums, all parts together
     int64_t ldo;              // row length of dH's partial sums
+    int64_t part_t, block_max, logits, slots, best;
     int64_t flags, kept, unit, order, place, h, w, part, picked, p, dh, bytes;   // offsets into the workspace
 };
 
@@ -472,8 +493,10 @@ int few_rows(int dtype, int64_t rows, int64_t dim, const void *W, int64_t ldw) {
 }
 
 Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, int64_t vocab, const void *W, int64_t ldw,
-              bool grad, int sms) {
+              bool grad, int sms, bool score = false, int top = 0) {
     Plan q{};
+    q.score = score;
+    q.top = top;
     q.planes = dtype == BL_F32 ? 3 : 1;
     q.pairs = dtype == BL_F32 ? 6 : 1;
     q.p_planes = dtype == BL_F32 ? 3 : rows <= kTwoPlaneRows ? 2 : 1;
@@ -498,6 +521,8 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     int64_t most = up(vocab, kTileN);
     if (grad) most = std::min(most, kPieceBytes / (q.tiled * 2 * q.p_planes));
     if (q.copy_w) most = std::min(most, kPieceBytes / (q.panels * 128 * q.planes));
+    const int few = few_rows(dtype, rows, dim, W, ldw);
+    if (top && !few) most = std::min(most, kLogitBytes / (rows * 4));
     most = std::max<int64_t>(most / kTileN * kTileN, 4096);
     q.pieces = cdiv(vocab, most);
     q.piece = up(cdiv(vocab, q.pieces), kTileN);
@@ -512,7 +537,6 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
         if (t == q.wide || cost < least) q.tile_n = t, least = cost;
     }
     q.part_ld = 2 * cdiv(vocab, q.tile_n);
-    const int few = few_rows(dtype, rows, dim, W, ldw);
     q.few_loss = grad && few;
     if (!grad) {
         q.few = few;
@@ -550,6 +574,18 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
     if (!grad) {
         q.part = take(rows * q.part_ld * 8);
         q.picked = take(rows * 4);
+        if (score) q.part_t = take(rows * q.part_ld * 4);
+        if (top) {
+            q.block_ld = cdiv(std::min(q.piece, vocab), 32);
+            q.block_max = take(rows * q.block_ld * 4);
+            q.logits = take(rows * q.block_ld * 128);
+            if (q.pieces > 1) q.best = take(rows * top * 8);
+            // one round of tiles starts before the first of them could raise a floor
+            if (!q.few && tall * cdiv(vocab, q.tile_n) > groups) {
+                q.slot_ld = static_cast<int>(up(top, 4));
+                q.slots = take(rows * q.slot_ld * 4);
+            }
+        }
     } else {
         q.p = take(q.p_planes * q.tiled * q.piece * 2);
         q.dh = take(q.slab_rows * q.ldo * 4);
@@ -693,6 +729,10 @@ struct Call {
     const int64_t *target;
     float *loss, *lse;               // bl_xent
     const float *lse_in, *g;         // bl_xent_grad
+    float *logp, *entropy;           // bl_score, and lse
+    float *top_logp;
+    int64_t *top_id;
+    const float *entropy_in, *e;     // bl_score_grad, and lse_in, g
     void *dH;
     int64_t lddh;
     void *dW;
@@ -724,21 +764,63 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     int flag_count = 0;
     if (q.compact)
         BL_TRY(launch_pdl(index_kernel, 1, 1024, 0, c.s, c.target, c.vocab, rows, order, place, kept,
-                          Cut{q.ctas, dim, q.wide, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.g, unit, c.loss, c.lse));
+                          Cut{q.ctas, dim, q.wide, q.first_kb, q.pairs, static_cast<int>(q.slab_rows), q.groups}, c.g, c.e, unit, c.loss,
+                          c.lse));
+    Scores scores{};
+    if (q.score && !q.grad) {
+        scores.target = c.target, scores.vocab = c.vocab, scores.rows = rows, scores.place = place;
+        scores.top = q.top;
+        scores.block_ld = q.block_ld;
+        scores.n = c.vocab;
+        scores.first = scores.last = true;
+        scores.part = reinterpret_cast<const float2 *>(c.ws + q.part);
+        scores.part_t = reinterpret_cast<const float *>(c.ws + q.part_t);
+        scores.picked = reinterpret_cast<const float *>(c.ws + q.picked);
+        scores.part_ld = q.part_ld;
+        scores.flags = flags;
+        scores.logp = c.logp, scores.entropy = c.entropy, scores.lse = c.lse;
+        scores.top_logp = c.top_logp, scores.top_id = c.top_id;
+        if (q.top) {
+            scores.block_max = reinterpret_cast<const float *>(c.ws + q.block_max);
+            scores.logits = reinterpret_cast<const float *>(c.ws + q.logits);
+            scores.best = reinterpret_cast<uint64_t *>(c.ws + q.best);
+        }
+    }
+    const auto join_scores = [&] {
+        const bool few_rows = c.rows <= 4 * c.sms;         // eight warps a row while all their CTAs run at once
+        return few_rows ? launch_pdl(scores_kernel<8>, static_cast<unsigned>(rows), 256, 0, c.s, scores)
+                        : launch_pdl(scores_kernel<1>, static_cast<unsigned>(cdiv(rows, 8)), 256, 0, c.s, scores);
+    };
     if (q.few) {
         const bool vec = few_vec(c.W, c.ldw, c.dim, sizeof(T));
-        auto kernel = q.few == 1 ? (vec ? few_kernel<T, 1, true> : few_kernel<T, 1, false>) : few_kernel<T, 4, false>;
-        if constexpr (PLANES == 3) {
-            if (q.few == 4 && vec) kernel = few_kernel<T, 4, true>;
-            if (q.few == 8) kernel = vec ? few_kernel<T, 8, true> : few_kernel<T, 8, false>;
-        }
+        const auto pick = [&](auto score) {
+            constexpr bool S = decltype(score)::value;
+            auto kernel = q.few == 1 ? (vec ? few_kernel<T, 1, true, S> : few_kernel<T, 1, false, S>) : few_kernel<T, 4, false, S>;
+            if constexpr (PLANES == 3) {
+                if (q.few == 4 && vec) kernel = few_kernel<T, 4, true, S>;
+                if (q.few == 8) kernel = vec ? few_kernel<T, 8, true, S> : few_kernel<T, 8, false, S>;
+            }
+            return kernel;
+        };
+        const auto kernel = q.score ? pick(std::true_type{}) : pick(std::false_type{});
         float2 *const part = reinterpret_cast<float2 *>(c.ws + q.part);
         float *const picked = reinterpret_cast<float *>(c.ws + q.picked);
-        static std::atomic<unsigned long long> allowed[6];
-        BL_TRY(allow_smem(kernel, few_smem(q.few), allowed[q.few / 4 + 3 * vec]));
+        float *const part_t = q.score ? reinterpret_cast<float *>(c.ws + q.part_t) : nullptr;
+        float *const logits = q.top ? reinterpret_cast<float *>(c.ws + q.logits) : nullptr;
+        static std::atomic<unsigned long long> allowed[12];
+        BL_TRY(allow_smem(kernel, few_smem(q.few), allowed[q.few / 4 + 3 * vec + 6 * q.score]));
         BL_TRY(launch_pdl(kernel, static_cast<unsigned>(q.part_ld), 256, static_cast<size_t>(q.few) * c.dim * 4, c.s,
                           static_cast<const T *>(c.H), c.ldh, rows, dim, static_cast<const T *>(c.W), c.ldw,
-                          static_cast<int>(c.vocab), c.target, part, q.part_ld, picked));
+                          static_cast<int>(c.vocab), c.target, part, q.part_ld, picked, part_t, logits, q.block_ld * 32));
+        if (q.score) {
+            if (q.top) {
+                const int64_t groups = cdiv(q.block_ld, 32), all = groups * c.rows;
+                BL_TRY(launch_pdl(block_max_kernel, static_cast<unsigned>(cdiv(all, 8)), 256, 0, c.s, logits, q.block_ld, c.vocab,
+                                  groups, all, reinterpret_cast<float *>(c.ws + q.block_max)));
+            }
+            BL_TRY(join_scores());
+            return BL_SUCCESS;
+        }
         BL_TRY(launch_pdl(loss_kernel, 1, 256, 0, c.s, part, q.part_ld, picked, c.target, c.vocab, rows, nullptr, nullptr, flags, 0,
                           c.loss, c.lse));
         return BL_SUCCESS;
@@ -748,7 +830,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     Copy copy_h{};
     if (q.copy_h) {
         copy_h = copy_of<T>(c.H, c.ldh, c.rows, c.dim, c.target, c.vocab, order, kept, q.ctas * kTileM, c.ws + q.h, q.tiled, c.sms);
-        if (!q.compact) copy_h.g = c.g, copy_h.unit = unit;
+        if (!q.compact) copy_h.g = c.g, copy_h.e = c.e, copy_h.unit = unit;
         BL_MAP(map_panels(&h_k, c.ws + q.h, q.seen, q.tiled, PLANES * q.panels, kTileM));
     } else {
         BL_MAP(map_bf16(&h_k, c.H, c.dim, c.rows, 1, c.ldh, c.ldh, kTileM));
@@ -763,6 +845,9 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     base.vocab = c.vocab;
     base.g = c.g;
     base.unit = unit;
+    if (q.slot_ld)
+        BL_TRY(launch_pdl(slots_kernel, static_cast<unsigned>(cdiv(c.rows * q.slot_ld, 256)), 256, 0, c.s,
+                          reinterpret_cast<int32_t *>(c.ws + q.slots), c.rows * q.slot_ld, q.top, q.slot_ld));
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t v0 = i * q.piece, n = std::min(q.piece, c.vocab - v0);
         const char *const w_at = static_cast<const char *>(c.W) + v0 * c.ldw * static_cast<int64_t>(sizeof(T));
@@ -795,7 +880,24 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             a.part = reinterpret_cast<float2 *>(c.ws + q.part) + 2 * (v0 / q.tile_n);
             a.part_ld = q.part_ld;
             a.picked = reinterpret_cast<float *>(c.ws + q.picked);
-            BL_TRY((launch_gemm<LOGITS, PLANES>(h_k, w_k, w_k, a, q.ctas, flag_count, c.sms, c.s)));
+            if (!q.score) {
+                BL_TRY((launch_gemm<LOGITS, PLANES>(h_k, w_k, w_k, a, q.ctas, flag_count, c.sms, c.s)));
+                continue;
+            }
+            a.part_t = reinterpret_cast<float *>(c.ws + q.part_t) + 2 * (v0 / q.tile_n);
+            a.top = q.top;
+            if (q.top) {
+                a.block_max = reinterpret_cast<float *>(c.ws + q.block_max);
+                a.logits = reinterpret_cast<float *>(c.ws + q.logits);
+                a.block_ld = q.block_ld;
+                a.slot_ld = q.slot_ld;
+                if (q.slot_ld) a.slots = reinterpret_cast<int32_t *>(c.ws + q.slots);
+            }
+            BL_TRY((launch_gemm<SCORES, PLANES>(h_k, w_k, w_k, a, q.ctas, flag_count, c.sms, c.s)));
+            if (q.top && i + 1 < q.pieces) {
+                scores.v0 = v0, scores.n = n, scores.first = i == 0, scores.last = false;
+                BL_TRY(join_scores());
+            }
             continue;
         }
         char *const pp = c.ws + q.p;
@@ -805,7 +907,13 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         BL_MAP(map_panels(&p_out, pp, q.seen, q.tiled, q.p_planes * p_panels, 32, q.p_planes == 1 ? 128 : 64));
         a.p_panels = static_cast<int>(p_panels);
         a.lse = c.lse_in;
-        BL_TRY((launch_with_p<PROBS, PLANES>(h_k, w_k, p_out, a, q, flag_count, c.sms, c.s)));
+        if (q.score) {
+            a.entropy = c.entropy_in;
+            a.e = c.e;
+            BL_TRY((launch_with_p<SPROBS, PLANES>(h_k, w_k, p_out, a, q, flag_count, c.sms, c.s)));
+        } else {
+            BL_TRY((launch_with_p<PROBS, PLANES>(h_k, w_k, p_out, a, q, flag_count, c.sms, c.s)));
+        }
         if (c.dH) {
             CUtensorMap p_k, sums;
             BL_MAP(map_panels(&p_k, pp, q.seen, q.tiled, q.p_planes * p_panels, kTileM));
@@ -848,7 +956,12 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
     }
     if (t_gave_up) BL_TRY(cudaMemsetAsync(flags, 1, 4, c.s));
     const Spoiled<T> spoiled{static_cast<T *>(c.dW), c.lddw, c.vocab, dim};
-    if (!q.grad) {
+    if (q.score && !q.grad) {
+        const int64_t v0 = (q.pieces - 1) * q.piece;
+        scores.v0 = v0, scores.n = c.vocab - v0, scores.first = q.pieces == 1, scores.last = true;
+        scores.flag_count = flag_count;
+        BL_TRY(join_scores());
+    } else if (!q.grad) {
         BL_TRY(launch_pdl(loss_kernel, static_cast<unsigned>(cdiv(c.rows, 8)), 256, 0, c.s,
                           reinterpret_cast<const float2 *>(c.ws + q.part), q.part_ld, reinterpret_cast<const float *>(c.ws + q.picked),
                           c.target, c.vocab, rows, order, kept, flags, flag_count, c.loss, c.lse));
@@ -935,18 +1048,31 @@ bl_status check_vector(const char *op, const char *name, const void *p, int alig
     return BL_SUCCESS;
 }
 
-bl_status entry(const char *op, int dtype, Call &c, bool grad, void *ws, int64_t ws_bytes, bl_stream_t stream) {
+bl_status check_top(const char *op, int64_t top, int64_t vocab) {
+    if (top < 0 || top > kMostTop || top > vocab)
+        return fail(BL_ERR_INVALID_ARGUMENT, "%s: top=%lld outside [0, %d] or above vocab", op, (long long)top, kMostTop);
+    return BL_SUCCESS;
+}
+
+bl_status entry(const char *op, int dtype, Call &c, bool grad, void *ws, int64_t ws_bytes, bl_stream_t stream, bool score = false,
+                int64_t top = 0) {
     clear_error();
     bl_status st = check_shape(op, dtype, c.rows, c.dim, c.vocab);
+    if (st == BL_SUCCESS) st = check_top(op, top, c.vocab);
     if (st == BL_SUCCESS) st = check_matrix(op, "H", c.H, c.ldh, c.dim, dtype);
     if (st == BL_SUCCESS) st = check_matrix(op, "W", c.W, c.ldw, c.dim, dtype);
     if (st == BL_SUCCESS) st = check_vector(op, "target", c.target, 8);
     if (!grad) {
-        if (st == BL_SUCCESS) st = check_vector(op, "loss", c.loss, 4);
+        if (st == BL_SUCCESS) st = check_vector(op, score ? "logp" : "loss", score ? c.logp : c.loss, 4);
         if (st == BL_SUCCESS) st = check_vector(op, "lse", c.lse, 4);
+        if (st == BL_SUCCESS && score) st = check_vector(op, "entropy", c.entropy, 4);
+        if (st == BL_SUCCESS && top) st = check_vector(op, "top_logp", c.top_logp, 4);
+        if (st == BL_SUCCESS && top) st = check_vector(op, "top_id", c.top_id, 8);
     } else {
         if (st == BL_SUCCESS) st = check_vector(op, "lse", c.lse_in, 4);
         if (st == BL_SUCCESS) st = check_vector(op, "g", c.g, 4);
+        if (st == BL_SUCCESS && score) st = check_vector(op, "entropy", c.entropy_in, 4);
+        if (st == BL_SUCCESS && score) st = check_vector(op, "e", c.e, 4);
         if (st == BL_SUCCESS && !c.dH && !c.dW) st = fail(BL_ERR_INVALID_ARGUMENT, "%s: dH and dW are both NULL", op);
         if (st == BL_SUCCESS && c.dH) st = check_matrix(op, "dH", c.dH, c.lddh, c.dim, dtype);
         if (st == BL_SUCCESS && c.dW) st = check_matrix(op, "dW", c.dW, c.lddw, c.dim, dtype);
@@ -955,21 +1081,38 @@ bl_status entry(const char *op, int dtype, Call &c, bool grad, void *ws, int64_t
     if (st != BL_SUCCESS) return st;
     c.sms = sm_count();
     if (c.sms <= 0) return fail(BL_ERR_CUDA, "%s: cannot query the current CUDA device", op);
-    const Plan q = plan_for(dtype, c.H, c.ldh, c.rows, c.dim, c.vocab, c.W, c.ldw, grad, c.sms);
+    const Plan q = plan_for(dtype, c.H, c.ldh, c.rows, c.dim, c.vocab, c.W, c.ldw, grad, c.sms, score, static_cast<int>(top));
     if (ws_bytes < q.bytes)
         return fail(BL_ERR_INVALID_ARGUMENT, "%s: workspace of %lld bytes is smaller than %lld", op, (long long)ws_bytes,
                     (long long)q.bytes);
     const auto vector = [&](const void *p, int64_t bytes) { return rows_at(p, 1, bytes, bytes, 1); };
     const int64_t es = dtype == BL_F32 ? 4 : 2;
-    Named all[8] = {{"dH", rows_at(c.dH, c.rows, c.dim, c.lddh, es)}, {"dW", rows_at(c.dW, c.vocab, c.dim, c.lddw, es)},
+    Named all[10] = {{"dH", rows_at(c.dH, c.rows, c.dim, c.lddh, es)}, {"dW", rows_at(c.dW, c.vocab, c.dim, c.lddw, es)},
                     {"the workspace", vector(ws, q.bytes)},           {"H", rows_at(c.H, c.rows, c.dim, c.ldh, es)},
                     {"W", rows_at(c.W, c.vocab, c.dim, c.ldw, es)},   {"target", vector(c.target, c.rows * 8)},
                     {"lse", vector(c.lse_in, c.rows * 4)},            {"g", vector(c.g, c.rows * 4)}};
-    if (!grad) {
-        all[0] = {"loss", vector(c.loss, c.rows * 4)};
-        all[1] = {"lse", vector(c.lse, c.rows * 4)};
+    int written = 3, count = 8;
+    if (grad && score) {
+        all[8] = {"entropy", vector(c.entropy_in, c.rows * 4)};
+        all[9] = {"e", vector(c.e, c.rows * 4)};
+        count = 10;
     }
-    st = check_apart(op, all, 3, grad ? 8 : 6);
+    if (!grad) {
+        const Named workspace = all[2], h = all[3], w = all[4], target = all[5];
+        written = count = 0;
+        if (!score) all[written++] = {"loss", vector(c.loss, c.rows * 4)};
+        else all[written++] = {"logp", vector(c.logp, c.rows * 4)};
+        all[written++] = {"lse", vector(c.lse, c.rows * 4)};
+        if (score) all[written++] = {"entropy", vector(c.entropy, c.rows * 4)};
+        if (top) {
+            all[written++] = {"top_logp", vector(c.top_logp, c.rows * top * 4)};
+            all[written++] = {"top_id", vector(c.top_id, c.rows * top * 8)};
+        }
+        all[written++] = workspace;
+        count = written;
+        for (const Named &n : {h, w, target}) all[count++] = n;
+    }
+    st = check_apart(op, all, written, count);
     if (st != BL_SUCCESS) return st;
     c.ws = static_cast<char *>(ws);
     c.s = reinterpret_cast<cudaStream_t>(stream);
@@ -1014,6 +1157,43 @@ bl_status bl_xent_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab,
     c.lse_in = lse, c.g = g;
     c.dH = dH, c.lddh = lddh, c.dW = dW, c.lddw = lddw;
     return bl::xent::entry("xent_grad", dtype, c, true, workspace, workspace_bytes, stream);
+}
+
+int64_t bl_score_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, int64_t top, const void *H, int64_t ldh,
+                           const void *W, int64_t ldw) {
+    using namespace bl::xent;
+    bl::clear_error();
+    if (check_shape("score_workspace", dtype, rows, dim, vocab) != BL_SUCCESS) return -1;
+    if (check_top("score_workspace", top, vocab) != BL_SUCCESS) return -1;
+    const int sms = bl::sm_count();
+    if (sms <= 0) {
+        bl::fail(BL_ERR_CUDA, "score_workspace: cannot query the current CUDA device");
+        return -1;
+    }
+    return plan_for(dtype, H, ldh, rows, dim, vocab, W, ldw, false, sms, true, static_cast<int>(top)).bytes;
+}
+
+bl_status bl_score(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, int64_t top, const void *H, int64_t ldh,
+                   const void *W, int64_t ldw, const int64_t *target, float *logp, float *entropy, float *lse, float *top_logp,
+                   int64_t *top_id, void *workspace, int64_t workspace_bytes, bl_stream_t stream) {
+    bl::xent::Call c{};
+    c.rows = rows, c.dim = dim, c.vocab = vocab;
+    c.H = H, c.ldh = ldh, c.W = W, c.ldw = ldw, c.target = target;
+    c.logp = logp, c.entropy = entropy, c.lse = lse;
+    c.top_logp = top_logp, c.top_id = top_id;
+    return bl::xent::entry("score", dtype, c, false, workspace, workspace_bytes, stream, true, top);
+}
+
+bl_status bl_score_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, const void *H, int64_t ldh, const void *W,
+                        int64_t ldw, const int64_t *target, const float *lse, const float *entropy, const float *g,
+                        const float *e, void *dH, int64_t lddh, void *dW, int64_t lddw, void *workspace,
+                        int64_t workspace_bytes, bl_stream_t stream) {
+    bl::xent::Call c{};
+    c.rows = rows, c.dim = dim, c.vocab = vocab;
+    c.H = H, c.ldh = ldh, c.W = W, c.ldw = ldw, c.target = target;
+    c.lse_in = lse, c.entropy_in = entropy, c.g = g, c.e = e;
+    c.dH = dH, c.lddh = lddh, c.dW = dW, c.lddw = lddw;
+    return bl::xent::entry("score_grad", dtype, c, true, workspace, workspace_bytes, stream, true);
 }
 
 bl_status bl_debug_xent_gave_up(int on) {

@@ -1,9 +1,12 @@
-// The tensor-core products of the softmax cross entropy, one persistent kernel for all four:
+// The tensor-core products of the softmax cross entropy and of token scores, one persistent kernel for all:
 //
 //   LOGITS  s = H W^T           A = H (K-major), B = W (K-major); keeps max and sum of exp per tile
 //   PROBS   s again, then       P = g (exp(s - lse) - onehot) as bf16 planes
 //   DH      dH = P W            A = P (K-major), B = W (MN-major); f32 partial sums
 //   DW      dW = P^T H          A = P (MN-major), B = H (MN-major); stored in W's type
+//   SCORES  s as in LOGITS      keeps the entropy's sum per tile too, the largest logit of every 32, and the
+//                               logits themselves where they may be among a row's likeliest (see score.cuh)
+//   SPROBS  s as in PROBS       P = g (onehot - exp(x)) - e exp(x) (x + entropy), x = s - lse
 //
 // A CTA computes 128 x 256 tiles, or a pair of CTAs 256 x 256 tiles (CTAS = 2: each holds its 128
 // rows of A and of the result and half of B, so B crosses shared memory once for 256 rows). One
@@ -53,7 +56,9 @@
 namespace bl {
 namespace xent {
 
-enum Mode : int { LOGITS = 0, PROBS = 1, DH = 2, DW = 3 };
+enum Mode : int { LOGITS = 0, PROBS = 1, DH = 2, DW = 3, SCORES = 4, SPROBS = 5 };
+__host__ __device__ constexpr bool forms_logits(int mode) { return mode == LOGITS || mode == SCORES; }
+__host__ __device__ constexpr bool forms_p(int mode) { return mode == PROBS || mode == SPROBS; }
 
 constexpr int kTileM = 128, kTileN = 256, kTileK = 64;          // rows are each CTA's
 constexpr int kEpilogueWarps = 8, kHalf = kTileN / 2;           // two warps share 32 rows: 128 columns each
@@ -109,7 +114,15 @@ struct GemmArgs {
     float2 *part;              // LOGITS: [row][part_ld] max and sum
     int64_t part_ld;
     float *picked;             // LOGITS: the target's logit of each row
-    const float *lse, *g;      // PROBS
+    const float *lse, *g;      // PROBS, SPROBS
+    const float *entropy, *e;  // SPROBS
+    // SCORES
+    float *part_t;             // beside `part`: sum of exp(s - max) (s - max)
+    int top;                   // alternatives wanted; 0: none of the following is looked at
+    float *block_max, *logits; // [row][block_ld] largest logit of 32, [row][32 block_ld]
+    int64_t block_ld;
+    int32_t *slots;            // [row][slot_ld] the largest logit of each of `top` groups of tiles so far; or null
+    int slot_ld;
     const float *unit;         // PROBS, DW: the scale of P, below
     int p_panels;              // of a plane of P
     void *out;                 // DW: the result, where its rows do not start on 16-byte boundaries
@@ -226,7 +239,7 @@ __device__ __forceinline__ void split3(float x, float &x0, float &x1, float &x2)
     x2 = fine ? __bfloat162float(__float2bfloat16_rn(r - x1)) : infinite ? x : 0.f;
 }
 
-// P is kept in units of the largest |g| of a row that counts, and dH and dW are multiplied by it in f32
+// P is kept in units of the largest |g| (SPROBS: or |e|) of a row that counts, and dH and dW are multiplied by it in f32
 // at the end: where all rows weigh the same, as in a mean, g then rounds nothing. (P_rv is close to
 // -g at the targets of unsure rows, so g's own rounding to bf16, up to 2^-8, would be the same for all of
 // them: gradients of 1279 rows of equal weight were up to 3.1e-3 off, rounded to bf16 themselves 1.7e-3.)
@@ -237,11 +250,25 @@ __device__ __forceinline__ float warp_max(float m) {
     return m;
 }
 // By all lanes of a warp, for rows in their places (at most a row tile).
-__device__ __forceinline__ float unit_of_rows(const float *g, const int64_t *target, int64_t vocab, int rows) {
+__device__ __forceinline__ float unit_of_rows(const float *g, const float *e, const int64_t *target, int64_t vocab, int rows) {
     float m = 0.f;
     for (int r = threadIdx.x & 31; r < rows; r += 32)
-        if (target[r] >= 0 && target[r] < vocab) m = fmaxf(m, fabsf(g[r]));
+        if (target[r] >= 0 && target[r] < vocab) m = fmaxf(m, e ? fmaxf(fabsf(g[r]), fabsf(e[r])) : fabsf(g[r]));
     return unit_from(warp_max(m));
+}
+
+// Floats in the order of whole numbers.
+__host__ __device__ __forceinline__ int32_t in_order(int32_t bits) { return bits < 0 ? bits ^ 0x7fffffff : bits; }
+constexpr int32_t kLowest = static_cast<int32_t>(0x807fffff);     // minus infinity's place
+
+__device__ __forceinline__ bool has_target(const int64_t *target, int64_t row, int64_t vocab) {
+    return !target || (target[row] >= 0 && target[row] < vocab);
+}
+// Whether any CTA of the call's products gave up: this thread's share of the flags.
+__device__ __forceinline__ int flags_seen(const int32_t *flags, int count) {
+    int bad = 0;
+    for (int i = threadIdx.x; i < count; i += blockDim.x) bad |= flags[i];
+    return bad;
 }
 
 // ---- epilogues. A warp owns 32 rows (a lane each) and 128 columns, in blocks of 32 columns.
@@ -251,7 +278,9 @@ struct Row {              // what an epilogue keeps of its row
     int part_rows;        // DH
     bool counted;
     float top, sum, picked;    // LOGITS
+    float t, floor;            // SCORES
     float lse, g;              // PROBS
+    float entropy, e;          // SPROBS
     float unit;                // PROBS, DW
 };
 
@@ -260,7 +289,7 @@ __device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s,
     r.row = row;
     r.m = s.m;
     if constexpr (MODE == DH) r.part_rows = part_rows(s.m);
-    if constexpr (MODE == LOGITS || MODE == PROBS) {
+    if constexpr (forms_logits(MODE) || forms_p(MODE)) {
         const int n0 = w.tn * a.tile_n;
         const int64_t src = row < s.m ? (a.order ? a.order[row] : row) : -1;
         const int64_t t = src >= 0 ? a.target[src] : -1, at = t - a.v0 - n0;
@@ -268,9 +297,26 @@ __device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s,
         r.at = r.counted && at >= 0 && at < min(a.n - n0, a.tile_n) ? static_cast<int>(at) : -1;
         r.top = -INFINITY;
         r.sum = r.picked = 0.f;
-        if constexpr (MODE == PROBS) {
+        if constexpr (MODE == SCORES) {
+            r.t = 0.f;
+            int32_t least = kLowest;
+            if (a.top > 0 && a.slots && row < s.m) {
+                const int4 *const p = reinterpret_cast<const int4 *>(a.slots + static_cast<int64_t>(row) * a.slot_ld);
+                least = 0x7fffffff;
+                for (int j = 0; j < a.slot_ld / 4; ++j) {
+                    const int4 q = __ldcg(p + j);
+                    least = min(min(least, min(q.x, q.y)), min(q.z, q.w));
+                }
+            }
+            r.floor = __int_as_float(in_order(least));
+        }
+        if constexpr (forms_p(MODE)) {
             r.lse = r.counted ? a.lse[src] : 0.f;
             r.g = r.counted ? a.g[src] / r.unit : 0.f;
+        }
+        if constexpr (MODE == SPROBS) {
+            r.entropy = r.counted ? a.entropy[src] : 0.f;
+            r.e = r.counted ? a.e[src] / r.unit : 0.f;
         }
     }
 }
@@ -304,12 +350,66 @@ __device__ __forceinline__ void block_logits(Row &r, const GemmArgs &a, const Wo
     r.top = m;
 }
 
+// As block_logits, with the entropy's sum. Where alternatives are wanted the block's largest logit is always
+// kept, the logits only where one of them reaches the row's floor: the least of the largest logits of `top`
+// groups of tiles, so that `top` logits at least are as large. What lies below is among no row's likeliest.
+__device__ __forceinline__ void block_scores(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
+    const int left = a.n - w.tn * a.tile_n - c0;
+    if (left < 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i < left ? v[i] : -INFINITY;
+    }
+    const uint32_t hit = r.at >= c0 && r.at < c0 + 32 ? 1u << (r.at - c0) : 0u;
+    float most = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (hit >> i & 1) r.picked = v[i];
+        most = fmaxf(most, v[i]);
+    }
+    if (a.top > 0 && r.row < r.m) {
+        const int64_t block = r.row * a.block_ld + (w.tn * a.tile_n + c0) / 32;
+        a.block_max[block] = most;
+        if (most >= r.floor) {
+            float4 *const p = reinterpret_cast<float4 *>(a.logits + block * 32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+    }
+    const float m = fmaxf(r.top, most), ref = m == -INFINITY ? 0.f : m;
+    // Moving the reference by d: sum of e (x + d) = t + d sum, all times exp(d). Nothing is left of tiles whose
+    // exponentials are 0, and an infinite d (no tile before) must not meet that 0.
+    const float d = fmaxf(r.top - ref, -1e30f), scale = exp2f(d * kLog2e);
+    r.t = scale * fmaf(d, r.sum, r.t);
+    r.sum *= scale;
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float at = v[i] - ref;
+        v[i] = exp2f(at * kLog2e);
+        x[i] = v[i] * fmaxf(at, -1e30f);           // a logit of minus infinity: 0 times a finite number
+    }
+    // pairwise, as in block_logits; every term of the second sum has one sign
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) v[i] += v[i + o], x[i] += x[i + o];
+    r.sum += v[0];
+    r.t += x[0];
+    r.top = m;
+}
+
 template <int MODE>
 __device__ __forceinline__ void end(const Row &r, const GemmArgs &a, const Work &w, int half) {
-    if constexpr (MODE == LOGITS) {
+    if constexpr (forms_logits(MODE)) {
         if (r.row < r.m) {
             a.part[r.row * a.part_ld + 2 * w.tn + half] = make_float2(r.top, r.sum);
             if (r.at >= half * kHalf && r.at < (half + 1) * kHalf) a.picked[r.row] = r.picked;
+            if constexpr (MODE == SCORES) {
+                a.part_t[r.row * a.part_ld + 2 * w.tn + half] = r.t;
+                if (a.top > 0 && a.slots && r.top > r.floor)
+                    atomicMax(a.slots + static_cast<int64_t>(r.row) * a.slot_ld + (2 * w.tn + half) % a.top,
+                              in_order(__float_as_int(r.top)));
+            }
         }
     }
 }
@@ -368,6 +468,15 @@ template <int MODE, int PLANES>
 __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const Work &w, int c0, int cols, float (&v)[32],
                                           const CUtensorMap *map, unsigned char *stage) {
     const int n0 = w.tn * a.tile_n, row0 = r.row - (threadIdx.x & 31);
+    if constexpr (MODE == SPROBS) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float x = v[i] - r.lse, e = PLANES == 3 ? expf(x) : exp2f(x * kLog2e);
+            const float g = i == r.at - c0 ? e - 1.f : e;           // where p is near 1 the difference is what counts
+            const float p = fmaf(r.e * e, fmaxf(x, -1e30f) + r.entropy, r.g * g);    // the floor as in block_scores
+            v[i] = r.counted && n0 + c0 + i < a.n ? -p : 0.f;
+        }
+    }
     if constexpr (MODE == PROBS) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -383,9 +492,9 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
         for (int i = 0; i < 32; ++i) v[i] *= r.unit;
     }
     // where the rows that count are copied together P has whole row tiles: dW multiplies their zeros
-    const bool there = row0 < r.m || (MODE == PROBS && a.kept != nullptr);
-    if constexpr (MODE == DH || PLANES == 3 || (MODE == PROBS && PLANES == 2)) {
-        if constexpr (MODE == PROBS) {
+    const bool there = row0 < r.m || (forms_p(MODE) && a.kept != nullptr);
+    if constexpr (MODE == DH || PLANES == 3 || (forms_p(MODE) && PLANES == 2)) {
+        if constexpr (forms_p(MODE)) {
             // planes of 32 values: 64 bytes a line each
 #pragma unroll
             for (int pl = 0; pl < PLANES; ++pl) {
@@ -417,7 +526,7 @@ __device__ __forceinline__ void block_out(const Row &r, const GemmArgs &a, const
         put_bf16(stage, c0, v);
         if ((c0 & 32) || c0 + 32 >= cols) {
             if (MODE == DW && a.out) lines_copy<__nv_bfloat16>(a, stage, row0, n0 + (c0 & ~63));
-            else if (there && MODE == PROBS) lines_store(map, stage, 0, row0, (n0 + c0) / 64, false);
+            else if (there && forms_p(MODE)) lines_store(map, stage, 0, row0, (n0 + c0) / 64, false);
             else if (there) lines_store(map, stage, n0 + (c0 & ~63), row0, 0, false);
         }
     }
@@ -427,6 +536,7 @@ template <int MODE, int PLANES>
 __device__ __forceinline__ void block(Row &r, const GemmArgs &a, const Work &w, int c0, int cols, float (&v)[32],
                                       const CUtensorMap *map, unsigned char *stage) {
     if constexpr (MODE == LOGITS) block_logits(r, a, w, c0, v);
+    else if constexpr (MODE == SCORES) block_scores(r, a, w, c0, v);
     else block_out<MODE, PLANES>(r, a, w, c0, cols, v, map, stage);
 }
 
@@ -441,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int BLOCKS = kHalf / 32;                        // a warp's columns
     // Chunks of K are added in registers. Where one chunk is all there is, the results of bf16 operands go out block
     // by block as they leave tensor memory instead.
-    constexpr bool MAY_BE_DIRECT = MODE != LOGITS && PLANES != 3;
+    constexpr bool MAY_BE_DIRECT = !forms_logits(MODE) && PLANES != 3;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kStageA;
@@ -596,13 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char *const stage = staging + (warp - 4) * kStageBytes;
         const Shape sh = shape_of<MODE, CTAS>(a);
         float unit = 1.f;
-        if constexpr (MODE == PROBS || MODE == DW) unit = *a.unit;
+        if constexpr (forms_p(MODE) || MODE == DW) unit = *a.unit;
         uint32_t done = 0;
         bool ok = true;
         for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
             const Work k = work_of(w, a, sh);
             int cols = min(a.n - k.tn * a.tile_n, a.tile_n);                   // this warp's columns end there
-            if (MODE == PROBS) cols = (cols + 63) & ~63;
+            if (forms_p(MODE)) cols = (cols + 63) & ~63;
             cols = min(cols, (half + 1) * kHalf);
             Row r;
             r.unit = unit;
@@ -670,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             end<MODE>(r, a, k, half);
         }
-        if (MODE != LOGITS && lane == 0) tc::bulk_wait_all();
+        if (!forms_logits(MODE) && lane == 0) tc::bulk_wait_all();
     }
     __syncwarp();
     tc::fence_before_sync();
