@@ -242,6 +242,33 @@ bl_status bl_score_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab
 int64_t bl_score_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab, int64_t top, const void *H,
                            int64_t ldh, const void *W, int64_t ldw);
 
+/*
+ * bl_orth -- orthogonalised steps: `steps` Newton-Schulz products on each of `batch` matrices,
+ *     X_0 = G / |G|_F,   A = X X^T (X^T X if X has more rows than columns),   X <- a X + (b A + c A A) X
+ * which keeps G's singular vectors and takes every singular value s to a s + b s^3 + c s^5 at each step.
+ *
+ *   dtype     BL_BF16 or BL_F32, of G and X.
+ *   rows, cols  1 .. 2^16 each.    batch  1 .. 2^20; 2^40 elements in all at most.
+ *   G         device pointer, ldg >= rows (one column: any); items stride_g >= 0 apart, in any order of memory.
+ *   X         the result, laid out by ldx and stride_x: no two elements of it share memory. It may be G, or overlap G.
+ *   steps     1 .. 64.
+ *   coefficients  HOST double[3]: a, b, c (read before the call returns). (3.4445, -4.7750, 2.0315) takes all
+ *             but the smallest singular values to about 0.7 .. 1.2 in five steps; (1.5, -0.5, 0) converges to 1.
+ *   workspace at least bl_orth_workspace(...) bytes, 256-byte aligned, free again once the call's work has
+ *             completed on the stream; it overlaps neither G nor X.
+ * The norm is exact for any finite values. A matrix of zeros gives zeros, one that holds infinity or NaN gives NaN.
+ * a X is formed from 22 bits of X in f32. The products take f16 operands, of 11 bits for bf16 and of 22 bits for
+ * f32 matrices, and add in f32. Between steps X must stay below 8 and A below 16 in every element, as any
+ * converging coefficients keep it; beyond that the result is not finite. The same call gives the same bits every time,
+ * whatever else is in the batch. A kernel that gave up waiting makes all of X NaN.
+ */
+bl_status bl_orth(bl_dtype dtype, int64_t rows, int64_t cols, int64_t batch, const void *G, int64_t ldg,
+                  int64_t stride_g, void *X, int64_t ldx, int64_t stride_x, int steps, const double *coefficients,
+                  void *workspace, int64_t workspace_bytes, bl_stream_t stream);
+
+/* Bytes of workspace that bl_orth needs on the current device (-1: the arguments are invalid). */
+int64_t bl_orth_workspace(bl_dtype dtype, int64_t rows, int64_t cols, int64_t batch);
+
 /* Static, human-readable name of a status code. */
 const char *bl_status_string(bl_status status);
 
@@ -300,8 +327,8 @@ bl_status bl_debug_tc_tile_f32(const float *A, const float *B, float *C, int32_t
                                bl_stream_t stream);
 
 /*
- * Diagnostic: with on != 0 the calling thread's bl_xent, bl_xent_grad, bl_score and bl_score_grad report,
- * from then on, that one of their matrix products gave up waiting, although none did: what a caller sees of it
+ * Diagnostic: with on != 0 the calling thread's bl_xent, bl_xent_grad, bl_score, bl_score_grad and bl_orth
+ * report, from then on, that one of their matrix products gave up waiting, although none did: what a caller sees of it
  * can be tested. on = 0 ends that. (The kernel for few rows of the first and third waits for nothing and
  * reports nothing.)
  */

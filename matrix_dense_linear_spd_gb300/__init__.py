@@ -1,5 +1,5 @@
 """Batched Cholesky factorisation (potrf) and SPD solves (posv, potrs) on GB300, and the
-operators of a training step around them (xent, xent_grad, score, score_grad, gnorm, gclip).
+operators of a training step around them (xent, xent_grad, score, score_grad, orth, gnorm, gclip).
 
 Thin ctypes binding over ``libbl.so`` (the C ABI in ``include/bl.h``). This module only
 marshals arguments: every step of the computation runs in the library's CUDA kernels. There is
@@ -27,7 +27,7 @@ EXPORTED = ("bl_potrf", "bl_posv", "bl_potrs", "bl_status_string", "bl_last_erro
             "bl_version", "bl_set_route", "bl_num_routes", "bl_route_name", "bl_route_capacity",
             "bl_select_debug", "bl_debug_tc_tile_f32", "bl_debug_peak", "bl_gnorm", "bl_gclip",
             "bl_gnorm_workspace", "bl_xent", "bl_xent_grad", "bl_xent_workspace", "bl_debug_xent_gave_up",
-            "bl_score", "bl_score_grad", "bl_score_workspace")
+            "bl_score", "bl_score_grad", "bl_score_workspace", "bl_orth", "bl_orth_workspace")
 
 
 class BLError(RuntimeError):
@@ -88,6 +88,10 @@ def _load():
     lib.bl_score_grad.restype = ctypes.c_int
     lib.bl_score_workspace.argtypes = [ctypes.c_int, i64, i64, i64, i64, vp, i64, vp, i64]
     lib.bl_score_workspace.restype = i64
+    lib.bl_orth.argtypes = [ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, i64, i64, ctypes.c_int, vp, vp, i64, vp]
+    lib.bl_orth.restype = ctypes.c_int
+    lib.bl_orth_workspace.argtypes = [ctypes.c_int, i64, i64, i64]
+    lib.bl_orth_workspace.restype = i64
     return lib
 
 
@@ -324,3 +328,12 @@ def score_grad(H, W, target, lse, entropy, g, e, dH=None, dW=None, stream=None):
     """Gradients of sum_r g_r logp_r + e_r entropy_r: (dH, dW) in H's and W's type, given score's lse and
     entropy; g and e are f32, one value a row. dH and dW as in xent_grad. Not recorded by autograd."""
     return (_binding or _training()).score_grad(H, W, target, lse, entropy, g, e, dH, dW, _raw(stream))
+
+
+def orth(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), out=None, stream=None):
+    """Orthogonalised step: X = G / |G|, then `steps` times X <- a X + (b A + c A A) X with A = X X^T (on the
+    shorter side), which keeps the singular vectors and takes the singular values towards 1. G is one matrix
+    (rows, cols) or a batch (batch, rows, cols), bf16 or f32, whose rows or columns are contiguous; the result has
+    its shape, type and memory order. `out` may be a tensor to write to, contiguous in the same direction; it may
+    be G itself. Not recorded by autograd."""
+    return (_binding or _training()).orth(G, steps, coefficients, out, _raw(stream))

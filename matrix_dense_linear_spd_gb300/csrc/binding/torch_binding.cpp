@@ -292,6 +292,64 @@ PyObject *do_score_grad(PyObject *const *a) {
     return pair(wrapped(dh), wrapped(dw));
 }
 
+// ------------------------------------------------------------------ orth
+
+// A matrix or a batch of them as lines of contiguous values: rows, or columns (turned).
+struct Lines {
+    int64_t batch, lines, width, ld, stride;
+    Lines(const at::Tensor &t, bool turned) {
+        const int64_t d = t.dim(), l = turned ? d - 1 : d - 2, w = turned ? d - 2 : d - 1;
+        batch = d == 3 ? t.size(0) : 1;
+        lines = t.size(l), width = t.size(w);
+        ld = lines > 1 ? t.stride(l) : std::max<int64_t>(width, 1);
+        stride = batch > 1 ? t.stride(0) : std::max<int64_t>(ld * lines, 1);
+    }
+    static bool fits(const at::Tensor &t, bool turned) {
+        const int64_t w = turned ? t.dim() - 2 : t.dim() - 1;
+        return t.size(w) <= 1 || t.stride(w) == 1;
+    }
+};
+
+PyObject *do_orth(PyObject *const *a) {
+    const at::Tensor &g = tensor(a[0], "G");
+    if (g.scalar_type() != at::kFloat && g.scalar_type() != at::kBFloat16)
+        refuse(PyExc_TypeError, "unsupported dtype %s", c10::toString(g.scalar_type()));
+    const bl_dtype code = g.scalar_type() == at::kFloat ? BL_F32 : BL_BF16;
+    if (g.dim() != 2 && g.dim() != 3) refuse(PyExc_ValueError, "G must be (rows, cols) or (batch, rows, cols)");
+    if (!g.is_cuda()) refuse(PyExc_ValueError, "G must be a CUDA tensor");
+    const long steps = PyLong_AsLong(a[1]);
+    if (steps == -1 && PyErr_Occurred()) throw Refused();
+    Ref three(PySequence_Fast(a[2], "coefficients must be three numbers"));
+    if (PySequence_Fast_GET_SIZE(three.o) != 3) refuse(PyExc_ValueError, "coefficients must be three numbers");
+    double coefficients[3];
+    for (int i = 0; i < 3; ++i) {
+        coefficients[i] = PyFloat_AsDouble(PySequence_Fast_GET_ITEM(three.o, i));
+        if (PyErr_Occurred()) throw Refused();
+    }
+    at::Tensor out;
+    if (a[3] != Py_None) {
+        out = tensor(a[3], "out");
+        if (out.scalar_type() != g.scalar_type() || out.sizes() != g.sizes() || out.device() != g.device())
+            refuse(PyExc_ValueError, "out must have G's type, shape and device");
+    }
+    bool turned = !Lines::fits(g, false) || (out.defined() && !Lines::fits(out, false));
+    if (!Lines::fits(g, turned)) refuse(PyExc_ValueError, "G's rows or columns must be contiguous");
+    if (out.defined() && !Lines::fits(out, turned)) refuse(PyExc_ValueError, "out must be contiguous in the direction that G is");
+    On on(g.device(), a[4]);
+    if (!out.defined()) {
+        out = turned ? at::empty(g.transpose(-2, -1).sizes(), g.options()).transpose(-2, -1) : at::empty(g.sizes(), g.options());
+    }
+    const Lines from(g, turned), to(out, turned);
+    const int64_t need = bl_orth_workspace(code, from.width, from.lines, from.batch);
+    if (need < 0) failed(BL_ERR_INVALID_ARGUMENT);
+    const c10::DataPtr ws = scratch(need);
+    const int st = bl_orth(code, from.width, from.lines, from.batch, g.data_ptr(), from.ld, from.stride, out.data_ptr(), to.ld, to.stride,
+                           steps < 0 || steps > 1000 ? -1 : static_cast<int>(steps), coefficients, ws.get(), need, on.bl());
+    if (st != BL_SUCCESS) failed(st);
+    written(out);
+    return THPVariable_Wrap(std::move(out));
+}
+
 // ------------------------------------------------------------------ the module
 
 template <typename F>
@@ -345,9 +403,14 @@ PyObject *py_score_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 10, [&] { return do_score_grad(a); });
 }
 
+// orth(G, steps, coefficients, out, stream)
+PyObject *py_orth(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 5, [&] { return do_orth(a); });
+}
+
 #define BL_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {{"init", py_init, METH_O, nullptr}, BL_METHOD(gnorm), BL_METHOD(gclip), BL_METHOD(xent),
-                         BL_METHOD(xent_grad), BL_METHOD(score), BL_METHOD(score_grad), {nullptr, nullptr, 0, nullptr}};
+                         BL_METHOD(xent_grad), BL_METHOD(score), BL_METHOD(score_grad), BL_METHOD(orth), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -14,6 +14,9 @@ void clear_error();
 // SMs of the current device (cached per device); 0 if it cannot be queried.
 int sm_count();
 
+// Whether this thread's calls report that a product gave up waiting (bl_debug_xent_gave_up).
+bool &gave_up_wanted();
+
 // Bytes [lo, hi) of memory that a call reads or writes.
 struct Range {
     uintptr_t lo, hi;

@@ -1,0 +1,21 @@
+// Launches of the orthogonalisation's products, compiled in a translation unit for each number of planes.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace bl {
+namespace orth {
+
+struct Args;
+
+// How a product reads its operands (see orth_gemm.cuh).
+enum Layout : int { GRAM_LINES = 0, GRAM_WIDTH = 1, SQUARE = 0, APPLY_LEFT = 2, APPLY_RIGHT = 3 };
+
+cudaError_t launch_one(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const Args &a,
+                       int sms, cudaStream_t s);
+cudaError_t launch_two(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const Args &a,
+                       int sms, cudaStream_t s);
+
+}  // namespace orth
+}  // namespace bl

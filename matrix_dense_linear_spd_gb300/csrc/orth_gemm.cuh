@@ -1,0 +1,470 @@
+// The tensor-core products of the orthogonalisation (orth.cu), one persistent kernel for all. With X stored as
+// `lines` rows of `width` contiguous values, A its Gram matrix on the shorter side and B = b A + c A A:
+//
+//   SYMMETRIC  A = X X^T or X^T X (K-major operands, or both MN-major), and B from A A (K-major)
+//   APPLY      a X + B X (K-major, MN-major) or a X + X B (both K-major)
+//
+// Everything between the products is f16 in two planes, x = hi + lo (22 bits), scaled by a power of two so that no
+// value leaves f16's range. PLANES = 1 multiplies the hi planes only; PLANES = 2 adds hi lo + lo hi + hi hi, which
+// leaves out 2^-22 of a product. The term a X is added from both planes in f32 in the epilogue in either case:
+// what the iteration multiplies by a in every step, the directions of small singular values, keeps 22 bits, and the
+// products' own rounding meets only directions that have grown (see orth.cu).
+//
+// A and B are symmetric: tiles above the diagonal are left out, and every 32 x 32 block below it is stored twice,
+// the second time transposed through shared memory, which also makes the results symmetric to the bit.
+//
+// A CTA computes 128 x tile_n tiles, or a pair of CTAs 256 x tile_n tiles (each holds its 128 rows and half of B).
+// Roles, waits and registers as in xent_gemm.cuh: a producer thread for each operand, one issuing thread, eight
+// epilogue warps that work on one accumulator of tensor memory while the next tile is added up in the other. With
+// PLANES = 2 the chain of K is cut into chunks that are added in registers: tensor memory's f32 sums cut where f32
+// would round, up to 2^-23.4 of the sum a step for the diagonal of A.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "pdl.cuh"
+#include "tma_sm100.cuh"
+
+namespace bl {
+namespace orth {
+
+enum Kind : int { SYMMETRIC = 0, APPLY = 1 };
+
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kEpilogueWarps = 8, kHalf = kTileN / 2;
+constexpr int kStageBytes = 32 * 128;
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
+static_assert(128 * kRegsFew + 32 * kEpilogueWarps * kRegsMany <= kThreads * kRegsLaunch, "more registers than the block has");
+constexpr uint32_t kPolls = 1u << 22;
+
+template <int PLANES, int CTAS>
+struct Ring {
+    static constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN / CTAS * kTileK * 2;
+    static constexpr int kStageA = PLANES * kBytesA, kStageB = PLANES * kBytesB;
+    static constexpr int kStages = 192 * 1024 / (kStageA + kStageB);
+    static constexpr int kSmem = kStages * (kStageA + kStageB) + kEpilogueWarps * kStageBytes + 1024;
+};
+
+struct Args {
+    int batch;
+    int rows, cols;            // of the product, of each item
+    int kblocks, chunk;        // 64-deep steps; how many are added in tensor memory before registers take over
+    int tile_n, tiles_m, tiles_n;
+    int per_item, total;       // tiles
+    float alpha, beta;         // result = alpha * product + beta * (add_hi + add_lo)
+    const __half *add_hi, *add_lo;      // [item][rows][add_ld], or null
+    int64_t add_ld;
+    int planes_out;            // of the f16 result
+    bool last;                 // APPLY: the result is the caller's, f32 or bf16
+    void *out;                 // where its lines do not start on 16-byte boundaries: stored without TMA
+    int64_t ldo, stride_o;
+    int32_t *gave_up;
+};
+
+struct Work {
+    int item, tm, tn;
+};
+template <int KIND, int CTAS>
+__device__ __forceinline__ Work work_of(int w, const Args &a) {
+    Work r;
+    r.item = w / a.per_item;
+    w -= r.item * a.per_item;
+    if constexpr (KIND == SYMMETRIC) {
+        // row tile after row tile, as many columns as reach its last row's diagonal
+        r.tm = 0;
+        while (true) {
+            const int n = min(a.tiles_n, ((r.tm + 1) * (CTAS * kTileM) + a.tile_n - 1) / a.tile_n);
+            if (w < n) break;
+            w -= n;
+            ++r.tm;
+        }
+        r.tn = w;
+    } else {
+        r.tm = w / a.tiles_n;
+        r.tn = w - r.tm * a.tiles_n;
+    }
+    return r;
+}
+// Columns of the tile that the product has, rounded up to what the instruction (a pair: each CTA's half; an
+// MN-major operand: whole groups of 64) can take.
+template <bool B_MN, int CTAS>
+__device__ __forceinline__ int cols_of(int tn, const Args &a) {
+    constexpr int UNIT = CTAS == 1 ? 16 : B_MN ? 128 : 32;
+    const int left = min(a.cols - tn * a.tile_n, a.tile_n);
+    return (left + UNIT - 1) & ~(UNIT - 1);
+}
+
+__device__ __forceinline__ uint32_t pack(__half lo, __half hi) {
+    const __half2 t = __halves2half2(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+
+// A warp's 32 lines on their way out: 64 bytes each (two planes fit the stage) in the 64-byte swizzle.
+__device__ __forceinline__ uint32_t at64(int line, int chunk) { return line * 64 + ((chunk ^ ((line >> 1) & 3)) << 4); }
+__device__ __forceinline__ void lines_free() {          // the last store has read its lines
+    if ((threadIdx.x & 31) == 0) tc::bulk_wait_read_all();
+    __syncwarp();
+}
+__device__ __forceinline__ void lines_store(const CUtensorMap *map, const unsigned char *stage, int x, int y, int z0, int z1) {
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        tc::tma_store_3d(map, stage, x, y, z0, false);
+        if (z1 >= 0) tc::tma_store_3d(map, stage + 2048, x, y, z1, false);
+        tc::bulk_commit();
+    }
+}
+
+struct Addend {
+    uint4 hi[4], lo[4];
+};
+// 32 columns of this lane's row of what the product is added to.
+__device__ __forceinline__ void fetch(Addend &d, const Args &a, const Work &w, int row, int col, bool there) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d.hi[j] = d.lo[j] = make_uint4(0, 0, 0, 0);
+    if (!there || !a.add_hi) return;
+    const int64_t at = (static_cast<int64_t>(w.item) * a.rows + row) * a.add_ld + col;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d.hi[j] = *reinterpret_cast<const uint4 *>(a.add_hi + at + 8 * j);
+    if (!a.add_lo) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d.lo[j] = *reinterpret_cast<const uint4 *>(a.add_lo + at + 8 * j);
+}
+__device__ __forceinline__ float2 sum2(uint32_t hi, uint32_t lo) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hi)), y = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    return make_float2(x.x + y.x, x.y + y.y);
+}
+__device__ __forceinline__ void combine(float (&v)[32], const Addend &d, const Args &a) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t h[4] = {d.hi[j].x, d.hi[j].y, d.hi[j].z, d.hi[j].w}, l[4] = {d.lo[j].x, d.lo[j].y, d.lo[j].z, d.lo[j].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 x = sum2(h[q], l[q]);
+            v[8 * j + 2 * q] = fmaf(a.alpha, v[8 * j + 2 * q], a.beta * x.x);
+            v[8 * j + 2 * q + 1] = fmaf(a.alpha, v[8 * j + 2 * q + 1], a.beta * x.y);
+        }
+    }
+}
+
+// 32 columns of a warp's 32 rows; `row0`, `col0`: where the block starts.
+template <int KIND, int PLANES>
+__device__ __forceinline__ void block_out(const Args &a, const Work &w, int row0, int col0, float (&v)[32], const CUtensorMap *map,
+                                          unsigned char *stage) {
+    const int lane = threadIdx.x & 31;
+    if (KIND == APPLY && a.last) {
+        using T = std::conditional_t<PLANES == 1, __nv_bfloat16, float>;
+        lines_free();
+        if constexpr (PLANES == 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(stage + at64(lane, j)) = make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                                                               bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+        if (!a.out) {
+            lines_store(map, stage, col0, row0, w.item, -1);
+            return;
+        }
+        __syncwarp();
+        T *p = static_cast<T *>(a.out) + w.item * a.stride_o + row0 * a.ldo + col0 + lane;
+        const int rows = min(32, a.rows - row0);
+        for (int q = 0; q < rows; ++q, p += a.ldo) {
+            T x;
+            if constexpr (PLANES == 1) x = *reinterpret_cast<const T *>(stage + at64(q, lane >> 3) + (lane & 7) * 2);
+            else x = *reinterpret_cast<const T *>(stage + q * 128 + (((lane >> 2) ^ (q & 7)) << 4) + (lane & 3) * 4);
+            if (col0 + lane < a.cols) *p = x;
+        }
+        __syncwarp();
+        return;
+    }
+    const int z1 = a.planes_out == 2 ? a.batch + w.item : -1;
+    __half hi[32], lo[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        hi[i] = __float2half_rn(v[i]);
+        lo[i] = __float2half_rn(v[i] - __half2float(hi[i]));
+    }
+    lines_free();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        *reinterpret_cast<uint4 *>(stage + at64(lane, j)) = make_uint4(pack(hi[8 * j], hi[8 * j + 1]), pack(hi[8 * j + 2], hi[8 * j + 3]),
+                                                                       pack(hi[8 * j + 4], hi[8 * j + 5]), pack(hi[8 * j + 6], hi[8 * j + 7]));
+        if (z1 >= 0)
+            *reinterpret_cast<uint4 *>(stage + 2048 + at64(lane, j)) = make_uint4(pack(lo[8 * j], lo[8 * j + 1]), pack(lo[8 * j + 2], lo[8 * j + 3]),
+                                                                                  pack(lo[8 * j + 4], lo[8 * j + 5]), pack(lo[8 * j + 6], lo[8 * j + 7]));
+    }
+    lines_store(map, stage, col0, row0, w.item, z1);
+    if (KIND == SYMMETRIC && row0 > col0) {
+        // the same block in its place above the diagonal: line i is column i, a lane's value at the lane's place
+        lines_free();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            *reinterpret_cast<__half *>(stage + at64(i, lane >> 3) + (lane & 7) * 2) = hi[i];
+            if (z1 >= 0) *reinterpret_cast<__half *>(stage + 2048 + at64(i, lane >> 3) + (lane & 7) * 2) = lo[i];
+        }
+        lines_store(map, stage, row0, col0, w.item, z1);
+    }
+}
+
+template <int KIND, bool A_MN, bool B_MN, int PLANES, int CTAS>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Args a) {
+    using R = Ring<PLANES, CTAS>;
+    constexpr int kBytesA = R::kBytesA, kBytesB = R::kBytesB, kStageA = R::kStageA, kStageB = R::kStageB, kStages = R::kStages;
+    constexpr int PAIRS = PLANES == 1 ? 1 : 3, BLOCKS = kHalf / 32;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+    unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kStageA;
+    unsigned char *const staging = base + kStages * (kStageA + kStageB);
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const uint32_t rank = CTAS == 1 ? 0 : tc::cluster_rank();
+    if (warp == 1) tc::tmem_take<CTAS>(&tmem_slot, 512);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&acc_full[s], 1);
+            tc::mbar_init(&acc_empty[s], CTAS * kEpilogueWarps);
+        }
+        tc::mbar_init(&drained, 1);
+        tc::mbar_fence_init();
+        gave_up = 0;
+        tc::tma_prefetch_map(&map_a);
+        tc::tma_prefetch_map(&map_b);
+        tc::tma_prefetch_map(&map_out);
+    }
+    __syncwarp();
+    pdl_release();
+    tc::fence_before_sync();
+    if constexpr (CTAS == 1) __syncthreads();
+    else tc::cluster_sync();                 // the peer's barriers are ready too
+    tc::fence_after_sync();
+    pdl_wait();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < 4) {
+      tc::regs_dec<kRegsFew>();
+      if (warp == 0 || warp == 2) {
+        if (lane == 0) {
+            const bool for_a = warp == 0, announce = for_a && rank == 0;
+            const uint32_t bar0 = CTAS == 1 ? tc::smem_u32(full) : tc::at_leader(full);
+            uint32_t s = 0, phase = 0, issued = 0;
+            bool ok = true;
+            for (int w = blockIdx.x / CTAS; ok && w < a.total; w += gridDim.x / CTAS) {
+                const Work k = work_of<KIND, CTAS>(w, a);
+                const int part = cols_of<B_MN, CTAS>(k.tn, a) / CTAS;       // this CTA's columns of B
+                const int m0 = (k.tm * CTAS + rank) * kTileM, n0 = k.tn * a.tile_n + rank * part;
+                const int groups_b = (part + 63) >> 6;
+                const uint32_t bytes = CTAS * PLANES * (kBytesA + (B_MN ? groups_b * (kTileK * 128) : a.tile_n / CTAS * 128));
+                for (int kb = 0; kb < a.kblocks; ++kb) {
+                    if (!tc::mbar_wait(&empty[s], phase ^ 1, kPolls)) {
+                        ok = false;
+                        break;
+                    }
+                    if (announce) tc::mbar_expect_tx(&full[s], bytes);
+                    const uint32_t bar = bar0 + 8 * s;
+#pragma unroll 1
+                    for (int p = 0; p < PLANES; ++p) {
+                        const int z = p * a.batch + k.item;
+                        if (for_a) {
+                            unsigned char *const d = tiles_a + s * kStageA + p * kBytesA;
+                            if constexpr (A_MN) {
+#pragma unroll
+                                for (int j = 0; j < kTileM / 64; ++j)
+                                    tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_a, bar, m0 + 64 * j, kb * kTileK, z);
+                            } else {
+                                tc::tma_load_3d<CTAS>(d, &map_a, bar, kb * kTileK, m0, z);
+                            }
+                        } else {
+                            unsigned char *const d = tiles_b + s * kStageB + p * kBytesB;
+                            if constexpr (B_MN) {
+#pragma unroll 1
+                                for (int j = 0; j < groups_b; ++j)
+                                    tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_b, bar, n0 + 64 * j, kb * kTileK, z);
+                            } else {
+                                tc::tma_load_3d<CTAS>(d, &map_b, bar, kb * kTileK, n0, z);
+                            }
+                        }
+                    }
+                    issued = min(issued + 1, static_cast<uint32_t>(kStages));
+                    if (++s == kStages) s = 0, phase ^= 1;
+                }
+            }
+            if (!ok) {
+                gave_up = 1;
+                // the copies in flight: the last `issued` stages before s, oldest first
+                for (uint32_t i = 0; rank == 0 && i < issued; ++i) {
+                    const uint32_t t = s + kStages - issued + i;
+                    tc::mbar_wait(&full[t % kStages], t >= kStages ? phase : phase ^ 1, kPolls);
+                }
+            }
+        }
+      } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint64_t da0 = A_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_a), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_a));
+            const uint64_t db0 = B_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_b), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_b));
+            uint32_t s = 0, phase = 0, done = 0;
+            bool ok = true;
+            for (int w = blockIdx.x / CTAS; ok && w < a.total; w += gridDim.x / CTAS) {
+                const Work k = work_of<KIND, CTAS>(w, a);
+                const uint32_t idesc = tc::idesc_f16(CTAS * kTileM, cols_of<B_MN, CTAS>(k.tn, a), A_MN, B_MN);
+                for (int c = 0; ok && c < a.kblocks; c += a.chunk, ++done) {
+                    const uint32_t acc = tmem + (done & 1) * kTileN;
+                    if (!tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const int steps = min(c + a.chunk, a.kblocks) - c;
+                    for (int i = 0; i < steps; ++i) {
+                        if (!tc::mbar_wait(&full[s], phase, kPolls)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (kStageB >> 4);
+#pragma unroll
+                        for (int q = 0; q < PAIRS; ++q) {
+                            const int pa = PLANES == 2 && q == 1, pb = PLANES == 2 && q == 0;       // hi lo, lo hi, hi hi
+#pragma unroll
+                            for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
+                                tc::mma_f16<CTAS>(acc, da + pa * (kBytesA >> 4) + j * (A_MN ? 2048 / 16 : 2),
+                                                  db + pb * (kBytesB >> 4) + j * (B_MN ? 2048 / 16 : 2), idesc,
+                                                  i > 0 || q > 0 || j > 0);
+                        }
+                        tc::mma_commit_all<CTAS>(&empty[s]);
+                        if (++s == kStages) s = 0, phase ^= 1;
+                    }
+                    if (ok) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
+                }
+            }
+            if (!ok) {
+                gave_up = 1;
+                tc::mma_commit_all<CTAS>(&drained);
+                tc::mbar_wait(&drained, 0, kPolls);
+            }
+        }
+      }
+    } else {
+        tc::regs_inc<kRegsMany>();
+        const int quad = warp & 3, half = (warp - 4) >> 2;  // a warp may read its quarter of the lanes
+        unsigned char *const stage = staging + (warp - 4) * kStageBytes;
+        uint32_t done = 0;
+        bool ok = true;
+        for (int w = blockIdx.x / CTAS; ok && w < a.total; w += gridDim.x / CTAS) {
+            const Work k = work_of<KIND, CTAS>(w, a);
+            const int n0 = k.tn * a.tile_n, row0 = (k.tm * CTAS + rank) * kTileM + quad * 32;
+            const int cols = min(min(a.cols - n0, a.tile_n), (half + 1) * kHalf);          // this warp's end there
+            const auto wanted = [&](int c0) { return row0 < a.rows && (KIND != SYMMETRIC || row0 >= n0 + c0); };
+            if constexpr (PLANES == 1) {
+                // blocks go out as they leave tensor memory; the next one's addend is on its way meanwhile
+                Addend next;
+                fetch(next, a, k, row0 + lane, n0 + half * kHalf, half * kHalf < cols && row0 + lane < a.rows && wanted(half * kHalf));
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls));
+                if (ok) {
+                    tc::fence_after_sync();
+                    const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll 1
+                    for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
+                        const Addend now = next;
+                        fetch(next, a, k, row0 + lane, n0 + c0 + 32, c0 + 32 < cols && row0 + lane < a.rows && wanted(c0 + 32));
+                        if (!wanted(c0)) continue;
+                        float v[32];
+                        __syncwarp();
+                        tc::tmem_ld32(acc + c0, v);
+                        combine(v, now, a);
+                        block_out<KIND, PLANES>(a, k, row0, n0 + c0, v, &map_out, stage);
+                    }
+                    __syncwarp();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[done & 1]);
+                        else tc::mbar_arrive_at(tc::at_leader(&acc_empty[done & 1]));
+                    }
+                    ++done;
+                }
+            } else {
+                float v[BLOCKS][32];
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[b][i] = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < a.kblocks; c += a.chunk, ++done) {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll
+                    for (int b = 0; b < BLOCKS; ++b) {
+                        const int c0 = half * kHalf + 32 * b;
+                        if (c0 < cols && wanted(c0)) {
+                            float x[32];
+                            __syncwarp();
+                            tc::tmem_ld32(acc + c0, x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[b][i] += x[i];
+                        }
+                    }
+                    __syncwarp();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[done & 1]);
+                        else tc::mbar_arrive_at(tc::at_leader(&acc_empty[done & 1]));
+                    }
+                }
+                if (ok) {
+                    // one copy of the code for the four blocks, whose sums move up
+#pragma unroll 1
+                    for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
+                        if (wanted(c0)) {
+                            Addend now;
+                            fetch(now, a, k, row0 + lane, n0 + c0, row0 + lane < a.rows);
+                            combine(v[0], now, a);
+                            block_out<KIND, PLANES>(a, k, row0, n0 + c0, v[0], &map_out, stage);
+                        }
+#pragma unroll
+                        for (int b = 0; b + 1 < BLOCKS; ++b)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[b][i] = v[b + 1][i];
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) gave_up = 1;
+        }
+        if (lane == 0) tc::bulk_wait_all();
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    if constexpr (CTAS == 1) __syncthreads();
+    else tc::cluster_sync();                 // nothing of the pair's is in flight towards either CTA
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_give<CTAS>(tmem, 512);
+    if (threadIdx.x == 0 && gave_up) atomicExch(a.gave_up, 1);
+}
+
+}  // namespace orth
+}  // namespace bl

@@ -28,9 +28,16 @@
 #include "host.h"
 #include "pdl.cuh"
 #include "score.cuh"
+#include "tensor_map.h"
 #include "xent_gemm.cuh"
 
 namespace bl {
+
+bool &gave_up_wanted() {
+    thread_local bool wanted = false;
+    return wanted;
+}
+
 namespace xent {
 
 // ------------------------------------------------------------------ elementwise kernels
@@ -474,10 +481,6 @@ struct Plan {
     int64_t flags, kept, unit, order, place, h, w, part, picked, p, dh, bytes;   // offsets into the workspace
 };
 
-bool for_tma(const void *p, int64_t ld, int64_t elem) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * elem % 16 == 0;
-}
-
 // The rows that the kernel for few rows takes (1, 4 or 8), or 0 where the tiled products are used:
 // where there are too many rows, or H does not fit shared memory. Measured, loss over a vocabulary of
 // 32000, this kernel against the tiles: dim 1024, bf16 1 row 15.7 us against 19.5, 2 rows 22 against 19.6;
@@ -596,35 +599,6 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
 
 // ------------------------------------------------------------------ launches
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess)
-            return EncodeFn(nullptr);
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
-
-// Planes of rows x inner values, copied in boxes of box_rows lines of line_bytes (128 or 64, the
-// swizzle's width too); what lies outside reads as zero and is not written. Planes are `plane`
-// values apart; with one plane any multiple of 16 bytes will do.
-bool make_map(CUtensorMap *map, CUtensorMapDataType type, int elem, const void *base, int64_t inner, int64_t rows, int64_t planes,
-              int64_t ld, int64_t plane, int box_rows, int line_bytes = 128) {
-    const EncodeFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * elem), static_cast<cuuint64_t>(plane * elem)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(line_bytes / elem), static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
-    return fn(map, type, 3, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              line_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 bool map_bf16(CUtensorMap *map, const void *base, int64_t inner, int64_t rows, int64_t planes, int64_t ld, int64_t plane,
               int box_rows, int line_bytes = 128) {
     return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, rows, planes, ld, plane, box_rows, line_bytes);
@@ -717,8 +691,6 @@ Copy copy_of(const void *src, int64_t ld, int64_t rows, int64_t dim, const int64
     w.blocks = static_cast<int>(std::min<int64_t>(cdiv(up(rows, tile) * w.panels * 8, 256), static_cast<int64_t>(sms) * 8));
     return w;
 }
-
-thread_local bool t_gave_up = false;       // bl_debug_xent_gave_up
 
 struct Call {
     int64_t rows, dim, vocab;
@@ -954,7 +926,7 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
             BL_TRY((launch_with_p<DW, PLANES>(p_mn, h_mn, to, d, q, flag_count, c.sms, c.s)));
         }
     }
-    if (t_gave_up) BL_TRY(cudaMemsetAsync(flags, 1, 4, c.s));
+    if (gave_up_wanted()) BL_TRY(cudaMemsetAsync(flags, 1, 4, c.s));
     const Spoiled<T> spoiled{static_cast<T *>(c.dW), c.lddw, c.vocab, dim};
     if (q.score && !q.grad) {
         const int64_t v0 = (q.pieces - 1) * q.piece;
@@ -1198,7 +1170,7 @@ bl_status bl_score_grad(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vocab
 
 bl_status bl_debug_xent_gave_up(int on) {
     bl::clear_error();
-    bl::xent::t_gave_up = on != 0;
+    bl::gave_up_wanted() = on != 0;
     return BL_SUCCESS;
 }
 
