@@ -250,17 +250,19 @@ int64_t bl_score_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vo
  *   dtype     BL_BF16 or BL_F32, of G and X.
  *   rows, cols  1 .. 2^16 each.    batch  1 .. 2^20; 2^40 elements in all at most.
  *   G         device pointer, ldg >= rows (one column: any); items stride_g >= 0 apart, in any order of memory.
- *   X         the result, laid out by ldx and stride_x: no two elements of it share memory. It may be G, or overlap G.
+ *   X         the result, laid out by ldx and stride_x: no two elements of it share memory. It may be G itself
+ *             (in place, laid out alike); else the memory from its first to its last element holds nothing of G's.
  *   steps     1 .. 64.
  *   coefficients  HOST double[3]: a, b, c (read before the call returns). (3.4445, -4.7750, 2.0315) takes all
  *             but the smallest singular values to about 0.7 .. 1.2 in five steps; (1.5, -0.5, 0) converges to 1.
  *   workspace at least bl_orth_workspace(...) bytes, 256-byte aligned, free again once the call's work has
- *             completed on the stream; it overlaps neither G nor X.
- * The norm is exact for any finite values. A matrix of zeros gives zeros, one that holds infinity or NaN gives NaN.
+ *             completed on the stream; it overlaps neither G nor X. Matrices of up to 128 x 256 or 256 x 128 need
+ *             none (0 bytes; it is not looked at).
+ * The norm is right to f32's accuracy for any finite values. A matrix of zeros gives zeros, one that holds infinity or NaN gives NaN.
  * a X is formed from 22 bits of X in f32. The products take f16 operands, of 11 bits for bf16 and of 22 bits for
  * f32 matrices, and add in f32. Between steps X must stay below 8 and A below 16 in every element, as any
- * converging coefficients keep it; beyond that the result is not finite. The same call gives the same bits every time,
- * whatever else is in the batch. A kernel that gave up waiting makes all of X NaN.
+ * converging coefficients keep it; beyond that the result is not finite. The same call gives the same bits every time, and a matrix
+ * the same bits whatever else is in the batch. A kernel that gave up waiting makes all of X NaN.
  */
 bl_status bl_orth(bl_dtype dtype, int64_t rows, int64_t cols, int64_t batch, const void *G, int64_t ldg,
                   int64_t stride_g, void *X, int64_t ldx, int64_t stride_x, int steps, const double *coefficients,

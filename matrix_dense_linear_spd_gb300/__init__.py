@@ -334,6 +334,6 @@ def orth(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), out=None, stream=No
     """Orthogonalised step: X = G / |G|, then `steps` times X <- a X + (b A + c A A) X with A = X X^T (on the
     shorter side), which keeps the singular vectors and takes the singular values towards 1. G is one matrix
     (rows, cols) or a batch (batch, rows, cols), bf16 or f32, whose rows or columns are contiguous; the result has
-    its shape, type and memory order. `out` may be a tensor to write to, contiguous in the same direction; it may
-    be G itself. Not recorded by autograd."""
+    its shape, type and memory order. `out` may be a tensor to write to, contiguous in the same direction: G
+    itself, or one that shares no memory with it. Not recorded by autograd."""
     return (_binding or _training()).orth(G, steps, coefficients, out, _raw(stream))

@@ -114,9 +114,11 @@ __global__ void __launch_bounds__(256) begin_kernel(const __grid_constant__ Sour
     double sum = 0.0;
     for (int i = threadIdx.x; i < q.chunks; i += 256) sum += q.sums[item * q.chunks + i];
     sum = block_sum(sum);
-    const double scale = !(sum < INFINITY) ? NAN : sum > 0.0 ? kScaleX / sqrt(sum) : 0.0;
-    const float factor = static_cast<float>(scale);
-    const bool plain = factor >= 1e-30f && factor <= 1e30f;
+    // the f64 unit is small: its root and quotient only where f32 does not hold the sum
+    const float f = static_cast<float>(sum);
+    const bool plain = f >= 1e-30f && f <= 1e30f;
+    const float factor = plain ? kScaleX / sqrtf(f) : 0.f;
+    const double scale = plain ? 0.0 : !(sum < INFINITY) ? NAN : sum > 0.0 ? kScaleX / sqrt(sum) : 0.0;
     const T *const g = static_cast<const T *>(q.g) + item * q.stride;
     __half *const to = x + item * q.lines * ldx;
     for (uint32_t i = chunk * 256 + threadIdx.x; i < all; i += q.chunks * 256) {
@@ -198,6 +200,7 @@ struct Plan {
 
 Plan plan_for(int dtype, int64_t lines, int64_t width, int64_t batch, int sms) {
     Plan q{};
+    if (fits_small(lines, width)) return q;
     q.planes = dtype == BL_F32 ? 2 : 1;
     q.lines = lines, q.width = width, q.batch = batch;
     q.wide = lines <= width;
@@ -396,7 +399,7 @@ bl_status bl_orth(bl_dtype dtype, int64_t rows, int64_t cols, int64_t batch, con
     if (steps < 1 || steps > 64) return fail(BL_ERR_INVALID_ARGUMENT, "orth: steps=%d outside [1, 64]", steps);
     if (!coefficients || !std::isfinite(coefficients[0]) || !std::isfinite(coefficients[1]) || !std::isfinite(coefficients[2]))
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: coefficients are NULL or not finite");
-    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+    if (!fits_small(cols, rows) && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: workspace is NULL or not 256-byte aligned");
     Call c{G, ldg, stride_g, X, ldx, stride_x, steps, coefficients, static_cast<char *>(workspace), bl::sm_count(),
            reinterpret_cast<cudaStream_t>(stream)};
@@ -404,13 +407,19 @@ bl_status bl_orth(bl_dtype dtype, int64_t rows, int64_t cols, int64_t batch, con
     const Plan q = plan_for(dtype, cols, rows, batch, c.sms);
     if (workspace_bytes < q.bytes)
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: workspace of %lld bytes is smaller than %lld", (long long)workspace_bytes, (long long)q.bytes);
-    // G is read before anything of X is written: they may share memory in any way
     const bl::Range ws = bl::range_of(workspace, q.bytes);
     const auto span = [&](const void *p, int64_t ld, int64_t stride) {
         return bl::range_of(p, ((batch > 1 ? (batch - 1) * stride : 0) + (cols - 1) * ld + rows) * es);
     };
     if (bl::meet(ws, span(G, ldg, stride_g)) || bl::meet(ws, span(X, ldx, stride_x)))
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: the workspace overlaps G or X");
+    const bool in_place = G == X && (cols == 1 || ldg == ldx) && (batch == 1 || stride_g == stride_x);
+    if (!in_place && bl::meet(span(G, ldg, stride_g), span(X, ldx, stride_x)))
+        return fail(BL_ERR_INVALID_ARGUMENT, "orth: X overlaps G and is not G");
+    if (fits_small(cols, rows)) {
+        const cudaError_t e = launch_small(dtype, cols, rows, batch, G, ldg, stride_g, X, ldx, stride_x, steps, coefficients, c.sms, c.s);
+        return e == cudaSuccess ? BL_SUCCESS : fail(BL_ERR_CUDA, "orth: %s", cudaGetErrorString(e));
+    }
     return dtype == BL_F32 ? run<float>(q, c) : run<__nv_bfloat16>(q, c);
 }
 

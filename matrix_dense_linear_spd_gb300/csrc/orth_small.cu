@@ -1,0 +1,353 @@
+// The orthogonalisation of small matrices: one CTA takes a matrix, or several that fill its 128 rows, through all
+// steps without going back to memory.
+//
+// The shorter side, up to 128, lies along the rows of tensor memory and the longer, up to 256, along its columns,
+// whichever of them is contiguous in memory. X stays in registers in f32, a thread holding half of a row; its f16
+// planes (the one that is multiplied, or both) are in shared memory in 64-column panels, which the Gram matrix reads
+// K-major and the product with B MN-major. A and then B take one further buffer. Three products follow each other
+// in every step, each waiting for the previous one's epilogue: latency bounds it. One 128 x 128 bf16 matrix takes
+// 5 steps in 24 us (744 in elementary operations), 200 f32 matrices of 96 x 64 in 42 us (1,030).
+//
+// Sides of up to 64, 32 and 16 leave room for 2, 4 and 8 matrices in the 128 rows: blocks of A off the diagonal are
+// set to 0, and what no f16 holds (a matrix that diverges) is cut, so that it meets its neighbours' zeros as a
+// finite number. Matrices share a CTA only where there are more of them than SMs.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "host.h"
+#include "orth.h"
+#include "orth_gemm.cuh"
+
+namespace bl {
+namespace orth {
+
+namespace {
+
+constexpr int kRows = 128, kSmallThreads = 256;
+
+struct Small {
+    const void *g;
+    void *x;
+    int64_t ldg, stride_g, ldx, stride_x;
+    int m, n;                       // shorter and longer side
+    bool turned;                    // the shorter side is the contiguous one
+    bool vec_g, vec_x;              // 16-byte pieces
+    int batch, share, rows_each;    // matrices of a CTA, and their rows
+    int steps;
+    float a, b, c;
+    int spoil;
+};
+
+// Row `row` of what lies in 64-column panels of 128 lines, 128-byte swizzle: 8 values starting at column c.
+__device__ __forceinline__ unsigned char *at128(unsigned char *base, int row, int c) {
+    return base + (c >> 6) * (kRows * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4);
+}
+
+template <int PLANES>
+__device__ __forceinline__ void put8(unsigned char *base, int plane_bytes, int row, int c, const float *v) {
+    __half hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        hi[i] = __float2half_rn(v[i]);
+        if (PLANES == 2) lo[i] = __float2half_rn(v[i] - __half2float(hi[i]));
+    }
+    *reinterpret_cast<uint4 *>(at128(base, row, c)) = make_uint4(pack(hi[0], hi[1]), pack(hi[2], hi[3]), pack(hi[4], hi[5]), pack(hi[6], hi[7]));
+    if (PLANES == 2)
+        *reinterpret_cast<uint4 *>(at128(base + plane_bytes, row, c)) =
+            make_uint4(pack(lo[0], lo[1]), pack(lo[2], lo[3]), pack(lo[4], lo[5]), pack(lo[6], lo[7]));
+}
+
+template <int PLANES>
+__device__ __forceinline__ void get8(unsigned char *base, int plane_bytes, int row, int c, float *v) {
+    const uint4 h = *reinterpret_cast<const uint4 *>(at128(base, row, c));
+    uint4 l = make_uint4(0, 0, 0, 0);
+    if (PLANES == 2) l = *reinterpret_cast<const uint4 *>(at128(base + plane_bytes, row, c));
+    const uint32_t hi[4] = {h.x, h.y, h.z, h.w}, lo[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = sum2(hi[i], lo[i]);
+        v[2 * i] = x.x, v[2 * i + 1] = x.y;
+    }
+}
+
+// NC: columns that a thread holds (the longer side is 2 NC at most).
+template <typename T, int NC>
+__global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(const __grid_constant__ Small q) {
+    constexpr int PLANES = sizeof(T) == 4 ? 2 : 1, PAIRS = PLANES == 1 ? 1 : 3;
+    constexpr int N = 2 * NC, kPlaneX = N / 64 * kRows * 128, kPlaneP = 2 * kRows * 128;
+    constexpr uint32_t kColumns = N > kRows ? N : kRows;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *const xs = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+    unsigned char *const ps = xs + PLANES * kPlaneX;
+    __shared__ uint64_t bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ double sums[8][2];
+    __shared__ float factors[8];
+    __shared__ double scales[8];
+    __shared__ int lost[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane, side = warp >> 2;
+    if (warp == 0) {
+        tc::tmem_alloc(&tmem_slot, kColumns);
+        tc::tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&bar, 1);
+        tc::mbar_fence_init();
+    }
+    if (threadIdx.x < 8) lost[threadIdx.x] = 0;
+    pdl_release();
+    pdl_wait();
+
+    // this thread's half row
+    const int slot = row / q.rows_each, r = row - slot * q.rows_each, c0 = side * NC;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * q.share + slot;
+    const bool in = slot < q.share && item < q.batch && r < q.m;
+    const int held = in ? max(0, min(NC, q.n - c0)) : 0;
+    const T *const g = static_cast<const T *>(q.g) + (in ? item * q.stride_g + (q.turned ? c0 * q.ldg + r : r * q.ldg + c0) : 0);
+    float x[NC];
+    constexpr int PER = 16 / sizeof(T);
+    if (q.vec_g) {
+#pragma unroll
+        for (int i = 0; i < NC; i += PER) {
+            __align__(16) T v[PER];
+            if (i + PER <= held) {
+                *reinterpret_cast<uint4 *>(v) = __ldg(reinterpret_cast<const uint4 *>(g + i));
+            } else {
+#pragma unroll
+                for (int e = 0; e < PER; ++e) v[e] = i + e < held ? g[i + e] : T(0.f);
+            }
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[i + e] = static_cast<float>(v[e]);
+        }
+    } else {
+        const int64_t step = q.turned ? q.ldg : 1;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) x[i] = i < held ? static_cast<float>(g[i * step]) : 0.f;
+    }
+    // the norm: 32 squares in f32, the rest in f64, of which an SM has little: a lane's sums, a warp's, the block's
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NC; i += 32) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s = fmaf(x[i + e], x[i + e], s);
+        if (s >= 1e-25f && s <= 1e30f) {
+            sum += s;
+        } else if (held > i) {
+#pragma unroll 1
+            for (int e = 0; e < 32; ++e) {
+                const double y = e < held - i ? static_cast<double>(static_cast<float>(g[(i + e) * (q.turned ? q.ldg : 1)])) : 0.0;
+                sum = fma(y, y, sum);
+            }
+        }
+    }
+    for (int o = 1; o < min(32, q.rows_each); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((lane & 15) == 0) sums[warp][lane >> 4] = sum;
+    __syncthreads();
+    if (threadIdx.x < q.share) {
+        // its 32-row groups (or half of one), both halves of each row
+        sum = 0.0;
+        const int first = threadIdx.x * q.rows_each / 32, count = max(1, q.rows_each / 32), which = q.rows_each == 16 ? threadIdx.x & 1 : 0;
+        for (int w = first; w < first + count; ++w) sum += sums[w][which] + sums[w + 4][which];
+        const float f = static_cast<float>(sum);
+        const bool plain = f >= 1e-30f && f <= 1e30f;
+        const double scale = !(sum < INFINITY) ? NAN : sum == 0.0 || plain ? 0.0 : 8192.0 / sqrt(sum);
+        scales[threadIdx.x] = scale;
+        factors[threadIdx.x] = plain ? 8192.f / sqrtf(f) : 0.f;          // 0: the scale is to be used
+    }
+    __syncthreads();
+    const float factor = slot < q.share ? factors[slot] : 0.f;
+    const double scale = slot < q.share ? scales[slot] : 0.0;
+    bool bad = scale != scale;
+    if (factor != 0.f) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) x[i] *= factor;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) x[i] = bad || scale == 0.0 ? 0.f : static_cast<float>(x[i] * scale);
+    }
+
+    const auto x_out = [&] {
+#pragma unroll
+        for (int i = 0; i < NC; i += 8) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fminf(fmaxf(x[i + e], -65504.f), 65504.f);
+            put8<PLANES>(xs, kPlaneX, row, c0 + i, v);
+        }
+    };
+    x_out();
+    const int rows = q.share == 1 ? (q.m + 15) & ~15 : kRows;            // of A and B
+    const int cols = (q.n + 15) & ~15;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t parity = 0;
+    bool ok = true;
+    uint32_t tmem = 0;
+    // One thread issues a product, all wait for it: A = X X^T (of_x), A A, or B X (apply)
+    const auto product = [&](bool of_x, bool apply, int k, int n) {
+        tc::fence_before_sync();
+        tc::fence_proxy_async_smem();
+        ok = !__syncthreads_or(!ok);
+        tc::fence_after_sync();
+        tmem = tmem_slot;
+        if (!ok) return;
+        if (threadIdx.x == 0) {
+            const uint32_t idesc = tc::idesc_f16(kRows, n, false, apply);
+            const uint32_t a_at = tc::smem_u32(of_x ? xs : ps), b_at = tc::smem_u32(apply || of_x ? xs : ps);
+            const int plane_a = of_x ? kPlaneX : kPlaneP, plane_b = apply || of_x ? kPlaneX : kPlaneP;
+#pragma unroll 1
+            for (int p = 0; p < PAIRS; ++p) {
+                const int pa = PLANES == 2 && p == 1, pb = PLANES == 2 && p == 0;
+#pragma unroll 1
+                for (int j = 0; j < k / 16; ++j) {
+                    // 16 k: 32 bytes along a line, lines of 64 k in panels; or 16 lines
+                    const uint64_t da = tc::sdesc_sw128(a_at + pa * plane_a + (j >> 2) * (kRows * 128)) + (j & 3) * 2;
+                    const uint64_t db = apply ? tc::sdesc_mn_sw128(b_at + pb * plane_b, kRows * 128) + j * (2048 / 16)
+                                              : tc::sdesc_sw128(b_at + pb * plane_b + (j >> 2) * (kRows * 128)) + (j & 3) * 2;
+                    tc::mma_f16<1>(tmem, da, db, idesc, p > 0 || j > 0);
+                }
+            }
+            tc::mma_commit(&bar);
+        }
+        ok = tc::mbar_wait(&bar, parity, kPolls);
+        parity ^= 1;
+        tc::fence_after_sync();
+    };
+    constexpr int PC = 64;                       // columns of A that a thread holds
+    const int p0 = side * PC, shift = 31 - __clz(q.rows_each), own = row >> shift;     // its matrix
+#pragma unroll 1
+    for (int step = 0; step < q.steps; ++step) {
+        // A, times 2^12
+        product(true, false, cols, rows);
+#pragma unroll 1
+        for (int c = p0; c < p0 + PC; c += 32) {
+            float t[32];
+            __syncwarp();
+            tc::tmem_ld32(tmem + lanes + c, t);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) t[i] = (c + i) >> shift == own ? t[i] * (4096.f / (8192.f * 8192.f)) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) put8<PLANES>(ps, kPlaneP, row, c + i, t + i);
+        }
+        // B = b A + c A A, times 2^12, in A's place
+        product(false, false, rows, rows);
+#pragma unroll 1
+        for (int c = p0; c < p0 + PC; c += 32) {
+            float t[32];
+            __syncwarp();
+            tc::tmem_ld32(tmem + lanes + c, t);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                float v[8];
+                get8<PLANES>(ps, kPlaneP, row, c + i, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = (c + i + e) >> shift == own ? fmaf(q.c / 4096.f, t[i + e], q.b * v[e]) : 0.f;
+                put8<PLANES>(ps, kPlaneP, row, c + i, v);
+            }
+        }
+        // X
+        product(false, true, rows, cols);
+#pragma unroll
+        for (int h = 0; h < NC; h += 32) {
+            float t[32];
+            __syncwarp();
+            tc::tmem_ld32(tmem + lanes + c0 + h, t);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float y = fmaf(q.a, x[h + i], t[i] * (1.f / 4096.f));
+                x[h + i] = c0 + h + i < q.n ? y : 0.f;
+                bad |= !(fabsf(x[h + i]) <= 65504.f);
+            }
+        }
+        if (step + 1 < q.steps) x_out();
+    }
+    // what a matrix or a product lost is seen in all of it
+    if (!ok) tc::mbar_wait(&bar, parity ^ 1, kPolls);            // what gave up may still come to its end
+    bad |= !ok || q.spoil;
+    if (bad && slot < 8) lost[slot] = 1;
+    __syncthreads();
+    bad = slot < 8 && lost[slot];
+    T *const to = static_cast<T *>(q.x) + (in ? item * q.stride_x + (q.turned ? c0 * q.ldx + r : r * q.ldx + c0) : 0);
+    const auto value = [&](float f) {
+        const float y = bad ? NAN : f * (1.f / 8192.f);
+        if constexpr (PLANES == 1) return __float2bfloat16_rn(y);
+        else return y;
+    };
+    if (q.vec_x) {
+#pragma unroll
+        for (int i = 0; i < NC; i += PER) {
+            __align__(16) T v[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) v[e] = value(x[i + e]);
+            if (i + PER <= held) {
+                *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    if (i + e < held) to[i + e] = v[e];
+            }
+        }
+    } else {
+        const int64_t step = q.turned ? q.ldx : 1;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            if (i < held) to[i * step] = value(x[i]);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem_slot, kColumns);
+}
+
+template <typename T, int NC>
+cudaError_t launch(const Small &q, cudaStream_t s) {
+    constexpr int PLANES = sizeof(T) == 4 ? 2 : 1;
+    constexpr int kSmem = PLANES * (2 * NC / 64 + 2) * kRows * 128 + 1024;
+    static std::atomic<unsigned long long> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (!(bit & done.load(std::memory_order_acquire))) {
+        e = cudaFuncSetAttribute(small_kernel<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return launch_pdl(small_kernel<T, NC>, static_cast<unsigned>((q.batch + q.share - 1) / q.share), kSmallThreads, kSmem, s, q);
+}
+template <typename T>
+cudaError_t launch(const Small &q, cudaStream_t s) {
+    return q.n <= 64 ? launch<T, 32>(q, s) : q.n <= 128 ? launch<T, 64>(q, s) : launch<T, 128>(q, s);
+}
+
+}  // namespace
+
+bool fits_small(int64_t lines, int64_t width) { return std::min(lines, width) <= kRows && std::max(lines, width) <= 256; }
+
+cudaError_t launch_small(int dtype, int64_t lines, int64_t width, int64_t batch, const void *g, int64_t ldg, int64_t stride_g, void *x,
+                         int64_t ldx, int64_t stride_x, int steps, const double *coefficients, int sms, cudaStream_t s) {
+    Small q{};
+    const int64_t es = dtype == BL_F32 ? 4 : 2;
+    q.g = g, q.x = x, q.ldg = ldg, q.stride_g = stride_g, q.ldx = ldx, q.stride_x = stride_x;
+    q.turned = lines > width;
+    q.m = static_cast<int>(std::min(lines, width));
+    q.n = static_cast<int>(std::max(lines, width));
+    const auto vec = [&](const void *p, int64_t ld, int64_t stride) {
+        return !q.turned && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && (batch == 1 || stride * es % 16 == 0);
+    };
+    q.vec_g = vec(g, ldg, stride_g);
+    q.vec_x = vec(x, ldx, stride_x);
+    q.batch = static_cast<int>(batch);
+    q.rows_each = q.m <= 16 ? 16 : q.m <= 32 ? 32 : q.m <= 64 ? 64 : kRows;
+    q.share = 1;
+    while (q.share * 2 * q.rows_each <= kRows && (batch + q.share - 1) / q.share > sms) q.share *= 2;
+    if (q.share == 1) q.rows_each = kRows;
+    q.steps = steps;
+    q.a = static_cast<float>(coefficients[0]), q.b = static_cast<float>(coefficients[1]), q.c = static_cast<float>(coefficients[2]);
+    q.spoil = gave_up_wanted();
+    return dtype == BL_F32 ? launch<float>(q, s) : launch<__nv_bfloat16>(q, s);
+}
+
+}  // namespace orth
+}  // namespace bl

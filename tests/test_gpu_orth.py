@@ -264,6 +264,30 @@ def test_a_product_that_gave_up_is_seen(kind, rows, cols):
     assert torch.equal(want, bl.orth(G))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,rows,cols,turned", [(400, 16, 16, False), (1001, 5, 40, False), (333, 60, 64, True), (700, 100, 30, False),
+                                                    (305, 128, 100, True), (200, 96, 64, False), (160, 256, 33, False)])
+def test_many_small_matrices(kind, batch, rows, cols, turned):
+    """Several share a CTA: each comes out as it does alone, whatever its neighbours hold."""
+    torch, bl = torch_cuda(), lib()
+    G = make(rows, cols, kind, batch, seed=batch, strong=2, turned=turned)
+    got = bl.orth(G)
+    check(got, G, 5, QUINTIC, kind)
+    for i in (0, 1, 7, batch // 2, batch - 1):
+        assert torch.equal(bl.orth(G[i]), got[i])
+    G[1] = float("inf")
+    G[4, 0, 0] = float("nan")
+    G[5] = 0
+    again = bl.orth(G)
+    assert bool(again[[1, 4]].isnan().all()) and bool((again[5] == 0).all())
+    rest = torch.ones(batch, dtype=torch.bool, device="cuda")
+    rest[[1, 4, 5]] = False
+    assert torch.equal(again[rest], got[rest])
+    # coefficients that diverge: nothing finite, or what the definition gives
+    wild = bl.orth(G, steps=20, coefficients=(30.0, 9.0, 1.0))
+    assert bool(wild[rest].isnan().any(2).any(1).all()) and bool((wild[5] == 0).all())
+
+
 def test_symmetric_matrices_stay_symmetric():
     """X of a symmetric G: every product is computed from symmetric operands, A and B are symmetric to the bit."""
     torch, bl = torch_cuda(), lib()
@@ -302,5 +326,10 @@ def test_refusals():
         bl.orth(G, out=torch.empty(1, 30, device="cuda").expand(20, 30))
     with pytest.raises(bl.BLError):
         bl.orth(G.expand(2, 20, 30), out=torch.empty(1, 20, 30, device="cuda").expand(2, 20, 30))
+    flat = torch.zeros(2000, device="cuda")
+    for shape in ((20, 30), (300, 3)):
+        n = shape[0] * shape[1]
+        with pytest.raises(bl.BLError, match="overlaps"):
+            bl.orth(flat[:n].view(shape), out=flat[1:n + 1].view(shape))
     X = bl.orth(G.requires_grad_())
     assert not X.requires_grad

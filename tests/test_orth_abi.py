@@ -16,10 +16,10 @@ def bl():
     return m
 
 
-GOOD = dict(dtype=4, rows=8, cols=16, batch=2, G=F, ldg=8, sg=128, X=2 * F, ldx=8, sx=128, steps=5, abc=(3.4445, -4.775, 2.0315), ws=3 * F)
+GOOD = dict(dtype=4, rows=8, cols=300, batch=2, G=F, ldg=8, sg=2400, X=2 * F, ldx=8, sx=2400, steps=5, abc=(3.4445, -4.775, 2.0315), ws=3 * F)
 WRONG = [dict(dtype=1), dict(dtype=5), dict(dtype=2), dict(rows=0), dict(rows=(1 << 16) + 1), dict(cols=0), dict(cols=(1 << 16) + 1),
          dict(batch=0), dict(batch=(1 << 20) + 1), dict(rows=1 << 16, cols=1 << 16, batch=1 << 9, ldg=1 << 16, ldx=1 << 16, sx=1 << 32, sg=1 << 32),
-         dict(G=None), dict(G=F + 1), dict(ldg=7), dict(sg=-1), dict(X=None), dict(X=F + 1), dict(ldx=7), dict(sx=-128), dict(sx=0), dict(sx=127),
+         dict(G=None), dict(G=F + 1), dict(ldg=7), dict(sg=-1), dict(X=None), dict(X=F + 1), dict(ldx=7), dict(sx=-128), dict(sx=0), dict(sx=2399),
          dict(ldx=1 << 40), dict(sx=8, ldx=15), dict(steps=0), dict(steps=65), dict(abc=None), dict(abc=(1.0, float("nan"), 0.0)),
          dict(abc=(float("inf"), 1.0, 0.0)), dict(ws=None), dict(ws=3 * F + 128)]
 
