@@ -32,10 +32,6 @@
 namespace bl {
 namespace orth {
 
-// X is kept times 2^13, A and B times 2^12: elements of X are at most 1.3 for coefficients as above, of A 1.7, and
-// f16 reaches 65504; typical ones, 1 / sqrt(long side), stay in f16's normal range for 22 bits up to sides of 2^16.
-constexpr float kScaleX = 8192.f, kScaleA = 4096.f;
-
 // ------------------------------------------------------------------ elementwise kernels
 
 struct Source {
@@ -114,11 +110,7 @@ __global__ void __launch_bounds__(256) begin_kernel(const __grid_constant__ Sour
     double sum = 0.0;
     for (int i = threadIdx.x; i < q.chunks; i += 256) sum += q.sums[item * q.chunks + i];
     sum = block_sum(sum);
-    // the f64 unit is small: its root and quotient only where f32 does not hold the sum
-    const float f = static_cast<float>(sum);
-    const bool plain = f >= 1e-30f && f <= 1e30f;
-    const float factor = plain ? kScaleX / sqrtf(f) : 0.f;
-    const double scale = plain ? 0.0 : !(sum < INFINITY) ? NAN : sum > 0.0 ? kScaleX / sqrt(sum) : 0.0;
+    const float2 factor = scale_of(sum);
     const T *const g = static_cast<const T *>(q.g) + item * q.stride;
     __half *const to = x + item * q.lines * ldx;
     for (uint32_t i = chunk * 256 + threadIdx.x; i < all; i += q.chunks * 256) {
@@ -127,9 +119,7 @@ __global__ void __launch_bounds__(256) begin_kernel(const __grid_constant__ Sour
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-            // norms out of f32's range: the factor in f64
-            const float a = plain ? v[e] * factor : static_cast<float>(v[e] * scale);
-            const float b = plain ? v[e + 1] * factor : static_cast<float>(v[e + 1] * scale);
+            const float a = v[e] * factor.x * factor.y, b = v[e + 1] * factor.x * factor.y;
             const __half ha = __float2half_rn(a), hb = __float2half_rn(b);
             hi[e / 2] = pack(ha, hb);
             lo[e / 2] = pack(__float2half_rn(a - __half2float(ha)), __float2half_rn(b - __half2float(hb)));
@@ -177,7 +167,7 @@ Shape shape_for(int64_t rows, int64_t cols, bool symmetric, bool b_mn, int64_t b
     int64_t least = 0;
     for (int ctas = 1; ctas <= 2; ++ctas) {
         if (ctas == 2 && rows <= kTileM) break;
-        for (int t = kTileN; t >= (ctas == 2 && b_mn ? 128 : 64); t /= 2) {        // a pair's halves: whole groups of 64
+        for (int t = ctas * 128; t >= (ctas == 2 && b_mn ? 128 : 64); t /= 2) {        // a pair's halves: whole groups of 64
             Shape s{ctas, t, static_cast<int>(cdiv(rows, ctas * kTileM)), static_cast<int>(cdiv(cols, t)), 0};
             s.per_item = tiles_of(s, symmetric);
             const int64_t rounds = cdiv(batch * s.per_item, std::max(1, sms / ctas));
@@ -270,7 +260,7 @@ bl_status run(const Plan &q, const Call &c) {
     BL_TRY(launch_pdl(begin_kernel<T>, blocks, 256, 0, c.s, src, reinterpret_cast<__half *>(c.ws + q.x[0]), q.ldx, plane_x));
     const float a = static_cast<float>(c.coefficients[0]), b = static_cast<float>(c.coefficients[1]), cc = static_cast<float>(c.coefficients[2]);
 
-    // maps: operands in lines of 128 bytes, results in lines of 64
+    // maps: operands in lines of 128 bytes; results, and what products are added to, in lines of 64
     const auto map_f16 = [&](CUtensorMap *m, int64_t at, int64_t inner, int64_t rows, int64_t planes, int64_t ld, int box_rows, int line) {
         return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, c.ws + at, inner, rows, planes * q.batch, ld, rows * ld, box_rows, line);
     };
@@ -307,22 +297,18 @@ bl_status run(const Plan &q, const Call &c) {
     gram.alpha = kScaleA / (kScaleX * kScaleX);
     Args square = args(q.square, q.small, q.small, q.small);
     square.alpha = cc / kScaleA, square.beta = b;
-    square.add_hi = reinterpret_cast<const __half *>(c.ws + q.a);
-    square.add_lo = PLANES == 2 ? square.add_hi + q.batch * q.small * q.lda : nullptr;
-    square.add_ld = q.lda;
+    square.planes_add = PLANES;
     for (int step = 0; step < c.steps; ++step) {
         const int from = step & 1;
         CUtensorMap x_gram_a, x_gram_b, x_apply;
         BL_MAP(operand(&x_gram_a, q, true, from, !q.wide, kTileM));
         BL_MAP(operand(&x_gram_b, q, true, from, !q.wide, q.gram.tile_n / q.gram.ctas));
         BL_MAP(operand(&x_apply, q, true, from, q.wide, kTileM));
-        BL_TRY(product(q.wide ? GRAM_LINES : GRAM_WIDTH, q.gram.ctas, x_gram_a, x_gram_b, a_out, gram, c.sms, c.s));
-        BL_TRY(product(SQUARE, q.square.ctas, sq_a, sq_b, b_out, square, c.sms, c.s));
+        BL_TRY(product(q.wide ? GRAM_LINES : GRAM_WIDTH, q.gram.ctas, x_gram_a, x_gram_b, a_out, a_out, gram, c.sms, c.s));
+        BL_TRY(product(SQUARE, q.square.ctas, sq_a, sq_b, a_out, b_out, square, c.sms, c.s));
         Args apply = args(q.apply, q.lines, q.width, q.small);
         apply.alpha = 1 / kScaleA, apply.beta = a;
-        apply.add_hi = reinterpret_cast<const __half *>(c.ws + q.x[from]);
-        apply.add_lo = apply.add_hi + plane_x;
-        apply.add_ld = q.ldx;
+        apply.planes_add = 2;
         apply.planes_out = 2;
         apply.last = step + 1 == c.steps;
         if (apply.last) {
@@ -331,8 +317,8 @@ bl_status run(const Plan &q, const Call &c) {
             apply.ldo = c.ldx, apply.stride_o = c.stride_x;
         }
         const CUtensorMap &to = !apply.last ? x_out[from ^ 1] : by_tma ? user_out : x_out[0];
-        if (q.wide) BL_TRY(product(APPLY_LEFT, q.apply.ctas, ap_s, x_apply, to, apply, c.sms, c.s));
-        else BL_TRY(product(APPLY_RIGHT, q.apply.ctas, x_apply, ap_s, to, apply, c.sms, c.s));
+        if (q.wide) BL_TRY(product(APPLY_LEFT, q.apply.ctas, ap_s, x_apply, x_out[from], to, apply, c.sms, c.s));
+        else BL_TRY(product(APPLY_RIGHT, q.apply.ctas, x_apply, ap_s, x_out[from], to, apply, c.sms, c.s));
     }
     if (gave_up_wanted()) BL_TRY(cudaMemsetAsync(gave_up, 1, 4, c.s));
     BL_TRY(launch_pdl(spoil_kernel<T>, static_cast<unsigned>(std::min<int64_t>(c.sms, q.batch * q.lines)), 256, 0, c.s, gave_up,

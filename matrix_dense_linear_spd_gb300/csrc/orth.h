@@ -14,10 +14,10 @@ struct Args;
 // How a product reads its operands (see orth_gemm.cuh).
 enum Layout : int { GRAM_LINES = 0, GRAM_WIDTH = 1, SQUARE = 0, APPLY_LEFT = 2, APPLY_RIGHT = 3 };
 
-cudaError_t launch_one(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const Args &a,
-                       int sms, cudaStream_t s);
-cudaError_t launch_two(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const Args &a,
-                       int sms, cudaStream_t s);
+cudaError_t launch_one(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo,
+                       const Args &a, int sms, cudaStream_t s);
+cudaError_t launch_two(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo,
+                       const Args &a, int sms, cudaStream_t s);
 
 // Small matrices, in one launch; needs no workspace.
 bool fits_small(int64_t lines, int64_t width);

@@ -34,20 +34,43 @@ namespace orth {
 
 enum Kind : int { SYMMETRIC = 0, APPLY = 1 };
 
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
-constexpr int kEpilogueWarps = 8, kHalf = kTileN / 2;
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;          // columns of a tile, at most
+constexpr int kEpilogueWarps = 8;                               // two share 32 rows
 constexpr int kStageBytes = 32 * 128;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
 static_assert(128 * kRegsFew + 32 * kEpilogueWarps * kRegsMany <= kThreads * kRegsLaunch, "more registers than the block has");
 constexpr uint32_t kPolls = 1u << 22;
 
+// X is kept times 2^13, A and B times 2^12: elements of X are at most 1.3 for coefficients as above, of A 1.7, and
+// f16 reaches 65504; typical ones, 1 / sqrt(long side), stay in f16's normal range for 22 bits up to sides of 2^16.
+constexpr float kScaleX = 8192.f, kScaleA = 4096.f;
+
+// What X_0's values are multiplied by, one after the other, for a given sum of squares: a power of two where the norm
+// lies outside of what f32 multiplies by without loss, then the rest. A matrix of zeros stays one; NaN if the norm is not finite.
+__device__ __forceinline__ float2 scale_of(double sum) {
+    if (!(sum < INFINITY)) return make_float2(1.f, NAN);
+    if (sum == 0.0) return make_float2(0.f, 0.f);
+    const float f = static_cast<float>(sum);
+    if (f >= 1e-30f && f <= 1e30f) return make_float2(1.f, kScaleX / sqrtf(f));      // the f64 unit is slow
+    const double norm = sqrt(sum);
+    const float power = norm < 1.0 ? 0x1p126f : 0x1p-126f;
+    return make_float2(power, static_cast<float>(kScaleX / (norm * power)));
+}
+
+// Shared memory of a CTA: the operands' ring (a pair shares tiles of 256 columns, a single CTA has 128), and 4 KB for
+// each epilogue warp's lines on their way out. What a product is added to comes in by TMA too: with one plane into lines of its
+// own, so that a block's are on their way while the previous block is worked on, with two (whose products take
+// three times as long) into those that the result leaves by. Read with 16-byte loads, each lane its own row, those lines took
+// the epilogue past the products: 12 x 1024 x 4096 bf16, B X 133 us.
 template <int PLANES, int CTAS>
 struct Ring {
-    static constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN / CTAS * kTileK * 2;
+    static constexpr int kTile = CTAS == 1 ? 128 : 256;
+    static constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTile / CTAS * kTileK * 2;
     static constexpr int kStageA = PLANES * kBytesA, kStageB = PLANES * kBytesB;
-    static constexpr int kStages = 192 * 1024 / (kStageA + kStageB);
-    static constexpr int kSmem = kStages * (kStageA + kStageB) + kEpilogueWarps * kStageBytes + 1024;
+    static constexpr int kStages = PLANES == 1 ? 5 : 3;
+    static constexpr int kLines = kEpilogueWarps * kStageBytes * (PLANES == 1 ? 2 : 1);
+    static constexpr int kSmem = kStages * (kStageA + kStageB) + kLines + 1024;
 };
 
 struct Args {
@@ -56,9 +79,8 @@ struct Args {
     int kblocks, chunk;        // 64-deep steps; how many are added in tensor memory before registers take over
     int tile_n, tiles_m, tiles_n;
     int per_item, total;       // tiles
-    float alpha, beta;         // result = alpha * product + beta * (add_hi + add_lo)
-    const __half *add_hi, *add_lo;      // [item][rows][add_ld], or null
-    int64_t add_ld;
+    float alpha, beta;         // result = alpha * product + beta * what is added
+    int planes_add;            // of the f16 matrix that is added; 0: none
     int planes_out;            // of the f16 result
     bool last;                 // APPLY: the result is the caller's, f32 or bf16
     void *out;                 // where its lines do not start on 16-byte boundaries: stored without TMA
@@ -124,20 +146,26 @@ __device__ __forceinline__ void lines_store(const CUtensorMap *map, const unsign
     }
 }
 
+// What the product is added to, 32 columns of a warp's rows at a time.
 struct Addend {
     uint4 hi[4], lo[4];
 };
-// 32 columns of this lane's row of what the product is added to.
-__device__ __forceinline__ void fetch(Addend &d, const Args &a, const Work &w, int row, int col, bool there) {
+__device__ __forceinline__ void addend_ask(const CUtensorMap *map, const Args &a, const Work &w, unsigned char *lines, uint64_t *bar,
+                                           int row0, int col0) {
+    if ((threadIdx.x & 31) != 0) return;
+    tc::mbar_expect_tx(bar, 2048 * a.planes_add);
+    for (int p = 0; p < a.planes_add; ++p) tc::tma_load_3d<1>(lines + p * 2048, map, tc::smem_u32(bar), col0, row0, p * a.batch + w.item);
+}
+__device__ __forceinline__ bool addend_take(Addend &d, const Args &a, const unsigned char *lines, uint64_t *bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kPolls));
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) d.hi[j] = d.lo[j] = make_uint4(0, 0, 0, 0);
-    if (!there || !a.add_hi) return;
-    const int64_t at = (static_cast<int64_t>(w.item) * a.rows + row) * a.add_ld + col;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d.hi[j] = *reinterpret_cast<const uint4 *>(a.add_hi + at + 8 * j);
-    if (!a.add_lo) return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d.lo[j] = *reinterpret_cast<const uint4 *>(a.add_lo + at + 8 * j);
+    for (int j = 0; j < 4; ++j) {
+        d.hi[j] = *reinterpret_cast<const uint4 *>(lines + at64(lane, j));
+        d.lo[j] = a.planes_add == 2 ? *reinterpret_cast<const uint4 *>(lines + 2048 + at64(lane, j)) : make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();                               // the lines may be filled again
+    return ok;
 }
 __device__ __forceinline__ float2 sum2(uint32_t hi, uint32_t lo) {
     const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hi)), y = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
@@ -222,15 +250,16 @@ __device__ __forceinline__ void block_out(const Args &a, const Work &w, int row0
 template <int KIND, bool A_MN, bool B_MN, int PLANES, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Args a) {
+                   const __grid_constant__ CUtensorMap map_add, const __grid_constant__ CUtensorMap map_out,
+                   const __grid_constant__ Args a) {
     using R = Ring<PLANES, CTAS>;
     constexpr int kBytesA = R::kBytesA, kBytesB = R::kBytesB, kStageA = R::kStageA, kStageB = R::kStageB, kStages = R::kStages;
-    constexpr int PAIRS = PLANES == 1 ? 1 : 3, BLOCKS = kHalf / 32;
+    constexpr int PAIRS = PLANES == 1 ? 1 : 3, kHalf = R::kTile / 2, BLOCKS = kHalf / 32;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kStageA;
     unsigned char *const staging = base + kStages * (kStageA + kStageB);
-    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], add_full[kEpilogueWarps], drained;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -246,11 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&acc_full[s], 1);
             tc::mbar_init(&acc_empty[s], CTAS * kEpilogueWarps);
         }
+        for (int s = 0; s < kEpilogueWarps; ++s) tc::mbar_init(&add_full[s], 1);
         tc::mbar_init(&drained, 1);
         tc::mbar_fence_init();
         gave_up = 0;
         tc::tma_prefetch_map(&map_a);
         tc::tma_prefetch_map(&map_b);
+        tc::tma_prefetch_map(&map_add);
         tc::tma_prefetch_map(&map_out);
     }
     __syncwarp();
@@ -369,26 +400,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::regs_inc<kRegsMany>();
         const int quad = warp & 3, half = (warp - 4) >> 2;  // a warp may read its quarter of the lanes
         unsigned char *const stage = staging + (warp - 4) * kStageBytes;
-        uint32_t done = 0;
+        unsigned char *const lines = PLANES == 1 ? stage + kEpilogueWarps * kStageBytes : stage;
+        uint64_t *const bar = &add_full[warp - 4];
+        const bool adds = a.planes_add > 0;
+        uint32_t done = 0, asked = 0;
         bool ok = true;
         for (int w = blockIdx.x / CTAS; ok && w < a.total; w += gridDim.x / CTAS) {
             const Work k = work_of<KIND, CTAS>(w, a);
-            const int n0 = k.tn * a.tile_n, row0 = (k.tm * CTAS + rank) * kTileM + quad * 32;
-            const int cols = min(min(a.cols - n0, a.tile_n), (half + 1) * kHalf);          // this warp's end there
-            const auto wanted = [&](int c0) { return row0 < a.rows && (KIND != SYMMETRIC || row0 >= n0 + c0); };
+            const int n0 = k.tn * a.tile_n, row0 = (k.tm * CTAS + rank) * kTileM + quad * 32, first = half * kHalf;
+            int cols = min(min(a.cols - n0, a.tile_n), first + kHalf);                     // this warp's end there
+            if (KIND == SYMMETRIC) cols = min(cols, row0 + 32 - n0);                       // or with the diagonal's block
+            if (row0 >= a.rows) cols = 0;
             if constexpr (PLANES == 1) {
                 // blocks go out as they leave tensor memory; the next one's addend is on its way meanwhile
-                Addend next;
-                fetch(next, a, k, row0 + lane, n0 + half * kHalf, half * kHalf < cols && row0 + lane < a.rows && wanted(half * kHalf));
+                if (adds && first < cols) addend_ask(&map_add, a, k, lines, bar, row0, n0 + first);
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls));
-                if (ok) {
+                if (!ok) {
+                    if (adds && first < cols) tc::mbar_wait(bar, asked & 1, kPolls);
+                } else {
                     tc::fence_after_sync();
                     const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll 1
-                    for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
-                        const Addend now = next;
-                        fetch(next, a, k, row0 + lane, n0 + c0 + 32, c0 + 32 < cols && row0 + lane < a.rows && wanted(c0 + 32));
-                        if (!wanted(c0)) continue;
+                    for (int c0 = first; c0 < cols; c0 += 32) {
+                        Addend now{};
+                        if (adds) {
+                            ok = addend_take(now, a, lines, bar, asked++ & 1) && ok;
+                            if (c0 + 32 < cols) addend_ask(&map_add, a, k, lines, bar, row0, n0 + c0 + 32);
+                        }
                         float v[32];
                         __syncwarp();
                         tc::tmem_ld32(acc + c0, v);
@@ -418,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll
                     for (int b = 0; b < BLOCKS; ++b) {
-                        const int c0 = half * kHalf + 32 * b;
-                        if (c0 < cols && wanted(c0)) {
+                        const int c0 = first + 32 * b;
+                        if (c0 < cols) {
                             float x[32];
                             __syncwarp();
                             tc::tmem_ld32(acc + c0, x);
@@ -438,13 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok) {
                     // one copy of the code for the four blocks, whose sums move up
 #pragma unroll 1
-                    for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
-                        if (wanted(c0)) {
-                            Addend now;
-                            fetch(now, a, k, row0 + lane, n0 + c0, row0 + lane < a.rows);
-                            combine(v[0], now, a);
-                            block_out<KIND, PLANES>(a, k, row0, n0 + c0, v[0], &map_out, stage);
+                    for (int c0 = first; c0 < cols; c0 += 32) {
+                        Addend now{};
+                        if (adds) {
+                            lines_free();
+                            addend_ask(&map_add, a, k, lines, bar, row0, n0 + c0);
+                            ok = addend_take(now, a, lines, bar, asked++ & 1) && ok;
                         }
+                        combine(v[0], now, a);
+                        block_out<KIND, PLANES>(a, k, row0, n0 + c0, v[0], &map_out, stage);
 #pragma unroll
                         for (int b = 0; b + 1 < BLOCKS; ++b)
 #pragma unroll

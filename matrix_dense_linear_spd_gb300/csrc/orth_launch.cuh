@@ -11,7 +11,7 @@ namespace bl {
 namespace orth {
 
 template <int KIND, bool A_MN, bool B_MN, int PLANES, int CTAS>
-cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const Args &a, int sms, cudaStream_t s) {
+cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo, const Args &a, int sms, cudaStream_t s) {
     constexpr int kSmem = Ring<PLANES, CTAS>::kSmem;
     const auto kernel = product_kernel<KIND, A_MN, B_MN, PLANES, CTAS>;
     static std::atomic<int> groups[64];         // CTAs, or pairs of CTAs, that the device runs at once
@@ -40,25 +40,25 @@ cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUt
         }
         if (dev < 64) groups[dev].store(most, std::memory_order_release);
     }
-    return launch_pdl_cluster(kernel, std::min(a.total, most) * CTAS, kThreads, kSmem, CTAS, s, ma, mb, mo, a);
+    return launch_pdl_cluster(kernel, std::min(a.total, most) * CTAS, kThreads, kSmem, CTAS, s, ma, mb, md, mo, a);
 }
 
 template <int PLANES>
-cudaError_t launch(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const Args &a, int sms,
+cudaError_t launch(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo, const Args &a, int sms,
                    cudaStream_t s) {
     switch (layout) {
         case GRAM_LINES:      // and SQUARE
-            return ctas == 1 ? launch_tiles<SYMMETRIC, false, false, PLANES, 1>(ma, mb, mo, a, sms, s)
-                             : launch_tiles<SYMMETRIC, false, false, PLANES, 2>(ma, mb, mo, a, sms, s);
+            return ctas == 1 ? launch_tiles<SYMMETRIC, false, false, PLANES, 1>(ma, mb, md, mo, a, sms, s)
+                             : launch_tiles<SYMMETRIC, false, false, PLANES, 2>(ma, mb, md, mo, a, sms, s);
         case GRAM_WIDTH:
-            return ctas == 1 ? launch_tiles<SYMMETRIC, true, true, PLANES, 1>(ma, mb, mo, a, sms, s)
-                             : launch_tiles<SYMMETRIC, true, true, PLANES, 2>(ma, mb, mo, a, sms, s);
+            return ctas == 1 ? launch_tiles<SYMMETRIC, true, true, PLANES, 1>(ma, mb, md, mo, a, sms, s)
+                             : launch_tiles<SYMMETRIC, true, true, PLANES, 2>(ma, mb, md, mo, a, sms, s);
         case APPLY_LEFT:
-            return ctas == 1 ? launch_tiles<APPLY, false, true, PLANES, 1>(ma, mb, mo, a, sms, s)
-                             : launch_tiles<APPLY, false, true, PLANES, 2>(ma, mb, mo, a, sms, s);
+            return ctas == 1 ? launch_tiles<APPLY, false, true, PLANES, 1>(ma, mb, md, mo, a, sms, s)
+                             : launch_tiles<APPLY, false, true, PLANES, 2>(ma, mb, md, mo, a, sms, s);
         default:
-            return ctas == 1 ? launch_tiles<APPLY, false, false, PLANES, 1>(ma, mb, mo, a, sms, s)
-                             : launch_tiles<APPLY, false, false, PLANES, 2>(ma, mb, mo, a, sms, s);
+            return ctas == 1 ? launch_tiles<APPLY, false, false, PLANES, 1>(ma, mb, md, mo, a, sms, s)
+                             : launch_tiles<APPLY, false, false, PLANES, 2>(ma, mb, md, mo, a, sms, s);
     }
 }
 

@@ -2,7 +2,7 @@
 // steps without going back to memory.
 //
 // The shorter side, up to 128, lies along the rows of tensor memory and the longer, up to 256, along its columns,
-// whichever of them is contiguous in memory. X stays in registers in f32, a thread holding half of a row; its f16
+// whichever of them is contiguous in memory. X stays in registers in f32, a thread holding a quarter of a row; its f16
 // planes (the one that is multiplied, or both) are in shared memory in 64-column panels, which the Gram matrix reads
 // K-major and the product with B MN-major. A and then B take one further buffer. Three products follow each other
 // in every step, each waiting for the previous one's epilogue: latency bounds it. One 128 x 128 bf16 matrix takes
@@ -24,7 +24,7 @@ namespace orth {
 
 namespace {
 
-constexpr int kRows = 128, kSmallThreads = 256;
+constexpr int kRows = 128, kSides = 4, kSmallThreads = kSides * kRows;
 
 struct Small {
     const void *g;
@@ -71,20 +71,35 @@ __device__ __forceinline__ void get8(unsigned char *base, int plane_bytes, int r
     }
 }
 
-// NC: columns that a thread holds (the longer side is 2 NC at most).
+// The values that a thread holds: which matrix, its row, and from which column on how many.
+struct Held {
+    int64_t item;
+    int r, c, count;
+    __device__ __forceinline__ Held(const Small &q, int block, int row, int c0, int most) {
+        const int slot = row / q.rows_each;
+        item = static_cast<int64_t>(block) * q.share + slot;
+        r = row - slot * q.rows_each;
+        c = c0;
+        count = slot < q.share && item < q.batch && r < q.m ? max(0, min(most, q.n - c0)) : 0;
+    }
+    __device__ __forceinline__ int64_t at(int64_t ld, int64_t stride, bool turned) const {
+        return count > 0 ? item * stride + (turned ? c * ld + r : r * ld + c) : 0;
+    }
+};
+
+// NC: columns that a thread holds (the longer side is 4 NC at most).
 template <typename T, int NC>
-__global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(const __grid_constant__ Small q) {
+__global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_constant__ Small q) {
     constexpr int PLANES = sizeof(T) == 4 ? 2 : 1, PAIRS = PLANES == 1 ? 1 : 3;
-    constexpr int N = 2 * NC, kPlaneX = N / 64 * kRows * 128, kPlaneP = 2 * kRows * 128;
+    constexpr int N = kSides * NC, kPlaneX = N / 64 * kRows * 128, kPlaneP = 2 * kRows * 128;
     constexpr uint32_t kColumns = N > kRows ? N : kRows;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const xs = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const ps = xs + PLANES * kPlaneX;
     __shared__ uint64_t bar;
     __shared__ uint32_t tmem_slot;
-    __shared__ double sums[8][2];
-    __shared__ float factors[8];
-    __shared__ double scales[8];
+    __shared__ double sums[4 * kSides][2];
+    __shared__ float2 factors[8];
     __shared__ int lost[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane, side = warp >> 2;
     if (warp == 0) {
@@ -99,12 +114,11 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(
     pdl_release();
     pdl_wait();
 
-    // this thread's half row
-    const int slot = row / q.rows_each, r = row - slot * q.rows_each, c0 = side * NC;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * q.share + slot;
-    const bool in = slot < q.share && item < q.batch && r < q.m;
-    const int held = in ? max(0, min(NC, q.n - c0)) : 0;
-    const T *const g = static_cast<const T *>(q.g) + (in ? item * q.stride_g + (q.turned ? c0 * q.ldg + r : r * q.ldg + c0) : 0);
+    // this thread's quarter of a row
+    const int slot = row / q.rows_each, c0 = side * NC;
+    const Held here(q, blockIdx.x, row, c0, NC);
+    const int held = here.count;
+    const T *const g = static_cast<const T *>(q.g) + here.at(q.ldg, q.stride_g, q.turned);
     float x[NC];
     constexpr int PER = 16 / sizeof(T);
     if (q.vec_g) {
@@ -122,21 +136,23 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(
         }
     } else {
         const int64_t step = q.turned ? q.ldg : 1;
+        const T *p = g;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) x[i] = i < held ? static_cast<float>(g[i * step]) : 0.f;
+        for (int i = 0; i < NC; ++i, p += step) x[i] = i < held ? static_cast<float>(*p) : 0.f;
     }
-    // the norm: 32 squares in f32, the rest in f64, of which an SM has little: a lane's sums, a warp's, the block's
+    // the norm: up to 32 squares in f32, the rest in f64, of which an SM has little: a lane's sums, a warp's, the block's
+    constexpr int GROUP = NC < 32 ? NC : 32;
     double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < NC; i += 32) {
+    for (int i = 0; i < NC; i += GROUP) {
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s = fmaf(x[i + e], x[i + e], s);
+        for (int e = 0; e < GROUP; ++e) s = fmaf(x[i + e], x[i + e], s);
         if (s >= 1e-25f && s <= 1e30f) {
             sum += s;
         } else if (held > i) {
 #pragma unroll 1
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < GROUP; ++e) {
                 const double y = e < held - i ? static_cast<double>(static_cast<float>(g[(i + e) * (q.turned ? q.ldg : 1)])) : 0.0;
                 sum = fma(y, y, sum);
             }
@@ -146,27 +162,17 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(
     if ((lane & 15) == 0) sums[warp][lane >> 4] = sum;
     __syncthreads();
     if (threadIdx.x < q.share) {
-        // its 32-row groups (or half of one), both halves of each row
+        // its 32-row groups (or half of one), all quarters of each row
         sum = 0.0;
         const int first = threadIdx.x * q.rows_each / 32, count = max(1, q.rows_each / 32), which = q.rows_each == 16 ? threadIdx.x & 1 : 0;
-        for (int w = first; w < first + count; ++w) sum += sums[w][which] + sums[w + 4][which];
-        const float f = static_cast<float>(sum);
-        const bool plain = f >= 1e-30f && f <= 1e30f;
-        const double scale = !(sum < INFINITY) ? NAN : sum == 0.0 || plain ? 0.0 : 8192.0 / sqrt(sum);
-        scales[threadIdx.x] = scale;
-        factors[threadIdx.x] = plain ? 8192.f / sqrtf(f) : 0.f;          // 0: the scale is to be used
+        for (int w = first; w < first + count; ++w) sum += (sums[w][which] + sums[w + 4][which]) + (sums[w + 8][which] + sums[w + 12][which]);
+        factors[threadIdx.x] = scale_of(sum);
     }
     __syncthreads();
-    const float factor = slot < q.share ? factors[slot] : 0.f;
-    const double scale = slot < q.share ? scales[slot] : 0.0;
-    bool bad = scale != scale;
-    if (factor != 0.f) {
+    const float2 factor = slot < q.share ? factors[slot] : make_float2(0.f, 0.f);
+    bool bad = factor.y != factor.y;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) x[i] *= factor;
-    } else {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) x[i] = bad || scale == 0.0 ? 0.f : static_cast<float>(x[i] * scale);
-    }
+    for (int i = 0; i < NC; ++i) x[i] = bad ? 0.f : x[i] * factor.x * factor.y;
 
     const auto x_out = [&] {
 #pragma unroll
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(
     };
     x_out();
     const int rows = q.share == 1 ? (q.m + 15) & ~15 : kRows;            // of A and B
-    const int cols = (q.n + 15) & ~15;
+    const int cols = (q.n + 31) & ~31;                                   // X is zero from n on
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t parity = 0;
     bool ok = true;
@@ -214,49 +220,51 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(
         parity ^= 1;
         tc::fence_after_sync();
     };
-    constexpr int PC = 64;                       // columns of A that a thread holds
+    constexpr int READ = NC == 32 ? 32 : 16;     // 64 values of X leave no room for more
+    constexpr int PC = kRows / kSides;           // columns of A that a thread holds
     const int p0 = side * PC, shift = 31 - __clz(q.rows_each), own = row >> shift;     // its matrix
+    const auto read = [&](int c, float (&t)[READ]) {
+        __syncwarp();
+        if constexpr (READ == 32) tc::tmem_ld32(tmem + lanes + c, t);
+        else tc::tmem_ld16(tmem + lanes + c, t);
+    };
+    const bool mine[2] = {p0 >> shift == own, (p0 + 16) >> shift == own};
 #pragma unroll 1
     for (int step = 0; step < q.steps; ++step) {
         // A, times 2^12
         product(true, false, cols, rows);
-#pragma unroll 1
-        for (int c = p0; c < p0 + PC; c += 32) {
-            float t[32];
-            __syncwarp();
-            tc::tmem_ld32(tmem + lanes + c, t);
+        float t[READ];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) t[i] = (c + i) >> shift == own ? t[i] * (4096.f / (8192.f * 8192.f)) : 0.f;
+        for (int h = 0; h < PC; h += READ) {
+            read(p0 + h, t);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) put8<PLANES>(ps, kPlaneP, row, c + i, t + i);
+            for (int i = 0; i < READ; ++i) t[i] = mine[(h + i) >> 4] ? t[i] * (4096.f / (8192.f * 8192.f)) : 0.f;
+#pragma unroll
+            for (int i = 0; i < READ; i += 8) put8<PLANES>(ps, kPlaneP, row, p0 + h + i, t + i);
         }
         // B = b A + c A A, times 2^12, in A's place
         product(false, false, rows, rows);
-#pragma unroll 1
-        for (int c = p0; c < p0 + PC; c += 32) {
-            float t[32];
-            __syncwarp();
-            tc::tmem_ld32(tmem + lanes + c, t);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+        for (int h = 0; h < PC; h += READ) {
+            read(p0 + h, t);
+#pragma unroll
+            for (int i = 0; i < READ; i += 8) {
                 float v[8];
-                get8<PLANES>(ps, kPlaneP, row, c + i, v);
+                get8<PLANES>(ps, kPlaneP, row, p0 + h + i, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = (c + i + e) >> shift == own ? fmaf(q.c / 4096.f, t[i + e], q.b * v[e]) : 0.f;
-                put8<PLANES>(ps, kPlaneP, row, c + i, v);
+                for (int e = 0; e < 8; ++e) v[e] = mine[(h + i) >> 4] ? fmaf(q.c / 4096.f, t[i + e], q.b * v[e]) : 0.f;
+                put8<PLANES>(ps, kPlaneP, row, p0 + h + i, v);
             }
         }
         // X
         product(false, true, rows, cols);
 #pragma unroll
-        for (int h = 0; h < NC; h += 32) {
-            float t[32];
-            __syncwarp();
-            tc::tmem_ld32(tmem + lanes + c0 + h, t);
+        for (int h = 0; h < NC; h += READ) {
+            if (c0 + h >= cols) break;
+            read(c0 + h, t);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float y = fmaf(q.a, x[h + i], t[i] * (1.f / 4096.f));
-                x[h + i] = c0 + h + i < q.n ? y : 0.f;
+            for (int i = 0; i < READ; ++i) {
+                x[h + i] = fmaf(q.a, x[h + i], t[i] * (1.f / 4096.f));
                 bad |= !(fabsf(x[h + i]) <= 65504.f);
             }
         }
@@ -268,7 +276,10 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(
     if (bad && slot < 8) lost[slot] = 1;
     __syncthreads();
     bad = slot < 8 && lost[slot];
-    T *const to = static_cast<T *>(q.x) + (in ? item * q.stride_x + (q.turned ? c0 * q.ldx + r : r * q.ldx + c0) : 0);
+    int again = row;                             // worked out again: kept, it crowds X out of its registers
+    asm volatile("" : "+r"(again));
+    const Held there(q, blockIdx.x, again, c0, NC);
+    T *const to = static_cast<T *>(q.x) + there.at(q.ldx, q.stride_x, q.turned);
     const auto value = [&](float f) {
         const float y = bad ? NAN : f * (1.f / 8192.f);
         if constexpr (PLANES == 1) return __float2bfloat16_rn(y);
@@ -280,19 +291,20 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(
             __align__(16) T v[PER];
 #pragma unroll
             for (int e = 0; e < PER; ++e) v[e] = value(x[i + e]);
-            if (i + PER <= held) {
+            if (i + PER <= there.count) {
                 *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(v);
             } else {
 #pragma unroll
                 for (int e = 0; e < PER; ++e)
-                    if (i + e < held) to[i + e] = v[e];
+                    if (i + e < there.count) to[i + e] = v[e];
             }
         }
     } else {
         const int64_t step = q.turned ? q.ldx : 1;
+        T *p = to;
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-            if (i < held) to[i * step] = value(x[i]);
+        for (int i = 0; i < NC; ++i, p += step)
+            if (i < there.count) *p = value(x[i]);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -303,7 +315,7 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 32 ? 2 : 1) small_kernel(
 template <typename T, int NC>
 cudaError_t launch(const Small &q, cudaStream_t s) {
     constexpr int PLANES = sizeof(T) == 4 ? 2 : 1;
-    constexpr int kSmem = PLANES * (2 * NC / 64 + 2) * kRows * 128 + 1024;
+    constexpr int kSmem = PLANES * (kSides * NC / 64 + 2) * kRows * 128 + 1024;
     static std::atomic<unsigned long long> done;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -318,7 +330,7 @@ cudaError_t launch(const Small &q, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t launch(const Small &q, cudaStream_t s) {
-    return q.n <= 64 ? launch<T, 32>(q, s) : q.n <= 128 ? launch<T, 64>(q, s) : launch<T, 128>(q, s);
+    return q.n <= 64 ? launch<T, 16>(q, s) : q.n <= 128 ? launch<T, 32>(q, s) : launch<T, 64>(q, s);
 }
 
 }  // namespace

@@ -52,6 +52,97 @@ struct List {
     }
 };
 
+// Sorted by all lanes of a warp, the largest in lane 0.
+__device__ __forceinline__ uint64_t sorted(uint64_t key) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size / 2; o > 0; o >>= 1) {
+            const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+            const bool larger = ((lane & o) == 0) == ((lane & size) == 0);      // this lane keeps the larger one
+            key = (key > other) == larger ? key : other;
+        }
+    return key;
+}
+
+// The `top` largest of many keys, by the WARPS warps that share a row.
+//
+// A floor first: of 32 interleaved sets of keys the `top`-th largest maximum, which `top` keys reach. Some 130 keys
+// at most reach it where their order is anything but contrived (of n in random order 32 ln(32 / (32 - top)), for top =
+// 20 that is 31); those are gathered in shared memory, and each finds its place by counting the larger ones. Where
+// more than kGathered reach the floor, a warp keeps a sorted list instead. Inserting all keys one by one into such a list
+// costs some 150 cycles for each that enters: 36 us for one row of 1000 blocks, against SELECT_ONE.
+constexpr int kGathered = 256;
+struct Gather {
+    uint64_t keys[kGathered], chosen[kMostTop], blocks[kMostTop], lanes[32];
+    int count;
+};
+template <int WARPS>
+__device__ __forceinline__ void row_sync() {
+    if constexpr (WARPS == 1) __syncwarp();
+    else __syncthreads();
+}
+// key(i) for i < n; `given`: a further key of this lane (0: none; first warp only). The result is g.chosen, 0 where there
+// are fewer. floor: what `top` keys are known to reach, or 0.
+template <int WARPS, typename F>
+__device__ __forceinline__ void select(Gather &g, int64_t n, uint64_t given, int top, uint64_t floor, const F &key) {
+    constexpr int HELD = 8;
+    constexpr int STEP = WARPS * 32;
+    const int lane = threadIdx.x & 31, thread = threadIdx.x % STEP;
+    const auto each = [&](const auto &f) {
+        for (int64_t i0 = thread; i0 - thread < n; i0 += STEP * HELD) {
+            uint64_t k[HELD];
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) k[h] = i0 + h * STEP < n ? key(i0 + h * STEP) : 0;
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) f(k[h]);
+        }
+    };
+    if (thread < 32) {
+        g.chosen[lane] = 0;
+        if (lane == 0) g.count = 0;
+    }
+    if (floor == 0) {
+        uint64_t most = 0;
+        each([&](uint64_t k) { most = k > most ? k : most; });
+        if constexpr (WARPS > 1) {
+            if (thread < 32) g.lanes[lane] = 0;
+            __syncthreads();
+            atomicMax(reinterpret_cast<unsigned long long *>(&g.lanes[lane]), static_cast<unsigned long long>(most));
+            __syncthreads();
+            most = g.lanes[lane];
+        }
+        floor = __shfl_sync(0xffffffffu, sorted(most), top - 1);
+    }
+    row_sync<WARPS>();
+    const auto gather = [&](uint64_t k) {
+        if (k != 0 && k >= floor) {
+            const int at = atomicAdd(&g.count, 1);
+            if (at < kGathered) g.keys[at] = k;
+        }
+    };
+    each(gather);
+    gather(given);
+    row_sync<WARPS>();
+    const int count = g.count;
+    if (count <= kGathered) {
+        for (int i = thread; i < count; i += STEP) {
+            const uint64_t k = g.keys[i];
+            int place = 0;
+            for (int j = 0; j < count; ++j) place += g.keys[j] > k;
+            if (place < top) g.chosen[place] = k;
+        }
+    } else if (thread < 32) {
+        List list;
+        list.start(0, top);
+        list.offer(given, top);
+        for (int64_t i0 = 0; i0 < n; i0 += 32) list.offer(i0 + lane < n ? key(i0 + lane) : 0, top);
+        if (lane < top) g.chosen[lane] = list.mine;
+    }
+    row_sync<WARPS>();
+}
+
 // The largest logit of every 32, where the logits come from the kernel for few rows. A warp takes 32 blocks.
 __global__ void __launch_bounds__(256) block_max_kernel(const float *logits, int64_t block_ld, int64_t vocab, int64_t groups,
                                                         int64_t all, float *block_max) {
@@ -115,7 +206,7 @@ struct Scores {
 template <int WARPS>
 __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Scores a) {
     constexpr int ROWS = 8 / WARPS, HELD = 8;
-    __shared__ uint64_t lists[8][kMostTop];
+    __shared__ Gather gathers[ROWS];
     pdl_release();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % WARPS;
@@ -124,60 +215,25 @@ __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Sco
     int64_t j = -1;
     if (row < a.rows) j = a.place ? a.place[row] : has_target(a.target, row, a.vocab) ? row : -1;
     const bool counts = j >= 0;
-    List list;
-    list.start(0, 1);
-    if (top > 0) {
-        uint64_t before = 0;
-        if (counts && !a.first && share == 0 && lane < top) before = a.best[j * top + lane];
-        // blocks: what the list holds already comes first among equals and is no block
-        list.start(before ? before | 0xffffffffull : 0, top);
-        const int64_t blocks = counts ? (a.n + 31) / 32 : 0;
-        const float *const most = a.block_max + (counts ? j : 0) * a.block_ld;
-        for (int64_t b0 = share * 32; b0 < blocks; b0 += WARPS * 32 * HELD) {
-            float m[HELD];
-#pragma unroll
-            for (int h = 0; h < HELD; ++h) {
-                const int64_t b = b0 + h * (WARPS * 32) + lane;
-                m[h] = b < blocks ? most[b] : NAN;
-            }
-#pragma unroll
-            for (int h = 0; h < HELD; ++h) list.offer(key_of(m[h], static_cast<uint32_t>(b0 + h * (WARPS * 32) + lane) + 1), top);
-        }
-        const auto join = [&] {                              // all warps' lists into the first warp's, and back
-            if constexpr (WARPS > 1) {
-                lists[warp][lane] = list.mine;
-                __syncthreads();
-                if (share == 0)
-                    for (int w = 1; w < WARPS; ++w) list.offer(lane < top ? lists[w][lane] : 0, top);
-                __syncthreads();
-            }
-        };
-        join();
-        uint64_t chosen = lane < top ? list.mine : 0;
-        if constexpr (WARPS > 1) {
-            if (share == 0) lists[0][lane] = chosen;
-            __syncthreads();
-            chosen = lists[0][lane];
-            __syncthreads();
-        }
-        // their logits
-        list.start(before, top);
-        const float *const s = a.logits + (counts ? j : 0) * a.block_ld * 32;
-        for (int i0 = share; i0 < top; i0 += WARPS * HELD) {
-            float v[HELD];
-            int64_t at[HELD];
-#pragma unroll
-            for (int h = 0; h < HELD; ++h) {
-                const int i = i0 + h * WARPS;
-                const uint64_t k = __shfl_sync(0xffffffffu, chosen, i & 31);
-                at[h] = i < top && k && index_of(k) ? static_cast<int64_t>(index_of(k) - 1) * 32 + lane : a.n;
-                v[h] = at[h] < a.n ? s[at[h]] : NAN;
-            }
-#pragma unroll
-            for (int h = 0; h < HELD; ++h) list.offer(key_of(v[h], static_cast<uint32_t>(a.v0 + at[h])), top);
-        }
-        join();
-        if (!a.last && counts && share == 0 && lane < top) a.best[j * top + lane] = list.mine;
+    uint64_t likeliest = 0;                              // the lane's
+    if (top > 0 && counts) {
+        Gather &g = gathers[warp / WARPS];
+        const uint64_t before = !a.first && share == 0 && lane < top ? a.best[j * top + lane] : 0;
+        // Blocks, by their largest logits. What the list holds already comes first among equals and is no block: its
+        // indices are below 32.
+        const float *const most = a.block_max + j * a.block_ld, *const s = a.logits + j * a.block_ld * 32;
+        select<WARPS>(g, (a.n + 31) / 32, before ? (before | 0xffffffffull) - lane : 0, top, 0,
+                      [&](int64_t b) { return key_of(most[b], static_cast<uint32_t>(b) + 32); });
+        if (share == 0) g.blocks[lane] = g.chosen[lane];
+        row_sync<WARPS>();
+        // their logits: as many as are wanted reach the last block's
+        select<WARPS>(g, top * 32, before, top, g.blocks[top - 1] >> 32 << 32, [&](int64_t i) -> uint64_t {
+            const uint64_t k = g.blocks[i >> 5];
+            const int64_t at = (static_cast<int64_t>(index_of(k)) - 32) * 32 + (i & 31);
+            return k && at >= 0 && at < a.n ? key_of(s[at], static_cast<uint32_t>(a.v0 + at)) : 0;
+        });
+        likeliest = g.chosen[lane];
+        if (!a.last && share == 0 && lane < top) a.best[j * top + lane] = likeliest;
     }
     if (!a.last || row >= a.rows || share != 0) return;
     float logp = 0.f, entropy = 0.f, lse = 0.f, ref = 0.f, log_sum = 0.f;
@@ -226,9 +282,9 @@ __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Sco
         a.lse[row] = lse;
     }
     if (lane < top) {
-        const bool there = sound && list.mine != 0;
-        a.top_logp[static_cast<int64_t>(row) * top + lane] = there ? (value_of(list.mine) - ref) - log_sum : counts ? NAN : 0.f;
-        a.top_id[static_cast<int64_t>(row) * top + lane] = there ? static_cast<int64_t>(index_of(list.mine)) : -1;
+        const bool there = sound && likeliest != 0;
+        a.top_logp[static_cast<int64_t>(row) * top + lane] = there ? (value_of(likeliest) - ref) - log_sum : counts ? NAN : 0.f;
+        a.top_id[static_cast<int64_t>(row) * top + lane] = there ? static_cast<int64_t>(index_of(likeliest)) : -1;
     }
 }
 
