@@ -160,22 +160,33 @@ int tiles_of(const Shape &s, bool symmetric) {
         n += std::min<int64_t>(s.tiles_n, cdiv(static_cast<int64_t>(tm + 1) * s.ctas * kTileM, s.tile_n));
     return n;
 }
-// The tile that takes the least time: rounds of all SMs, times a tile's steps. A step takes as long as its columns
-// plus what its operands' way into shared memory adds where few columns share a row tile.
+// Cycles of a 64-deep step: the products' own, 8192 multiply-adds a cycle on two SMs, or the operands' way into shared
+// memory, 64 bytes a cycle and SM, whichever takes longer.
+int64_t step_cycles(int ctas, int tile_n, int planes) {
+    const int64_t products = (planes == 1 ? 1 : 3) * 2 * tile_n, bytes = planes * (kTileM * 128 + tile_n / ctas * 128);
+    return std::max(products, bytes / 64);
+}
+// The tile that takes the least time, in rounds of all SMs. What comes before and after a round's steps takes some
+// 2000 cycles.
 Shape shape_for(int64_t rows, int64_t cols, bool symmetric, bool b_mn, int64_t batch, int64_t kblocks, int planes, int sms) {
     Shape best{};
     int64_t least = 0;
-    for (int ctas = 1; ctas <= 2; ++ctas) {
-        if (ctas == 2 && rows <= kTileM) break;
+    for (int ctas = 2; ctas >= 1; --ctas) {
+        if (ctas == 2 && rows <= kTileM) continue;
         for (int t = ctas * 128; t >= (ctas == 2 && b_mn ? 128 : 64); t /= 2) {        // a pair's halves: whole groups of 64
             Shape s{ctas, t, static_cast<int>(cdiv(rows, ctas * kTileM)), static_cast<int>(cdiv(cols, t)), 0};
             s.per_item = tiles_of(s, symmetric);
             const int64_t rounds = cdiv(batch * s.per_item, std::max(1, sms / ctas));
-            const int64_t cost = rounds * (kblocks * (planes == 1 ? 1 : 3) * (t + (ctas == 1 ? 64 : 32)) + 1000);
+            const int64_t cost = rounds * (kblocks * step_cycles(ctas, t, planes) + 2000);
             if (best.ctas == 0 || cost < least) best = s, least = cost;
         }
     }
     return best;
+}
+template <int PLANES>
+int stages_of(const Shape &s, bool adds) {
+    const int stage = s.ctas == 1 ? Ring<PLANES, 1>::stage(s.tile_n) : Ring<PLANES, 2>::stage(s.tile_n);
+    return std::min(kMostStages, (adds ? Ring<PLANES, 1>::kBytesAdd : Ring<PLANES, 1>::kBytes) / stage);
 }
 
 struct Plan {
@@ -277,7 +288,7 @@ bl_status run(const Plan &q, const Call &c) {
         BL_MAP(make_map(&user_out, PLANES == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sizeof(T), c.X, q.width,
                         q.lines, q.batch, c.ldx, q.batch == 1 ? c.ldx * q.lines : c.stride_x, 32, PLANES == 1 ? 64 : 128));
 
-    const auto args = [&](const Shape &s, int64_t rows, int64_t cols, int64_t k) {
+    const auto args = [&](const Shape &s, int64_t rows, int64_t cols, int64_t k, int planes_add) {
         Args r{};
         r.batch = static_cast<int>(q.batch);
         r.rows = static_cast<int>(rows), r.cols = static_cast<int>(cols);
@@ -286,6 +297,8 @@ bl_status run(const Plan &q, const Call &c) {
         r.tile_n = s.tile_n, r.tiles_m = s.tiles_m, r.tiles_n = s.tiles_n;
         r.per_item = s.per_item, r.total = static_cast<int>(q.batch * s.per_item);
         r.planes_out = PLANES;
+        r.planes_add = planes_add;
+        r.stages = stages_of<PLANES>(s, planes_add > 0);
         r.gave_up = gave_up;
         return r;
     };
@@ -293,11 +306,12 @@ bl_status run(const Plan &q, const Call &c) {
     BL_MAP(operand(&sq_a, q, false, 0, false, kTileM));
     BL_MAP(operand(&sq_b, q, false, 0, false, q.square.tile_n / q.square.ctas));
     BL_MAP(operand(&ap_s, q, false, 1, false, q.wide ? kTileM : q.apply.tile_n / q.apply.ctas));
-    Args gram = args(q.gram, q.small, q.small, std::max(q.lines, q.width));
+    Args gram = args(q.gram, q.small, q.small, std::max(q.lines, q.width), 0);
     gram.alpha = kScaleA / (kScaleX * kScaleX);
-    Args square = args(q.square, q.small, q.small, q.small);
+    Args square = args(q.square, q.small, q.small, q.small, PLANES);
     square.alpha = cc / kScaleA, square.beta = b;
-    square.planes_add = PLANES;
+    gram.result = reinterpret_cast<__half *>(c.ws + q.a), square.result = reinterpret_cast<__half *>(c.ws + q.b);
+    gram.result_ld = square.result_ld = q.lda;
     for (int step = 0; step < c.steps; ++step) {
         const int from = step & 1;
         CUtensorMap x_gram_a, x_gram_b, x_apply;
@@ -306,9 +320,8 @@ bl_status run(const Plan &q, const Call &c) {
         BL_MAP(operand(&x_apply, q, true, from, q.wide, kTileM));
         BL_TRY(product(q.wide ? GRAM_LINES : GRAM_WIDTH, q.gram.ctas, x_gram_a, x_gram_b, a_out, a_out, gram, c.sms, c.s));
         BL_TRY(product(SQUARE, q.square.ctas, sq_a, sq_b, a_out, b_out, square, c.sms, c.s));
-        Args apply = args(q.apply, q.lines, q.width, q.small);
+        Args apply = args(q.apply, q.lines, q.width, q.small, 2);
         apply.alpha = 1 / kScaleA, apply.beta = a;
-        apply.planes_add = 2;
         apply.planes_out = 2;
         apply.last = step + 1 == c.steps;
         if (apply.last) {

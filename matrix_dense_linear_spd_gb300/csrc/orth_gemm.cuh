@@ -58,19 +58,20 @@ __device__ __forceinline__ float2 scale_of(double sum) {
     return make_float2(power, static_cast<float>(kScaleX / (norm * power)));
 }
 
-// Shared memory of a CTA: the operands' ring (a pair shares tiles of 256 columns, a single CTA has 128), and 4 KB for
-// each epilogue warp's lines on their way out. What a product is added to comes in by TMA too: with one plane into lines of its
-// own, so that a block's are on their way while the previous block is worked on, with two (whose products take
-// three times as long) into those that the result leaves by. Read with 16-byte loads, each lane its own row, those lines took
-// the epilogue past the products: 12 x 1024 x 4096 bf16, B X 133 us.
+// Shared memory of a CTA: the operands' ring, and 4 KB for each epilogue warp's lines on their way out. What a product is
+// added to comes in by TMA too: with one plane into lines of its own, so that a block's are on their way while the
+// previous block is worked on, with two (whose products take three times as long) into those that the result
+// leaves by. (Read with 16-byte loads, each lane its own row, it held the products up: 12 x 1024 x 4096 bf16, five steps
+// 1160 us, so 970.) A stage is as small as the tile's columns allow: the narrow tiles of small matrices wait for memory,
+// 1.3 us a stage, so the more of them are on their way the better.
+constexpr int kMostStages = 8;
 template <int PLANES, int CTAS>
 struct Ring {
-    static constexpr int kTile = CTAS == 1 ? 128 : 256;
-    static constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTile / CTAS * kTileK * 2;
-    static constexpr int kStageA = PLANES * kBytesA, kStageB = PLANES * kBytesB;
-    static constexpr int kStages = PLANES == 1 ? 5 : 3;
-    static constexpr int kLines = kEpilogueWarps * kStageBytes * (PLANES == 1 ? 2 : 1);
-    static constexpr int kSmem = kStages * (kStageA + kStageB) + kLines + 1024;
+    static constexpr int kTile = CTAS == 1 ? 128 : 256;             // columns of a tile, at most
+    static constexpr int kBytesA = kTileM * kTileK * 2, kStageA = PLANES * kBytesA;
+    static constexpr int kBytes = 192 * 1024, kBytesAdd = PLANES == 1 ? 160 * 1024 : kBytes;     // where something is added
+    static constexpr int kSmem = kBytes + kEpilogueWarps * kStageBytes + 1024;
+    static constexpr int stage(int tile_n) { return kStageA + PLANES * (tile_n / CTAS * 128); }
 };
 
 struct Args {
@@ -80,7 +81,10 @@ struct Args {
     int tile_n, tiles_m, tiles_n;
     int per_item, total;       // tiles
     float alpha, beta;         // result = alpha * product + beta * what is added
+    int stages;                // of the ring
     int planes_add;            // of the f16 matrix that is added; 0: none
+    __half *result;            // SYMMETRIC: [plane][item][rows][result_ld]
+    int64_t result_ld;
     int planes_out;            // of the f16 result
     bool last;                 // APPLY: the result is the caller's, f32 or bf16
     void *out;                 // where its lines do not start on 16-byte boundaries: stored without TMA
@@ -235,15 +239,15 @@ __device__ __forceinline__ void block_out(const Args &a, const Work &w, int row0
                                                                                   pack(lo[8 * j + 4], lo[8 * j + 5]), pack(lo[8 * j + 6], lo[8 * j + 7]));
     }
     lines_store(map, stage, col0, row0, w.item, z1);
-    if (KIND == SYMMETRIC && row0 > col0) {
-        // the same block in its place above the diagonal: line i is column i, a lane's value at the lane's place
-        lines_free();
+    if (KIND == SYMMETRIC && row0 > col0 && row0 + lane < a.rows) {
+        // the same block in its place above the diagonal: column i is a line there, on which the lanes lie side by side
+        __half *p = a.result + (static_cast<int64_t>(w.item) * a.rows + col0) * a.result_ld + row0 + lane;
+        const int64_t plane = static_cast<int64_t>(a.batch) * a.rows * a.result_ld;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            *reinterpret_cast<__half *>(stage + at64(i, lane >> 3) + (lane & 7) * 2) = hi[i];
-            if (z1 >= 0) *reinterpret_cast<__half *>(stage + 2048 + at64(i, lane >> 3) + (lane & 7) * 2) = lo[i];
+        for (int i = 0; i < 32; ++i, p += a.result_ld) {
+            *p = hi[i];                              // col0 + 31 < row0: such lines are there
+            if (z1 >= 0) p[plane] = lo[i];
         }
-        lines_store(map, stage, row0, col0, w.item, z1);
     }
 }
 
@@ -253,13 +257,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap map_add, const __grid_constant__ CUtensorMap map_out,
                    const __grid_constant__ Args a) {
     using R = Ring<PLANES, CTAS>;
-    constexpr int kBytesA = R::kBytesA, kBytesB = R::kBytesB, kStageA = R::kStageA, kStageB = R::kStageB, kStages = R::kStages;
-    constexpr int PAIRS = PLANES == 1 ? 1 : 3, kHalf = R::kTile / 2, BLOCKS = kHalf / 32;
+    constexpr int kBytesA = R::kBytesA, kStageA = R::kStageA;
+    constexpr int PAIRS = PLANES == 1 ? 1 : 3, BLOCKS = R::kTile / 64;
+    const uint32_t stages = a.stages, bytes_b = a.tile_n / CTAS * 128, stage_b = PLANES * bytes_b;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char *const tiles_a = base, *const tiles_b = base + kStages * kStageA;
-    unsigned char *const staging = base + kStages * (kStageA + kStageB);
-    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], add_full[kEpilogueWarps], drained;
+    unsigned char *const tiles_a = base, *const tiles_b = base + stages * kStageA;
+    unsigned char *const staging = base + R::kBytes;
+    __shared__ uint64_t full[kMostStages], empty[kMostStages], acc_full[2], acc_empty[2], add_full[kEpilogueWarps], drained;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rank = CTAS == 1 ? 0 : tc::cluster_rank();
     if (warp == 1) tc::tmem_take<CTAS>(&tmem_slot, 512);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMostStages; ++s) {
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tc::tma_load_3d<CTAS>(d, &map_a, bar, kb * kTileK, m0, z);
                             }
                         } else {
-                            unsigned char *const d = tiles_b + s * kStageB + p * kBytesB;
+                            unsigned char *const d = tiles_b + s * stage_b + p * bytes_b;
                             if constexpr (B_MN) {
 #pragma unroll 1
                                 for (int j = 0; j < groups_b; ++j)
@@ -337,16 +342,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    issued = min(issued + 1, static_cast<uint32_t>(kStages));
-                    if (++s == kStages) s = 0, phase ^= 1;
+                    issued = min(issued + 1, stages);
+                    if (++s == stages) s = 0, phase ^= 1;
                 }
             }
             if (!ok) {
                 gave_up = 1;
                 // the copies in flight: the last `issued` stages before s, oldest first
                 for (uint32_t i = 0; rank == 0 && i < issued; ++i) {
-                    const uint32_t t = s + kStages - issued + i;
-                    tc::mbar_wait(&full[t % kStages], t >= kStages ? phase : phase ^ 1, kPolls);
+                    const uint32_t t = s + stages - issued + i;
+                    tc::mbar_wait(&full[t % stages], t >= stages ? phase : phase ^ 1, kPolls);
                 }
             }
         }
@@ -373,18 +378,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         tc::fence_after_sync();
-                        const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (kStageB >> 4);
+                        const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (stage_b >> 4);
 #pragma unroll
                         for (int q = 0; q < PAIRS; ++q) {
                             const int pa = PLANES == 2 && q == 1, pb = PLANES == 2 && q == 0;       // hi lo, lo hi, hi hi
 #pragma unroll
                             for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
                                 tc::mma_f16<CTAS>(acc, da + pa * (kBytesA >> 4) + j * (A_MN ? 2048 / 16 : 2),
-                                                  db + pb * (kBytesB >> 4) + j * (B_MN ? 2048 / 16 : 2), idesc,
+                                                  db + pb * (bytes_b >> 4) + j * (B_MN ? 2048 / 16 : 2), idesc,
                                                   i > 0 || q > 0 || j > 0);
                         }
                         tc::mma_commit_all<CTAS>(&empty[s]);
-                        if (++s == kStages) s = 0, phase ^= 1;
+                        if (++s == stages) s = 0, phase ^= 1;
                     }
                     if (ok) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
                 }
@@ -400,15 +405,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::regs_inc<kRegsMany>();
         const int quad = warp & 3, half = (warp - 4) >> 2;  // a warp may read its quarter of the lanes
         unsigned char *const stage = staging + (warp - 4) * kStageBytes;
-        unsigned char *const lines = PLANES == 1 ? stage + kEpilogueWarps * kStageBytes : stage;
+        unsigned char *const lines = PLANES == 1 ? base + R::kBytesAdd + (warp - 4) * kStageBytes : stage;
         uint64_t *const bar = &add_full[warp - 4];
         const bool adds = a.planes_add > 0;
         uint32_t done = 0, asked = 0;
         bool ok = true;
         for (int w = blockIdx.x / CTAS; ok && w < a.total; w += gridDim.x / CTAS) {
             const Work k = work_of<KIND, CTAS>(w, a);
-            const int n0 = k.tn * a.tile_n, row0 = (k.tm * CTAS + rank) * kTileM + quad * 32, first = half * kHalf;
-            int cols = min(min(a.cols - n0, a.tile_n), first + kHalf);                     // this warp's end there
+            const int n0 = k.tn * a.tile_n, row0 = (k.tm * CTAS + rank) * kTileM + quad * 32, first = half * (a.tile_n / 2);
+            int cols = min(a.cols - n0, first + a.tile_n / 2);                     // this warp's end there
             if (KIND == SYMMETRIC) cols = min(cols, row0 + 32 - n0);                       // or with the diagonal's block
             if (row0 >= a.rows) cols = 0;
             if constexpr (PLANES == 1) {
