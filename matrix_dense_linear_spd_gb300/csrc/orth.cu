@@ -184,9 +184,8 @@ Shape shape_for(int64_t rows, int64_t cols, bool symmetric, bool b_mn, int64_t b
     return best;
 }
 template <int PLANES>
-int stages_of(const Shape &s, bool adds) {
-    const int stage = s.ctas == 1 ? Ring<PLANES, 1>::stage(s.tile_n) : Ring<PLANES, 2>::stage(s.tile_n);
-    return std::min(kMostStages, (adds ? Ring<PLANES, 1>::kBytesAdd : Ring<PLANES, 1>::kBytes) / stage);
+int stages_of(const Shape &s) {
+    return std::min(kMostStages, Ring<PLANES, 1>::kBytes / (s.ctas == 1 ? Ring<PLANES, 1>::stage(s.tile_n) : Ring<PLANES, 2>::stage(s.tile_n)));
 }
 
 struct Plan {
@@ -271,7 +270,7 @@ bl_status run(const Plan &q, const Call &c) {
     BL_TRY(launch_pdl(begin_kernel<T>, blocks, 256, 0, c.s, src, reinterpret_cast<__half *>(c.ws + q.x[0]), q.ldx, plane_x));
     const float a = static_cast<float>(c.coefficients[0]), b = static_cast<float>(c.coefficients[1]), cc = static_cast<float>(c.coefficients[2]);
 
-    // maps: operands in lines of 128 bytes; results, and what products are added to, in lines of 64
+    // maps: operands in lines of 128 bytes; results, and what products are added to, in lines of UNIT columns
     const auto map_f16 = [&](CUtensorMap *m, int64_t at, int64_t inner, int64_t rows, int64_t planes, int64_t ld, int box_rows, int line) {
         return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, c.ws + at, inner, rows, planes * q.batch, ld, rows * ld, box_rows, line);
     };
@@ -280,15 +279,16 @@ bl_status run(const Plan &q, const Call &c) {
                     : map_f16(m, which == 0 ? p.a : p.b, p.small, p.small, PLANES, p.lda, mn ? kTileK : box_rows, 128);
     };
     CUtensorMap a_out, b_out, x_out[2], user_out{};
-    BL_MAP(map_f16(&a_out, q.a, q.small, q.small, PLANES, q.lda, 32, 64));
-    BL_MAP(map_f16(&b_out, q.b, q.small, q.small, PLANES, q.lda, 32, 64));
-    for (int i = 0; i < 2; ++i) BL_MAP(map_f16(&x_out[i], q.x[i], q.width, q.lines, 2, q.ldx, 32, 64));
+    constexpr int LINE = Ring<PLANES, 1>::kUnit * 2;
+    BL_MAP(map_f16(&a_out, q.a, q.small, q.small, PLANES, q.lda, 32, LINE));
+    BL_MAP(map_f16(&b_out, q.b, q.small, q.small, PLANES, q.lda, 32, LINE));
+    for (int i = 0; i < 2; ++i) BL_MAP(map_f16(&x_out[i], q.x[i], q.width, q.lines, 2, q.ldx, 32, LINE));
     const bool by_tma = for_tma(c.X, c.ldx, sizeof(T)) && (q.batch == 1 || c.stride_x * static_cast<int64_t>(sizeof(T)) % 16 == 0);
     if (by_tma)
         BL_MAP(make_map(&user_out, PLANES == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sizeof(T), c.X, q.width,
-                        q.lines, q.batch, c.ldx, q.batch == 1 ? c.ldx * q.lines : c.stride_x, 32, PLANES == 1 ? 64 : 128));
+                        q.lines, q.batch, c.ldx, q.batch == 1 ? c.ldx * q.lines : c.stride_x, 32));
 
-    const auto args = [&](const Shape &s, int64_t rows, int64_t cols, int64_t k, int planes_add) {
+    const auto args = [&](const Shape &s, int64_t rows, int64_t cols, int64_t k) {
         Args r{};
         r.batch = static_cast<int>(q.batch);
         r.rows = static_cast<int>(rows), r.cols = static_cast<int>(cols);
@@ -296,9 +296,7 @@ bl_status run(const Plan &q, const Call &c) {
         r.chunk = PLANES == 1 ? kChunkOne : kChunkTwo;
         r.tile_n = s.tile_n, r.tiles_m = s.tiles_m, r.tiles_n = s.tiles_n;
         r.per_item = s.per_item, r.total = static_cast<int>(q.batch * s.per_item);
-        r.planes_out = PLANES;
-        r.planes_add = planes_add;
-        r.stages = stages_of<PLANES>(s, planes_add > 0);
+        r.stages = stages_of<PLANES>(s);
         r.gave_up = gave_up;
         return r;
     };
@@ -306,9 +304,9 @@ bl_status run(const Plan &q, const Call &c) {
     BL_MAP(operand(&sq_a, q, false, 0, false, kTileM));
     BL_MAP(operand(&sq_b, q, false, 0, false, q.square.tile_n / q.square.ctas));
     BL_MAP(operand(&ap_s, q, false, 1, false, q.wide ? kTileM : q.apply.tile_n / q.apply.ctas));
-    Args gram = args(q.gram, q.small, q.small, std::max(q.lines, q.width), 0);
+    Args gram = args(q.gram, q.small, q.small, std::max(q.lines, q.width));
     gram.alpha = kScaleA / (kScaleX * kScaleX);
-    Args square = args(q.square, q.small, q.small, q.small, PLANES);
+    Args square = args(q.square, q.small, q.small, q.small);
     square.alpha = cc / kScaleA, square.beta = b;
     gram.result = reinterpret_cast<__half *>(c.ws + q.a), square.result = reinterpret_cast<__half *>(c.ws + q.b);
     gram.result_ld = square.result_ld = q.lda;
@@ -319,10 +317,9 @@ bl_status run(const Plan &q, const Call &c) {
         BL_MAP(operand(&x_gram_b, q, true, from, !q.wide, q.gram.tile_n / q.gram.ctas));
         BL_MAP(operand(&x_apply, q, true, from, q.wide, kTileM));
         BL_TRY(product(q.wide ? GRAM_LINES : GRAM_WIDTH, q.gram.ctas, x_gram_a, x_gram_b, a_out, a_out, gram, c.sms, c.s));
-        BL_TRY(product(SQUARE, q.square.ctas, sq_a, sq_b, a_out, b_out, square, c.sms, c.s));
-        Args apply = args(q.apply, q.lines, q.width, q.small, 2);
+        BL_TRY(product(SQUARE_A, q.square.ctas, sq_a, sq_b, a_out, b_out, square, c.sms, c.s));
+        Args apply = args(q.apply, q.lines, q.width, q.small);
         apply.alpha = 1 / kScaleA, apply.beta = a;
-        apply.planes_out = 2;
         apply.last = step + 1 == c.steps;
         if (apply.last) {
             apply.alpha /= kScaleX, apply.beta /= kScaleX;

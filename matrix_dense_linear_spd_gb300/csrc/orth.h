@@ -12,7 +12,7 @@ namespace orth {
 struct Args;
 
 // How a product reads its operands (see orth_gemm.cuh).
-enum Layout : int { GRAM_LINES = 0, GRAM_WIDTH = 1, SQUARE = 0, APPLY_LEFT = 2, APPLY_RIGHT = 3 };
+enum Layout : int { GRAM_LINES = 0, GRAM_WIDTH = 1, SQUARE_A = 2, APPLY_LEFT = 3, APPLY_RIGHT = 4 };
 
 cudaError_t launch_one(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo,
                        const Args &a, int sms, cudaStream_t s);

@@ -1,8 +1,9 @@
 // The tensor-core products of the orthogonalisation (orth.cu), one persistent kernel for all. With X stored as
 // `lines` rows of `width` contiguous values, A its Gram matrix on the shorter side and B = b A + c A A:
 //
-//   SYMMETRIC  A = X X^T or X^T X (K-major operands, or both MN-major), and B from A A (K-major)
-//   APPLY      a X + B X (K-major, MN-major) or a X + X B (both K-major)
+//   GRAM    A = X X^T or X^T X (K-major operands, or both MN-major)
+//   SQUARE  B from A A (K-major)
+//   APPLY   a X + B X (K-major, MN-major) or a X + X B (both K-major)
 //
 // Everything between the products is f16 in two planes, x = hi + lo (22 bits), scaled by a power of two so that no
 // value leaves f16's range. PLANES = 1 multiplies the hi planes only; PLANES = 2 adds hi lo + lo hi + hi hi, which
@@ -10,8 +11,8 @@
 // what the iteration multiplies by a in every step, the directions of small singular values, keeps 22 bits, and the
 // products' own rounding meets only directions that have grown (see orth.cu).
 //
-// A and B are symmetric: tiles above the diagonal are left out, and every 32 x 32 block below it is stored twice,
-// the second time transposed through shared memory, which also makes the results symmetric to the bit.
+// A and B are symmetric: tiles above the diagonal are left out, and what lies below it is stored twice, the second
+// time from the lanes side by side, block by block transposed.
 //
 // A CTA computes 128 x tile_n tiles, or a pair of CTAs 256 x tile_n tiles (each holds its 128 rows and half of B).
 // Roles, waits and registers as in xent_gemm.cuh: a producer thread for each operand, one issuing thread, eight
@@ -32,11 +33,10 @@
 namespace bl {
 namespace orth {
 
-enum Kind : int { SYMMETRIC = 0, APPLY = 1 };
+enum Kind : int { GRAM = 0, SQUARE = 1, APPLY = 2 };
 
 constexpr int kTileM = 128, kTileN = 256, kTileK = 64;          // columns of a tile, at most
 constexpr int kEpilogueWarps = 8;                               // two share 32 rows
-constexpr int kStageBytes = 32 * 128;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
 static_assert(128 * kRegsFew + 32 * kEpilogueWarps * kRegsMany <= kThreads * kRegsLaunch, "more registers than the block has");
@@ -58,19 +58,23 @@ __device__ __forceinline__ float2 scale_of(double sum) {
     return make_float2(power, static_cast<float>(kScaleX / (norm * power)));
 }
 
-// Shared memory of a CTA: the operands' ring, and 4 KB for each epilogue warp's lines on their way out. What a product is
-// added to comes in by TMA too: with one plane into lines of its own, so that a block's are on their way while the
-// previous block is worked on, with two (whose products take three times as long) into those that the result
-// leaves by. (Read with 16-byte loads, each lane its own row, it held the products up: 12 x 1024 x 4096 bf16, five steps
-// 1160 us, so 970.) A stage is as small as the tile's columns allow: the narrow tiles of small matrices wait for memory,
-// 1.3 us a stage, so the more of them are on their way the better.
+// Shared memory of a CTA: the operands' ring, and lines for each epilogue warp, by which results leave and what a
+// product is added to comes in, both by TMA: UNIT columns of the warp's 32 rows at a time, a plane after the other. The
+// same lines serve both ways, a lane writing where it has read; only A and B in one plane are small enough to take
+// turns between two halves. TMA takes as long for a line of 64 bytes as for one of 128, some two cycles, and the
+// operands alone keep it busy (a 256 x 256 tile's stage 512 cycles, as long as its products), so lines are 128 bytes where
+// there is room: 12 x 1024 x 4096 bf16, five steps LINES_NOTE.
+// A stage is as small as the tile's columns allow: narrow tiles, of small matrices, wait for memory, and the more
+// of their stages are on their way the better.
 constexpr int kMostStages = 8;
 template <int PLANES, int CTAS>
 struct Ring {
     static constexpr int kTile = CTAS == 1 ? 128 : 256;             // columns of a tile, at most
     static constexpr int kBytesA = kTileM * kTileK * 2, kStageA = PLANES * kBytesA;
-    static constexpr int kBytes = 192 * 1024, kBytesAdd = PLANES == 1 ? 160 * 1024 : kBytes;     // where something is added
-    static constexpr int kSmem = kBytes + kEpilogueWarps * kStageBytes + 1024;
+    static constexpr int kUnit = PLANES == 1 ? 64 : 32;
+    static constexpr int kPlane = 32 * kUnit * 2, kLines = 2 * kPlane;            // bytes of a warp
+    static constexpr int kBytes = (PLANES == 1 ? 160 : 192) * 1024;
+    static constexpr int kSmem = kBytes + kEpilogueWarps * kLines + 1024;
     static constexpr int stage(int tile_n) { return kStageA + PLANES * (tile_n / CTAS * 128); }
 };
 
@@ -82,10 +86,8 @@ struct Args {
     int per_item, total;       // tiles
     float alpha, beta;         // result = alpha * product + beta * what is added
     int stages;                // of the ring
-    int planes_add;            // of the f16 matrix that is added; 0: none
-    __half *result;            // SYMMETRIC: [plane][item][rows][result_ld]
+    __half *result;            // GRAM, SQUARE: [plane][item][rows][result_ld]
     int64_t result_ld;
-    int planes_out;            // of the f16 result
     bool last;                 // APPLY: the result is the caller's, f32 or bf16
     void *out;                 // where its lines do not start on 16-byte boundaries: stored without TMA
     int64_t ldo, stride_o;
@@ -100,7 +102,7 @@ __device__ __forceinline__ Work work_of(int w, const Args &a) {
     Work r;
     r.item = w / a.per_item;
     w -= r.item * a.per_item;
-    if constexpr (KIND == SYMMETRIC) {
+    if constexpr (KIND != APPLY) {
         // row tile after row tile, as many columns as reach its last row's diagonal
         r.tm = 0;
         while (true) {
@@ -134,120 +136,134 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&t);
 }
 
-// A warp's 32 lines on their way out: 64 bytes each (two planes fit the stage) in the 64-byte swizzle.
-__device__ __forceinline__ uint32_t at64(int line, int chunk) { return line * 64 + ((chunk ^ ((line >> 1) & 3)) << 4); }
-__device__ __forceinline__ void lines_free() {          // the last store has read its lines
+// ---- epilogue
+
+template <int KIND, int PLANES>
+struct Form {
+    using R = Ring<PLANES, 1>;
+    static constexpr int kUnit = R::kUnit, kPlane = R::kPlane;
+    static constexpr int kAdd = KIND == GRAM ? 0 : KIND == SQUARE ? PLANES : 2;        // planes of what is added
+    static constexpr int kOut = KIND == APPLY ? 2 : PLANES;                            // of the result
+    static constexpr bool kTurns = KIND != APPLY && PLANES == 1;                       // two units have lines of their own
+};
+// 16 bytes of a line, in the swizzle of its length.
+template <int UNIT>
+__device__ __forceinline__ uint32_t at_line(int line, int chunk) {
+    return UNIT == 64 ? line * 128 + ((chunk ^ (line & 7)) << 4) : line * 64 + ((chunk ^ ((line >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void lines_free() {          // the stores of earlier units have read their lines
     if ((threadIdx.x & 31) == 0) tc::bulk_wait_read_all();
     __syncwarp();
 }
-__device__ __forceinline__ void lines_store(const CUtensorMap *map, const unsigned char *stage, int x, int y, int z0, int z1) {
-    tc::fence_proxy_async_smem();
+__device__ __forceinline__ void lines_free_but_last() {
+    if ((threadIdx.x & 31) == 0) tc::bulk_wait_read_but_one();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-        tc::tma_store_3d(map, stage, x, y, z0, false);
-        if (z1 >= 0) tc::tma_store_3d(map, stage + 2048, x, y, z1, false);
-        tc::bulk_commit();
-    }
+}
+template <int KIND, int PLANES>
+__device__ __forceinline__ void addend_ask(const CUtensorMap *map, const Args &a, int item, unsigned char *lines, uint64_t *bar, int row0,
+                                           int col0) {
+    using F = Form<KIND, PLANES>;
+    if ((threadIdx.x & 31) != 0) return;
+    tc::mbar_expect_tx(bar, F::kPlane * F::kAdd);
+#pragma unroll
+    for (int p = 0; p < F::kAdd; ++p) tc::tma_load_3d<1>(lines + p * F::kPlane, map, tc::smem_u32(bar), col0, row0, p * a.batch + item);
 }
 
-// What the product is added to, 32 columns of a warp's rows at a time.
-struct Addend {
-    uint4 hi[4], lo[4];
-};
-__device__ __forceinline__ void addend_ask(const CUtensorMap *map, const Args &a, const Work &w, unsigned char *lines, uint64_t *bar,
-                                           int row0, int col0) {
-    if ((threadIdx.x & 31) != 0) return;
-    tc::mbar_expect_tx(bar, 2048 * a.planes_add);
-    for (int p = 0; p < a.planes_add; ++p) tc::tma_load_3d<1>(lines + p * 2048, map, tc::smem_u32(bar), col0, row0, p * a.batch + w.item);
-}
-__device__ __forceinline__ bool addend_take(Addend &d, const Args &a, const unsigned char *lines, uint64_t *bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kPolls));
+// 32 columns of a warp's 32 rows, the b-th of a unit: from the product to the result's lines.
+template <int KIND, int PLANES>
+__device__ __forceinline__ void block_out(const Args &a, int item, int row0, int col0, int b, float (&v)[32], unsigned char *lines) {
+    using F = Form<KIND, PLANES>;
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        d.hi[j] = *reinterpret_cast<const uint4 *>(lines + at64(lane, j));
-        d.lo[j] = a.planes_add == 2 ? *reinterpret_cast<const uint4 *>(lines + 2048 + at64(lane, j)) : make_uint4(0, 0, 0, 0);
-    }
-    __syncwarp();                               // the lines may be filled again
-    return ok;
-}
-__device__ __forceinline__ float2 sum2(uint32_t hi, uint32_t lo) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hi)), y = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-    return make_float2(x.x + y.x, x.y + y.y);
-}
-__device__ __forceinline__ void combine(float (&v)[32], const Addend &d, const Args &a) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t h[4] = {d.hi[j].x, d.hi[j].y, d.hi[j].z, d.hi[j].w}, l[4] = {d.lo[j].x, d.lo[j].y, d.lo[j].z, d.lo[j].w};
+        uint32_t h[4] = {}, l[4] = {};
+        if constexpr (F::kAdd >= 1) *reinterpret_cast<uint4 *>(h) = *reinterpret_cast<const uint4 *>(lines + at_line<F::kUnit>(lane, 4 * b + j));
+        if constexpr (F::kAdd == 2)
+            *reinterpret_cast<uint4 *>(l) = *reinterpret_cast<const uint4 *>(lines + F::kPlane + at_line<F::kUnit>(lane, 4 * b + j));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float2 x = sum2(h[q], l[q]);
-            v[8 * j + 2 * q] = fmaf(a.alpha, v[8 * j + 2 * q], a.beta * x.x);
-            v[8 * j + 2 * q + 1] = fmaf(a.alpha, v[8 * j + 2 * q + 1], a.beta * x.y);
+            float &x = v[8 * j + 2 * q], &y = v[8 * j + 2 * q + 1];
+            x *= a.alpha, y *= a.alpha;
+            if constexpr (F::kAdd == 2) {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&l[q]));
+                x = fmaf(a.beta, t.x, x), y = fmaf(a.beta, t.y, y);
+            }
+            if constexpr (F::kAdd >= 1) {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&h[q]));
+                x = fmaf(a.beta, t.x, x), y = fmaf(a.beta, t.y, y);
+            }
         }
     }
-}
-
-// 32 columns of a warp's 32 rows; `row0`, `col0`: where the block starts.
-template <int KIND, int PLANES>
-__device__ __forceinline__ void block_out(const Args &a, const Work &w, int row0, int col0, float (&v)[32], const CUtensorMap *map,
-                                          unsigned char *stage) {
-    const int lane = threadIdx.x & 31;
     if (KIND == APPLY && a.last) {
-        using T = std::conditional_t<PLANES == 1, __nv_bfloat16, float>;
-        lines_free();
         if constexpr (PLANES == 1) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4 *>(stage + at64(lane, j)) = make_uint4(bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                                                               bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
+                *reinterpret_cast<uint4 *>(lines + at_line<64>(lane, 4 * b + j)) = make_uint4(
+                    bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]), bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
         } else {
+            __syncwarp();                   // lines of f32 lie across what other lanes have read
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<float4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                *reinterpret_cast<float4 *>(lines + at_line<64>(lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
-        if (!a.out) {
-            lines_store(map, stage, col0, row0, w.item, -1);
-            return;
+        return;
+    }
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        hi[i] = *reinterpret_cast<const uint32_t *>(&h);
+        if constexpr (F::kOut == 2) {
+            const float2 back = __half22float2(h);
+            const __half2 l = __floats2half2_rn(v[2 * i] - back.x, v[2 * i + 1] - back.y);
+            lo[i] = *reinterpret_cast<const uint32_t *>(&l);
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        *reinterpret_cast<uint4 *>(lines + at_line<F::kUnit>(lane, 4 * b + j)) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+        if constexpr (F::kOut == 2)
+            *reinterpret_cast<uint4 *>(lines + F::kPlane + at_line<F::kUnit>(lane, 4 * b + j)) =
+                make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+    }
+    if (KIND != APPLY && (row0 & ~(F::kUnit - 1)) > col0 && row0 + lane < a.rows) {
+        // the same block in its place above the diagonal: column i is a line there, on which the lanes lie side by side
+        // (col0 + 31 lies before this unit's rows: such lines are there)
+        uint16_t *p = reinterpret_cast<uint16_t *>(a.result) + (static_cast<int64_t>(item) * a.rows + col0) * a.result_ld + row0 + lane;
+        const int64_t plane = static_cast<int64_t>(a.batch) * a.rows * a.result_ld;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, p += a.result_ld) {
+            *p = static_cast<uint16_t>(hi[i / 2] >> (i % 2 * 16));
+            if constexpr (F::kOut == 2) p[plane] = static_cast<uint16_t>(lo[i / 2] >> (i % 2 * 16));
+        }
+    }
+}
+// A unit's lines leave.
+template <int KIND, int PLANES>
+__device__ __forceinline__ void unit_out(const CUtensorMap *map, const Args &a, int item, int row0, int col0, unsigned char *lines) {
+    using F = Form<KIND, PLANES>;
+    using T = std::conditional_t<PLANES == 1, __nv_bfloat16, float>;
+    const int lane = threadIdx.x & 31;
+    if (KIND == APPLY && a.last && a.out) {             // lines that TMA cannot store
         __syncwarp();
-        T *p = static_cast<T *>(a.out) + w.item * a.stride_o + row0 * a.ldo + col0 + lane;
         const int rows = min(32, a.rows - row0);
-        for (int q = 0; q < rows; ++q, p += a.ldo) {
-            T x;
-            if constexpr (PLANES == 1) x = *reinterpret_cast<const T *>(stage + at64(q, lane >> 3) + (lane & 7) * 2);
-            else x = *reinterpret_cast<const T *>(stage + q * 128 + (((lane >> 2) ^ (q & 7)) << 4) + (lane & 3) * 4);
-            if (col0 + lane < a.cols) *p = x;
+        for (int c = lane; c < F::kUnit; c += 32) {
+            T *p = static_cast<T *>(a.out) + item * a.stride_o + row0 * a.ldo + col0 + c;
+            constexpr int PER = 16 / sizeof(T);
+            for (int q = 0; q < rows; ++q, p += a.ldo) {
+                const T x = *reinterpret_cast<const T *>(lines + at_line<64>(q, c / PER) + c % PER * sizeof(T));
+                if (col0 + c < a.cols) *p = x;
+            }
         }
         __syncwarp();
         return;
     }
-    const int z1 = a.planes_out == 2 ? a.batch + w.item : -1;
-    __half hi[32], lo[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        hi[i] = __float2half_rn(v[i]);
-        lo[i] = __float2half_rn(v[i] - __half2float(hi[i]));
-    }
-    lines_free();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        *reinterpret_cast<uint4 *>(stage + at64(lane, j)) = make_uint4(pack(hi[8 * j], hi[8 * j + 1]), pack(hi[8 * j + 2], hi[8 * j + 3]),
-                                                                       pack(hi[8 * j + 4], hi[8 * j + 5]), pack(hi[8 * j + 6], hi[8 * j + 7]));
-        if (z1 >= 0)
-            *reinterpret_cast<uint4 *>(stage + 2048 + at64(lane, j)) = make_uint4(pack(lo[8 * j], lo[8 * j + 1]), pack(lo[8 * j + 2], lo[8 * j + 3]),
-                                                                                  pack(lo[8 * j + 4], lo[8 * j + 5]), pack(lo[8 * j + 6], lo[8 * j + 7]));
-    }
-    lines_store(map, stage, col0, row0, w.item, z1);
-    if (KIND == SYMMETRIC && row0 > col0 && row0 + lane < a.rows) {
-        // the same block in its place above the diagonal: column i is a line there, on which the lanes lie side by side
-        __half *p = a.result + (static_cast<int64_t>(w.item) * a.rows + col0) * a.result_ld + row0 + lane;
-        const int64_t plane = static_cast<int64_t>(a.batch) * a.rows * a.result_ld;
-#pragma unroll
-        for (int i = 0; i < 32; ++i, p += a.result_ld) {
-            *p = hi[i];                              // col0 + 31 < row0: such lines are there
-            if (z1 >= 0) p[plane] = lo[i];
-        }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tc::tma_store_3d(map, lines, col0, row0, item, false);
+        if (F::kOut == 2 && !(KIND == APPLY && a.last)) tc::tma_store_3d(map, lines + F::kPlane, col0, row0, a.batch + item, false);
+        tc::bulk_commit();
     }
 }
 
@@ -263,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + stages * kStageA;
-    unsigned char *const staging = base + R::kBytes;
+    unsigned char *const all_lines = base + R::kBytes;
     __shared__ uint64_t full[kMostStages], empty[kMostStages], acc_full[2], acc_empty[2], add_full[kEpilogueWarps], drained;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
@@ -356,7 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
       } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        // The whole warp goes through the steps, so that what the products are issued with is known to be the same in
+        // all lanes; one lane issues.
+        if (rank == 0) {
             const uint64_t da0 = A_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_a), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_a));
             const uint64_t db0 = B_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_b), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_b));
             uint32_t s = 0, phase = 0, done = 0;
@@ -366,35 +384,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t idesc = tc::idesc_f16(CTAS * kTileM, cols_of<B_MN, CTAS>(k.tn, a), A_MN, B_MN);
                 for (int c = 0; ok && c < a.kblocks; c += a.chunk, ++done) {
                     const uint32_t acc = tmem + (done & 1) * kTileN;
-                    if (!tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls));
+                    if (!ok) break;
                     tc::fence_after_sync();
                     const int steps = min(c + a.chunk, a.kblocks) - c;
                     for (int i = 0; i < steps; ++i) {
-                        if (!tc::mbar_wait(&full[s], phase, kPolls)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], phase, kPolls));
+                        if (!ok) break;
                         tc::fence_after_sync();
                         const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (stage_b >> 4);
+                        if (tc::elect()) {
 #pragma unroll
-                        for (int q = 0; q < PAIRS; ++q) {
-                            const int pa = PLANES == 2 && q == 1, pb = PLANES == 2 && q == 0;       // hi lo, lo hi, hi hi
+                            for (int q = 0; q < PAIRS; ++q) {
+                                const int pa = PLANES == 2 && q == 1, pb = PLANES == 2 && q == 0;       // hi lo, lo hi, hi hi
 #pragma unroll
-                            for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
-                                tc::mma_f16<CTAS>(acc, da + pa * (kBytesA >> 4) + j * (A_MN ? 2048 / 16 : 2),
-                                                  db + pb * (bytes_b >> 4) + j * (B_MN ? 2048 / 16 : 2), idesc,
-                                                  i > 0 || q > 0 || j > 0);
+                                for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
+                                    tc::mma_f16<CTAS>(acc, da + pa * (kBytesA >> 4) + j * (A_MN ? 2048 / 16 : 2),
+                                                      db + pb * (bytes_b >> 4) + j * (B_MN ? 2048 / 16 : 2), idesc,
+                                                      i > 0 || q > 0 || j > 0);
+                            }
+                            tc::mma_commit_all<CTAS>(&empty[s]);
+                            if (i + 1 == steps) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
                         }
-                        tc::mma_commit_all<CTAS>(&empty[s]);
+                        __syncwarp();
                         if (++s == stages) s = 0, phase ^= 1;
                     }
-                    if (ok) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
                 }
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 gave_up = 1;
                 tc::mma_commit_all<CTAS>(&drained);
                 tc::mbar_wait(&drained, 0, kPolls);
@@ -404,39 +421,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         tc::regs_inc<kRegsMany>();
         const int quad = warp & 3, half = (warp - 4) >> 2;  // a warp may read its quarter of the lanes
-        unsigned char *const stage = staging + (warp - 4) * kStageBytes;
-        unsigned char *const lines = PLANES == 1 ? base + R::kBytesAdd + (warp - 4) * kStageBytes : stage;
+        using F = Form<KIND, PLANES>;
+        constexpr int UNIT = F::kUnit;
+        unsigned char *const lines0 = all_lines + (warp - 4) * R::kLines;
         uint64_t *const bar = &add_full[warp - 4];
-        const bool adds = a.planes_add > 0;
-        uint32_t done = 0, asked = 0;
+        uint32_t done = 0, units = 0;
         bool ok = true;
+        // columns of a tile that this warp has: a half, or all where a half is less than a unit
+        const int mine = max(a.tile_n / 2, UNIT), first = half * mine;
         for (int w = blockIdx.x / CTAS; ok && w < a.total; w += gridDim.x / CTAS) {
             const Work k = work_of<KIND, CTAS>(w, a);
-            const int n0 = k.tn * a.tile_n, row0 = (k.tm * CTAS + rank) * kTileM + quad * 32, first = half * (a.tile_n / 2);
-            int cols = min(a.cols - n0, first + a.tile_n / 2);                     // this warp's end there
-            if (KIND == SYMMETRIC) cols = min(cols, row0 + 32 - n0);                       // or with the diagonal's block
+            const int n0 = k.tn * a.tile_n, row0 = (k.tm * CTAS + rank) * kTileM + quad * 32;
+            int cols = min(a.cols - n0, min(first + mine, a.tile_n));                      // they end there
+            if (KIND != APPLY) cols = min(cols, (row0 & ~(UNIT - 1)) + UNIT - n0);         // or with the diagonal's unit
             if (row0 >= a.rows) cols = 0;
+            const auto lines_of = [&](uint32_t u) { return lines0 + (F::kTurns ? (u & 1) * F::kPlane : 0); };
+            const auto ask = [&](int c0) {             // for the next unit, whose lines are free before
+                if constexpr (F::kTurns) lines_free_but_last();
+                else lines_free();
+                if constexpr (F::kAdd > 0) addend_ask<KIND, PLANES>(&map_add, a, k.item, lines_of(units), bar, row0, n0 + c0);
+            };
+            const auto take = [&] {
+                if constexpr (F::kAdd > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, units & 1, kPolls)) && ok;
+            };
             if constexpr (PLANES == 1) {
-                // blocks go out as they leave tensor memory; the next one's addend is on its way meanwhile
-                if (adds && first < cols) addend_ask(&map_add, a, k, lines, bar, row0, n0 + first);
+                // blocks go out as they leave tensor memory
+                if (first < cols) ask(first);
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls));
                 if (!ok) {
-                    if (adds && first < cols) tc::mbar_wait(bar, asked & 1, kPolls);
+                    if (first < cols) take();
                 } else {
                     tc::fence_after_sync();
                     const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll 1
-                    for (int c0 = first; c0 < cols; c0 += 32) {
-                        Addend now{};
-                        if (adds) {
-                            ok = addend_take(now, a, lines, bar, asked++ & 1) && ok;
-                            if (c0 + 32 < cols) addend_ask(&map_add, a, k, lines, bar, row0, n0 + c0 + 32);
+                    for (int c0 = first; c0 < cols; c0 += UNIT) {
+                        take();
+#pragma unroll 1
+                        for (int b = 0; b < 2 && n0 + c0 + 32 * b < a.cols; ++b) {
+                            float v[32];
+                            __syncwarp();
+                            tc::tmem_ld32(acc + c0 + 32 * b, v);
+                            block_out<KIND, PLANES>(a, k.item, row0, n0 + c0 + 32 * b, b, v, lines_of(units));
                         }
-                        float v[32];
-                        __syncwarp();
-                        tc::tmem_ld32(acc + c0, v);
-                        combine(v, now, a);
-                        block_out<KIND, PLANES>(a, k, row0, n0 + c0, v, &map_out, stage);
+                        unit_out<KIND, PLANES>(&map_out, a, k.item, row0, n0 + c0, lines_of(units));
+                        ++units;
+                        if (c0 + UNIT < cols) ask(c0 + UNIT);
                     }
                     __syncwarp();
                     tc::fence_before_sync();
@@ -479,17 +508,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (ok) {
-                    // one copy of the code for the four blocks, whose sums move up
+                    // one copy of the code for the blocks, whose sums move up
 #pragma unroll 1
-                    for (int c0 = first; c0 < cols; c0 += 32) {
-                        Addend now{};
-                        if (adds) {
-                            lines_free();
-                            addend_ask(&map_add, a, k, lines, bar, row0, n0 + c0);
-                            ok = addend_take(now, a, lines, bar, asked++ & 1) && ok;
-                        }
-                        combine(v[0], now, a);
-                        block_out<KIND, PLANES>(a, k, row0, n0 + c0, v[0], &map_out, stage);
+                    for (int c0 = first; c0 < cols; c0 += UNIT) {
+                        ask(c0);
+                        take();
+                        block_out<KIND, PLANES>(a, k.item, row0, n0 + c0, 0, v[0], lines0);
+                        unit_out<KIND, PLANES>(&map_out, a, k.item, row0, n0 + c0, lines0);
+                        ++units;
 #pragma unroll
                         for (int b = 0; b + 1 < BLOCKS; ++b)
 #pragma unroll

@@ -47,12 +47,15 @@ template <int PLANES>
 cudaError_t launch(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo, const Args &a, int sms,
                    cudaStream_t s) {
     switch (layout) {
-        case GRAM_LINES:      // and SQUARE
-            return ctas == 1 ? launch_tiles<SYMMETRIC, false, false, PLANES, 1>(ma, mb, md, mo, a, sms, s)
-                             : launch_tiles<SYMMETRIC, false, false, PLANES, 2>(ma, mb, md, mo, a, sms, s);
+        case GRAM_LINES:
+            return ctas == 1 ? launch_tiles<GRAM, false, false, PLANES, 1>(ma, mb, md, mo, a, sms, s)
+                             : launch_tiles<GRAM, false, false, PLANES, 2>(ma, mb, md, mo, a, sms, s);
         case GRAM_WIDTH:
-            return ctas == 1 ? launch_tiles<SYMMETRIC, true, true, PLANES, 1>(ma, mb, md, mo, a, sms, s)
-                             : launch_tiles<SYMMETRIC, true, true, PLANES, 2>(ma, mb, md, mo, a, sms, s);
+            return ctas == 1 ? launch_tiles<GRAM, true, true, PLANES, 1>(ma, mb, md, mo, a, sms, s)
+                             : launch_tiles<GRAM, true, true, PLANES, 2>(ma, mb, md, mo, a, sms, s);
+        case SQUARE_A:
+            return ctas == 1 ? launch_tiles<SQUARE, false, false, PLANES, 1>(ma, mb, md, mo, a, sms, s)
+                             : launch_tiles<SQUARE, false, false, PLANES, 2>(ma, mb, md, mo, a, sms, s);
         case APPLY_LEFT:
             return ctas == 1 ? launch_tiles<APPLY, false, true, PLANES, 1>(ma, mb, md, mo, a, sms, s)
                              : launch_tiles<APPLY, false, true, PLANES, 2>(ma, mb, md, mo, a, sms, s);

@@ -58,6 +58,10 @@ __device__ __forceinline__ void put8(unsigned char *base, int plane_bytes, int r
             make_uint4(pack(lo[0], lo[1]), pack(lo[2], lo[3]), pack(lo[4], lo[5]), pack(lo[6], lo[7]));
 }
 
+__device__ __forceinline__ float2 sum2(uint32_t hi, uint32_t lo) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hi)), y = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    return make_float2(x.x + y.x, x.y + y.y);
+}
 template <int PLANES>
 __device__ __forceinline__ void get8(unsigned char *base, int plane_bytes, int row, int c, float *v) {
     const uint4 h = *reinterpret_cast<const uint4 *>(at128(base, row, c));
