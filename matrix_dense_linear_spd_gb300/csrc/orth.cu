@@ -232,6 +232,7 @@ Plan plan_for(int dtype, int64_t lines, int64_t width, int64_t batch, int sms) {
 
 // K is added in tensor memory over so many 64-deep steps at a time: two planes as in the cross entropy's f32
 // products, one plane (whose results are rounded to 11 bits, or added to a X) without end.
+constexpr int64_t kGroupBytes = int64_t(16) << 20;
 constexpr int kChunkTwo = 2, kChunkOne = 1 << 20;
 
 struct Call {
@@ -266,6 +267,9 @@ bl_status run(const Plan &q, const Call &c) {
     src.vec = for_tma(c.G, c.ldg, sizeof(T)) && (q.batch == 1 || c.stride_g * static_cast<int64_t>(sizeof(T)) % 16 == 0);
     const unsigned blocks = static_cast<unsigned>(q.batch * q.chunks);
     const int64_t plane_x = q.batch * q.lines * q.ldx;
+    // tiles of B's side whose operands are kGroupBytes at most
+    const int64_t tile_bytes = (q.wide ? q.apply.ctas * kTileM : q.apply.tile_n) * q.small * 2 * PLANES;
+    const int group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kGroupBytes / tile_bytes, 1 << 16)));
     BL_TRY(launch_pdl(sums_kernel<T>, blocks, 256, 0, c.s, src, gave_up));
     BL_TRY(launch_pdl(begin_kernel<T>, blocks, 256, 0, c.s, src, reinterpret_cast<__half *>(c.ws + q.x[0]), q.ldx, plane_x));
     const float a = static_cast<float>(c.coefficients[0]), b = static_cast<float>(c.coefficients[1]), cc = static_cast<float>(c.coefficients[2]);
@@ -320,6 +324,8 @@ bl_status run(const Plan &q, const Call &c) {
         BL_TRY(product(SQUARE_A, q.square.ctas, sq_a, sq_b, a_out, b_out, square, c.sms, c.s));
         Args apply = args(q.apply, q.lines, q.width, q.small);
         apply.alpha = 1 / kScaleA, apply.beta = a;
+        apply.rows_first = q.wide;
+        apply.group = group;
         apply.last = step + 1 == c.steps;
         if (apply.last) {
             apply.alpha /= kScaleX, apply.beta /= kScaleX;

@@ -67,6 +67,9 @@ __device__ __forceinline__ float2 scale_of(double sum) {
 // A stage is as small as the tile's columns allow: narrow tiles, of small matrices, wait for memory, and the more
 // of their stages are on their way the better.
 constexpr int kMostStages = 8;
+// Accumulators: tensor memory's 512 columns hold as many as the tile's width allows. Two would do for wide tiles; the
+// chunks of narrow ones, of two planes, take less time than an epilogue takes to answer (517 x 1031 f32 BUFS_NOTE).
+constexpr int kMostAccs = 8;
 template <int PLANES, int CTAS>
 struct Ring {
     static constexpr int kTile = CTAS == 1 ? 128 : 256;             // columns of a tile, at most
@@ -91,6 +94,8 @@ struct Args {
     bool last;                 // APPLY: the result is the caller's, f32 or bf16
     void *out;                 // where its lines do not start on 16-byte boundaries: stored without TMA
     int64_t ldo, stride_o;
+    bool rows_first;           // APPLY: the order of tiles
+    int group;
     int32_t *gave_up;
 };
 
@@ -113,8 +118,15 @@ __device__ __forceinline__ Work work_of(int w, const Args &a) {
         }
         r.tn = w;
     } else {
-        r.tm = w / a.tiles_n;
-        r.tn = w - r.tm * a.tiles_n;
+        // B's side of the tiles varies first, `group` of them at a time, so that this much of B stays in L2 while X
+        // goes by: with all of its 32 MB at a time one product of 8192 x 4096 reads 540 MB of memory, and the five steps take
+        // GROUP_NOTE.
+        const int inner = a.rows_first ? a.tiles_m : a.tiles_n, outer = a.rows_first ? a.tiles_n : a.tiles_m;
+        const int g = w / (a.group * outer), size = min(a.group, inner - g * a.group);
+        w -= g * a.group * outer;
+        const int o = w / size, i = g * a.group + w - o * size;
+        r.tm = a.rows_first ? i : o;
+        r.tn = a.rows_first ? o : i;
     }
     return r;
 }
@@ -275,12 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     using R = Ring<PLANES, CTAS>;
     constexpr int kBytesA = R::kBytesA, kStageA = R::kStageA;
     constexpr int PAIRS = PLANES == 1 ? 1 : 3, BLOCKS = R::kTile / 64;
+    const uint32_t accs = 512 / a.tile_n, acc_bits = 31 - __clz(accs);       // a power of two
     const uint32_t stages = a.stages, bytes_b = a.tile_n / CTAS * 128, stage_b = PLANES * bytes_b;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *const base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char *const tiles_a = base, *const tiles_b = base + stages * kStageA;
     unsigned char *const all_lines = base + R::kBytes;
-    __shared__ uint64_t full[kMostStages], empty[kMostStages], acc_full[2], acc_empty[2], add_full[kEpilogueWarps], drained;
+    __shared__ uint64_t full[kMostStages], empty[kMostStages], acc_full[kMostAccs], acc_empty[kMostAccs], add_full[kEpilogueWarps], drained;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -292,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kMostAccs; ++s) {
             tc::mbar_init(&acc_full[s], 1);
             tc::mbar_init(&acc_empty[s], CTAS * kEpilogueWarps);
         }
@@ -373,24 +386,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (warp == 1) {
         // The whole warp goes through the steps, so that what the products are issued with is known to be the same in
-        // all lanes; one lane issues.
+        // all lanes; one lane issues. A lane looks at one stage's barrier, so that all that is there is found at once:
+        // a barrier takes 150 cycles to look at, the four products of a stage 160 to issue.
         if (rank == 0) {
             const uint64_t da0 = A_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_a), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_a));
             const uint64_t db0 = B_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_b), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_b));
-            uint32_t s = 0, phase = 0, done = 0;
+            uint32_t s = 0, phase = 0, done = 0, there = 0;
             bool ok = true;
+            const auto look = [&] {                    // how many stages from s on are there
+                const uint32_t t = s + lane, wrapped = t >= stages;
+                for (uint32_t i = 0; there == 0 && i < kPolls; ++i) {
+                    const bool full_now = lane < static_cast<int>(stages) && tc::mbar_wait(&full[wrapped ? t - stages : t], phase ^ wrapped, 1);
+                    there = __ffs(~__ballot_sync(0xffffffffu, full_now)) - 1;
+                }
+                __syncwarp();
+                return there > 0;
+            };
             for (int w = blockIdx.x / CTAS; ok && w < a.total; w += gridDim.x / CTAS) {
                 const Work k = work_of<KIND, CTAS>(w, a);
                 const uint32_t idesc = tc::idesc_f16(CTAS * kTileM, cols_of<B_MN, CTAS>(k.tn, a), A_MN, B_MN);
                 for (int c = 0; ok && c < a.kblocks; c += a.chunk, ++done) {
-                    const uint32_t acc = tmem + (done & 1) * kTileN;
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls));
+                    const uint32_t at = done & (accs - 1), acc = tmem + at * a.tile_n;
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_empty[at], (done >> acc_bits & 1) ^ 1, kPolls));
                     if (!ok) break;
-                    tc::fence_after_sync();
                     const int steps = min(c + a.chunk, a.kblocks) - c;
                     for (int i = 0; i < steps; ++i) {
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], phase, kPolls));
+                        if (there == 0) ok = look();
                         if (!ok) break;
+                        --there;
                         tc::fence_after_sync();
                         const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (stage_b >> 4);
                         if (tc::elect()) {
@@ -404,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                       i > 0 || q > 0 || j > 0);
                             }
                             tc::mma_commit_all<CTAS>(&empty[s]);
-                            if (i + 1 == steps) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
+                            if (i + 1 == steps) tc::mma_commit_all<CTAS>(&acc_full[at]);
                         }
                         __syncwarp();
                         if (++s == stages) s = 0, phase ^= 1;
@@ -447,12 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (PLANES == 1) {
                 // blocks go out as they leave tensor memory
                 if (first < cols) ask(first);
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls));
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & (accs - 1)], done >> acc_bits & 1, kPolls));
                 if (!ok) {
                     if (first < cols) take();
                 } else {
                     tc::fence_after_sync();
-                    const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
+                    const uint32_t acc = tmem + (done & (accs - 1)) * a.tile_n + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll 1
                     for (int c0 = first; c0 < cols; c0 += UNIT) {
                         take();
@@ -471,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[done & 1]);
-                        else tc::mbar_arrive_at(tc::at_leader(&acc_empty[done & 1]));
+                        if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[done & (accs - 1)]);
+                        else tc::mbar_arrive_at(tc::at_leader(&acc_empty[done & (accs - 1)]));
                     }
                     ++done;
                 }
@@ -484,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i) v[b][i] = 0.f;
 #pragma unroll 1
                 for (int c = 0; c < a.kblocks; c += a.chunk, ++done) {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & 1], done >> 1 & 1, kPolls));
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & (accs - 1)], done >> acc_bits & 1, kPolls));
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint32_t acc = tmem + (done & 1) * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
+                    const uint32_t acc = tmem + (done & (accs - 1)) * a.tile_n + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll
                     for (int b = 0; b < BLOCKS; ++b) {
                         const int c0 = first + 32 * b;
@@ -503,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[done & 1]);
-                        else tc::mbar_arrive_at(tc::at_leader(&acc_empty[done & 1]));
+                        if constexpr (CTAS == 1) tc::mbar_arrive(&acc_empty[done & (accs - 1)]);
+                        else tc::mbar_arrive_at(tc::at_leader(&acc_empty[done & (accs - 1)]));
                     }
                 }
                 if (ok) {
@@ -526,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok && lane == 0) gave_up = 1;
         }
-        if (lane == 0) tc::bulk_wait_all();
+        if (lane == 0) tc::bulk_wait_read_all();         // the grid's end, which the next kernel waits for, is the stores' too
     }
     __syncwarp();
     tc::fence_before_sync();
