@@ -87,17 +87,22 @@ __device__ __forceinline__ void row_sync() {
 // are fewer. floor: what `top` keys are known to reach, or 0.
 template <int WARPS, typename F>
 __device__ __forceinline__ void select(Gather &g, int64_t n, uint64_t given, int top, uint64_t floor, const F &key) {
-    constexpr int HELD = 8;
-    constexpr int STEP = WARPS * 32;
+    constexpr int HELD = 16, STEP = WARPS * 32;
     const int lane = threadIdx.x & 31, thread = threadIdx.x % STEP;
+    // Keys are looked at twice; where a thread can hold its own they are read once.
+    uint64_t k[HELD];
+    const auto read = [&](int64_t i0) {
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) k[h] = i0 + h * STEP < n ? key(i0 + h * STEP) : 0;
+    };
+    bool held = false;
     const auto each = [&](const auto &f) {
         for (int64_t i0 = thread; i0 - thread < n; i0 += STEP * HELD) {
-            uint64_t k[HELD];
-#pragma unroll
-            for (int h = 0; h < HELD; ++h) k[h] = i0 + h * STEP < n ? key(i0 + h * STEP) : 0;
+            if (!held) read(i0);
 #pragma unroll
             for (int h = 0; h < HELD; ++h) f(k[h]);
         }
+        held = n <= STEP * HELD;
     };
     if (thread < 32) {
         g.chosen[lane] = 0;
@@ -202,7 +207,8 @@ struct Scores {
     int64_t *top_id;
 };
 
-// WARPS warps share a row: 8 where rows are few, else 1.
+// WARPS warps share a row: 8 where rows are few or long, else 1. (4096 rows of 3126 blocks: 1127 us in
+// all, and 1135; of 1000 blocks 283, and 248.)
 template <int WARPS>
 __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Scores a) {
     constexpr int ROWS = 8 / WARPS, HELD = 8;
@@ -235,26 +241,36 @@ __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Sco
         likeliest = g.chosen[lane];
         if (!a.last && share == 0 && lane < top) a.best[j * top + lane] = likeliest;
     }
-    if (!a.last || row >= a.rows || share != 0) return;
+    if (!a.last) return;
+    // what is left of the row, by all of its warps
+    __shared__ float tops[8], sums[8], sums_t[8];
     float logp = 0.f, entropy = 0.f, lse = 0.f, ref = 0.f, log_sum = 0.f;
     bool sound = false;
     if (counts) {
+        constexpr int STEP = WARPS * 32;
+        const int thread = threadIdx.x % STEP;
         const float2 *const p = a.part + j * a.part_ld;
         const float *const pt = a.part_t + j * a.part_ld;
         float2 v[HELD];
         float t[HELD];
 #pragma unroll
         for (int h = 0; h < HELD; ++h) {
-            const bool in = lane + 32 * h < a.part_ld;
-            v[h] = in ? p[lane + 32 * h] : make_float2(-INFINITY, 0.f);
-            t[h] = in ? pt[lane + 32 * h] : 0.f;
+            const bool in = thread + STEP * h < a.part_ld;
+            v[h] = in ? p[thread + STEP * h] : make_float2(-INFINITY, 0.f);
+            t[h] = in ? pt[thread + STEP * h] : 0.f;
         }
         const float picked = a.picked[j];
         float most = -INFINITY, sum = 0.f, sum_t = 0.f;
 #pragma unroll
         for (int h = 0; h < HELD; ++h) most = fmaxf(most, v[h].x);
-        for (int64_t i = lane + 32 * HELD; i < a.part_ld; i += 32) most = fmaxf(most, p[i].x);
+#pragma unroll 8
+        for (int64_t i = thread + STEP * HELD; i < a.part_ld; i += STEP) most = fmaxf(most, p[i].x);
         most = warp_max(most);
+        if constexpr (WARPS > 1) {
+            if (lane == 0) tops[warp] = most;
+            __syncthreads();
+            for (int w = 0; w < WARPS; ++w) most = fmaxf(most, tops[w]);
+        }
         ref = most == -INFINITY ? 0.f : most;
         const auto add = [&](float2 x, float xt) {
             const float d = fmaxf(x.x - ref, -1e30f);
@@ -263,11 +279,18 @@ __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Sco
         };
 #pragma unroll
         for (int h = 0; h < HELD; ++h) add(v[h], t[h]);
-        for (int64_t i = lane + 32 * HELD; i < a.part_ld; i += 32) add(p[i], pt[i]);
+#pragma unroll 8
+        for (int64_t i = thread + STEP * HELD; i < a.part_ld; i += STEP) add(p[i], pt[i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
             sum_t += __shfl_xor_sync(0xffffffffu, sum_t, o);
+        }
+        if constexpr (WARPS > 1) {
+            if (lane == 0) sums[warp] = sum, sums_t[warp] = sum_t;
+            __syncthreads();
+            sum = sum_t = 0.f;
+            for (int w = 0; w < WARPS; ++w) sum += sums[w], sum_t += sums_t[w];
         }
         log_sum = logf(sum);
         sound = sum > 0.f && !bad;
@@ -276,6 +299,7 @@ __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Sco
         logp = sound ? (picked - ref) - log_sum : NAN;
         entropy = sound ? log_sum - sum_t / sum : NAN;
     }
+    if (row >= a.rows || share != 0) return;
     if (lane == 0) {
         a.logp[row] = logp;
         a.entropy[row] = entropy;

@@ -441,6 +441,8 @@ constexpr int kChunkF32 = 2, kChunkLoss = 16, kChunkFew = 1, kChunkBf16 = 256;
 // 131072 in bf16 and 1024 x 1024 x 32000 in f32 at 64, 128, 512 and 2048 MB: 11.04, 10.84, 10.66, 10.65 ms
 // and 1.22, 1.13, 1.04, 1.04 ms
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
+// Blocks or parts of a row from which on eight warps join them, whatever the number of rows.
+constexpr int64_t kLongRow = 2048;
 // Bytes of the logits that a piece's blocks may keep for the alternatives (few of them are written).
 constexpr int64_t kLogitBytes = int64_t(2) << 30;
 
@@ -759,8 +761,9 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         }
     }
     const auto join_scores = [&] {
-        const bool few_rows = c.rows <= 4 * c.sms;         // eight warps a row while all their CTAs run at once
-        return few_rows ? launch_pdl(scores_kernel<8>, static_cast<unsigned>(rows), 256, 0, c.s, scores)
+        // eight warps a row while all their CTAs run at once, and where a row's blocks or parts keep them busy
+        const bool eight = c.rows <= 4 * c.sms || q.block_ld >= kLongRow || q.part_ld >= kLongRow;
+        return eight ? launch_pdl(scores_kernel<8>, static_cast<unsigned>(rows), 256, 0, c.s, scores)
                         : launch_pdl(scores_kernel<1>, static_cast<unsigned>(cdiv(rows, 8)), 256, 0, c.s, scores);
     };
     if (q.few) {
