@@ -44,20 +44,26 @@ __device__ __forceinline__ unsigned char *at128(unsigned char *base, int row, in
     return base + (c >> 6) * (kRows * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4);
 }
 
-template <int PLANES>
+// CUT: what f16 does not hold is cut to what it does.
+template <int PLANES, bool CUT = false>
 __device__ __forceinline__ void put8(unsigned char *base, int plane_bytes, int row, int c, const float *v) {
-    __half hi[8], lo[8];
+    const __half2 limit = __float2half2_rn(65504.f);
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        hi[i] = __float2half_rn(v[i]);
-        if (PLANES == 2) lo[i] = __float2half_rn(v[i] - __half2float(hi[i]));
+    for (int i = 0; i < 4; ++i) {
+        __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        if (CUT) h = __hmax2(__hmin2(h, limit), __hneg2(limit));
+        hi[i] = *reinterpret_cast<const uint32_t *>(&h);
+        if (PLANES == 2) {
+            const float2 back = __half22float2(h);
+            __half2 l = __floats2half2_rn(v[2 * i] - back.x, v[2 * i + 1] - back.y);
+            if (CUT) l = __hmax2(__hmin2(l, limit), __hneg2(limit));
+            lo[i] = *reinterpret_cast<const uint32_t *>(&l);
+        }
     }
-    *reinterpret_cast<uint4 *>(at128(base, row, c)) = make_uint4(pack(hi[0], hi[1]), pack(hi[2], hi[3]), pack(hi[4], hi[5]), pack(hi[6], hi[7]));
-    if (PLANES == 2)
-        *reinterpret_cast<uint4 *>(at128(base + plane_bytes, row, c)) =
-            make_uint4(pack(lo[0], lo[1]), pack(lo[2], lo[3]), pack(lo[4], lo[5]), pack(lo[6], lo[7]));
+    *reinterpret_cast<uint4 *>(at128(base, row, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (PLANES == 2) *reinterpret_cast<uint4 *>(at128(base + plane_bytes, row, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
-
 __device__ __forceinline__ float2 sum2(uint32_t hi, uint32_t lo) {
     const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hi)), y = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
     return make_float2(x.x + y.x, x.y + y.y);
@@ -102,7 +108,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     unsigned char *const ps = xs + PLANES * kPlaneX;
     __shared__ uint64_t bar;
     __shared__ uint32_t tmem_slot;
-    __shared__ double sums[4 * kSides][2];
+    __shared__ double sums[4 * kSides][2];       // f32 values, or f64
     __shared__ float2 factors[8];
     __shared__ int lost[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane, side = warp >> 2;
@@ -115,6 +121,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         tc::mbar_fence_init();
     }
     if (threadIdx.x < 8) lost[threadIdx.x] = 0;
+    __syncthreads();
     pdl_release();
     pdl_wait();
 
@@ -144,33 +151,49 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < NC; ++i, p += step) x[i] = i < held ? static_cast<float>(*p) : 0.f;
     }
-    // the norm: up to 32 squares in f32, the rest in f64, of which an SM has little: a lane's sums, a warp's, the block's
+    // The norm: in f32, pairs of lanes and warps, and once more in f64, which an SM has little of, for a matrix whose
+    // squares leave f32's comfortable range.
     constexpr int GROUP = NC < 32 ? NC : 32;
-    double sum = 0.0;
+    float sum = 0.f, most = 0.f;
 #pragma unroll
     for (int i = 0; i < NC; i += GROUP) {
-        float s = 0.f;
+        float s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < GROUP; ++e) s = fmaf(x[i + e], x[i + e], s);
-        if (s >= 1e-25f && s <= 1e30f) {
-            sum += s;
-        } else if (held > i) {
-#pragma unroll 1
-            for (int e = 0; e < GROUP; ++e) {
-                const double y = e < held - i ? static_cast<double>(static_cast<float>(g[(i + e) * (q.turned ? q.ldg : 1)])) : 0.0;
-                sum = fma(y, y, sum);
-            }
-        }
+        for (int e = 0; e < GROUP; ++e) s[e & 1] = fmaf(x[i + e], x[i + e], s[e & 1]), most = fmaxf(most, fabsf(x[i + e]));
+        sum += s[0] + s[1];
     }
-    for (int o = 1; o < min(32, q.rows_each); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (slot < q.share && !(sum <= 1e30f && (sum >= 1e-25f || most == 0.f))) lost[slot] = 1;
+    const int together = min(32, q.rows_each);
+    for (int o = 1; o < together; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if ((lane & 15) == 0) sums[warp][lane >> 4] = sum;
     __syncthreads();
+    const bool wide = slot < q.share && lost[slot];
+    if (__syncthreads_or(wide)) {
+        double all = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < held && wide; ++i) {
+            const double y = static_cast<double>(static_cast<float>(g[i * (q.turned ? q.ldg : 1)]));
+            all = fma(y, y, all);
+        }
+        for (int o = 1; o < together; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        if (wide && (lane & 15) == 0) sums[warp][lane >> 4] = all;
+        __syncthreads();
+    }
     if (threadIdx.x < q.share) {
         // its 32-row groups (or half of one), all quarters of each row
-        sum = 0.0;
         const int first = threadIdx.x * q.rows_each / 32, count = max(1, q.rows_each / 32), which = q.rows_each == 16 ? threadIdx.x & 1 : 0;
-        for (int w = first; w < first + count; ++w) sum += (sums[w][which] + sums[w + 4][which]) + (sums[w + 8][which] + sums[w + 12][which]);
-        factors[threadIdx.x] = scale_of(sum);
+        if (lost[threadIdx.x]) {
+            double all = 0.0;
+            for (int w = first; w < first + count; ++w) all += (sums[w][which] + sums[w + 4][which]) + (sums[w + 8][which] + sums[w + 12][which]);
+            factors[threadIdx.x] = scale_of(all);
+        } else {
+            float all = 0.f;
+            for (int w = first; w < first + count; ++w)
+                all += (static_cast<float>(sums[w][which]) + static_cast<float>(sums[w + 4][which])) +
+                       (static_cast<float>(sums[w + 8][which]) + static_cast<float>(sums[w + 12][which]));
+            factors[threadIdx.x] = all > 0.f ? make_float2(1.f, kScaleX / sqrtf(all)) : make_float2(0.f, 0.f);
+        }
+        lost[threadIdx.x] = 0;
     }
     __syncthreads();
     const float2 factor = slot < q.share ? factors[slot] : make_float2(0.f, 0.f);
@@ -181,17 +204,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     const auto x_out = [&] {
 #pragma unroll
         for (int i = 0; i < NC; i += 8) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fminf(fmaxf(x[i + e], -65504.f), 65504.f);
-            put8<PLANES>(xs, kPlaneX, row, c0 + i, v);
+            put8<PLANES, true>(xs, kPlaneX, row, c0 + i, x + i);
         }
     };
     x_out();
     const int rows = q.share == 1 ? (q.m + 15) & ~15 : kRows;            // of A and B
     const int cols = (q.n + 31) & ~31;                                   // X is zero from n on
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint32_t parity = 0;
+    uint32_t parity = 0, largest = 0;
     bool ok = true;
     uint32_t tmem = 0;
     // One thread issues a product, all wait for it: A = X X^T (of_x), A A, or B X (apply)
@@ -202,23 +222,30 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         tc::fence_after_sync();
         tmem = tmem_slot;
         if (!ok) return;
-        if (threadIdx.x == 0) {
+        if (warp == 0) {
+            // by the warp as a whole, one lane issuing: 40 cycles a product, 115 in a branch of one thread's
             const uint32_t idesc = tc::idesc_f16(kRows, n, false, apply);
-            const uint32_t a_at = tc::smem_u32(of_x ? xs : ps), b_at = tc::smem_u32(apply || of_x ? xs : ps);
-            const int plane_a = of_x ? kPlaneX : kPlaneP, plane_b = apply || of_x ? kPlaneX : kPlaneP;
+            const uint64_t da0 = tc::sdesc_sw128(tc::smem_u32(of_x ? xs : ps));
+            const uint64_t db0 = apply ? tc::sdesc_mn_sw128(tc::smem_u32(xs), kRows * 128) : da0;
+            const int plane_a = (of_x ? kPlaneX : kPlaneP) >> 4, plane_b = (apply || of_x ? kPlaneX : kPlaneP) >> 4;
+            const int panel_b = apply ? 4 * 2048 / 16 : kRows * 128 / 16, step_b = apply ? 2048 / 16 : 2;
+            if (tc::elect()) {
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) {
+                    uint64_t da = da0 + (PLANES == 2 && p == 1 ? plane_a : 0), db = db0 + (PLANES == 2 && p == 0 ? plane_b : 0);
 #pragma unroll 1
-            for (int p = 0; p < PAIRS; ++p) {
-                const int pa = PLANES == 2 && p == 1, pb = PLANES == 2 && p == 0;
-#pragma unroll 1
-                for (int j = 0; j < k / 16; ++j) {
-                    // 16 k: 32 bytes along a line, lines of 64 k in panels; or 16 lines
-                    const uint64_t da = tc::sdesc_sw128(a_at + pa * plane_a + (j >> 2) * (kRows * 128)) + (j & 3) * 2;
-                    const uint64_t db = apply ? tc::sdesc_mn_sw128(b_at + pb * plane_b, kRows * 128) + j * (2048 / 16)
-                                              : tc::sdesc_sw128(b_at + pb * plane_b + (j >> 2) * (kRows * 128)) + (j & 3) * 2;
-                    tc::mma_f16<1>(tmem, da, db, idesc, p > 0 || j > 0);
+                    for (int j0 = 0; j0 < k; j0 += 64) {
+                        // 16 k: 32 bytes along a line, lines of 64 k in panels; or 16 lines
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j0 + 16 * j < k) tc::mma_f16<1>(tmem, da + j * 2, db + j * step_b, idesc, p > 0 || j0 > 0 || j > 0);
+                        da += kRows * 128 / 16;
+                        db += panel_b;
+                    }
                 }
+                tc::mma_commit(&bar);
             }
-            tc::mma_commit(&bar);
+            __syncwarp();
         }
         ok = tc::mbar_wait(&bar, parity, kPolls);
         parity ^= 1;
@@ -269,14 +296,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < READ; ++i) {
                 x[h + i] = fmaf(q.a, x[h + i], t[i] * (1.f / 4096.f));
-                bad |= !(fabsf(x[h + i]) <= 65504.f);
+                largest = max(largest, __float_as_uint(x[h + i]) & 0x7fffffffu);        // NaN is larger than infinity
             }
         }
         if (step + 1 < q.steps) x_out();
     }
     // what a matrix or a product lost is seen in all of it
     if (!ok) tc::mbar_wait(&bar, parity ^ 1, kPolls);            // what gave up may still come to its end
-    bad |= !ok || q.spoil;
+    bad |= !ok || q.spoil || largest > __float_as_uint(65504.f);
     if (bad && slot < 8) lost[slot] = 1;
     __syncthreads();
     bad = slot < 8 && lost[slot];
