@@ -99,7 +99,7 @@ struct Held {
 
 // NC: columns that a thread holds (the longer side is 4 NC at most).
 template <typename T, int NC>
-__global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_constant__ Small q) {
+__global__ void __launch_bounds__(kSmallThreads, NC == 16 && sizeof(T) == 2 ? 2 : 1) small_kernel(const __grid_constant__ Small q) {
     constexpr int PLANES = sizeof(T) == 4 ? 2 : 1, PAIRS = PLANES == 1 ? 1 : 3;
     constexpr int N = kSides * NC, kPlaneX = N / 64 * kRows * 128, kPlaneP = 2 * kRows * 128;
     constexpr uint32_t kColumns = N > kRows ? N : kRows;
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     unsigned char *const ps = xs + PLANES * kPlaneX;
     __shared__ uint64_t bar;
     __shared__ uint32_t tmem_slot;
-    __shared__ double sums[4 * kSides][2];       // f32 values, or f64
-    __shared__ float2 factors[8];
+    __shared__ __align__(16) float sums[8][kSides];
+    __shared__ double wide_sums[8][kSides];
     __shared__ int lost[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane, side = warp >> 2;
     if (warp == 0) {
@@ -165,9 +165,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     if (slot < q.share && !(sum <= 1e30f && (sum >= 1e-25f || most == 0.f))) lost[slot] = 1;
     const int together = min(32, q.rows_each);
     for (int o = 1; o < together; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((lane & 15) == 0) sums[warp][lane >> 4] = sum;
+    // by 32-row groups (or 16-row ones), the four quarters of a row together
+    if ((lane & 15) == 0) sums[(warp & 3) * 2 + (lane >> 4)][side] = sum;
     __syncthreads();
     const bool wide = slot < q.share && lost[slot];
+    // this matrix's entries: one of 16 rows, or every other one, of 32
+    const int step_w = together == 16 ? 1 : 2, from = slot * q.rows_each / 16, until = min(8, from + max(1, q.rows_each / 16));
+    float2 factor = make_float2(0.f, 0.f);
     if (__syncthreads_or(wide)) {
         double all = 0.0;
 #pragma unroll 1
@@ -176,27 +180,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             all = fma(y, y, all);
         }
         for (int o = 1; o < together; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        if (wide && (lane & 15) == 0) sums[warp][lane >> 4] = all;
+        if ((lane & 15) == 0) wide_sums[(warp & 3) * 2 + (lane >> 4)][side] = all;
+        __syncthreads();
+        all = 0.0;
+        for (int w = from; w < until; w += step_w) all += (wide_sums[w][0] + wide_sums[w][1]) + (wide_sums[w][2] + wide_sums[w][3]);
+        factor = scale_of(all);
+        if (threadIdx.x < 8) lost[threadIdx.x] = 0;
         __syncthreads();
     }
-    if (threadIdx.x < q.share) {
-        // its 32-row groups (or half of one), all quarters of each row
-        const int first = threadIdx.x * q.rows_each / 32, count = max(1, q.rows_each / 32), which = q.rows_each == 16 ? threadIdx.x & 1 : 0;
-        if (lost[threadIdx.x]) {
-            double all = 0.0;
-            for (int w = first; w < first + count; ++w) all += (sums[w][which] + sums[w + 4][which]) + (sums[w + 8][which] + sums[w + 12][which]);
-            factors[threadIdx.x] = scale_of(all);
-        } else {
-            float all = 0.f;
-            for (int w = first; w < first + count; ++w)
-                all += (static_cast<float>(sums[w][which]) + static_cast<float>(sums[w + 4][which])) +
-                       (static_cast<float>(sums[w + 8][which]) + static_cast<float>(sums[w + 12][which]));
-            factors[threadIdx.x] = all > 0.f ? make_float2(1.f, kScaleX / sqrtf(all)) : make_float2(0.f, 0.f);
+    if (!wide) {
+        sum = 0.f;
+        for (int w = from; w < until; w += step_w) {
+            const float4 t = *reinterpret_cast<const float4 *>(sums[w]);
+            sum += (t.x + t.y) + (t.z + t.w);
         }
-        lost[threadIdx.x] = 0;
+        factor = sum > 0.f ? make_float2(1.f, kScaleX / sqrtf(sum)) : make_float2(0.f, 0.f);
     }
-    __syncthreads();
-    const float2 factor = slot < q.share ? factors[slot] : make_float2(0.f, 0.f);
     bool bad = factor.y != factor.y;
 #pragma unroll
     for (int i = 0; i < NC; ++i) x[i] = bad ? 0.f : x[i] * factor.x * factor.y;
@@ -211,20 +210,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     const int rows = q.share == 1 ? (q.m + 15) & ~15 : kRows;            // of A and B
     const int cols = (q.n + 31) & ~31;                                   // X is zero from n on
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint32_t parity = 0, largest = 0;
+    uint32_t largest = 0;
     bool ok = true;
-    uint32_t tmem = 0;
     // One thread issues a product, all wait for it: A = X X^T (of_x), A A, or B X (apply)
-    const auto product = [&](bool of_x, bool apply, int k, int n) {
+    const auto product = [&](int parity, bool of_x, bool apply, int k, int n) {
         tc::fence_before_sync();
         tc::fence_proxy_async_smem();
         ok = !__syncthreads_or(!ok);
         tc::fence_after_sync();
-        tmem = tmem_slot;
         if (!ok) return;
         if (warp == 0) {
             // by the warp as a whole, one lane issuing: 40 cycles a product, 115 in a branch of one thread's
-            const uint32_t idesc = tc::idesc_f16(kRows, n, false, apply);
+            const uint32_t tmem = tmem_slot, idesc = tc::idesc_f16(kRows, n, false, apply);
             const uint64_t da0 = tc::sdesc_sw128(tc::smem_u32(of_x ? xs : ps));
             const uint64_t db0 = apply ? tc::sdesc_mn_sw128(tc::smem_u32(xs), kRows * 128) : da0;
             const int plane_a = (of_x ? kPlaneX : kPlaneP) >> 4, plane_b = (apply || of_x ? kPlaneX : kPlaneP) >> 4;
@@ -248,7 +245,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             __syncwarp();
         }
         ok = tc::mbar_wait(&bar, parity, kPolls);
-        parity ^= 1;
         tc::fence_after_sync();
     };
     constexpr int READ = NC == 32 ? 32 : 16;     // 64 values of X leave no room for more
@@ -256,14 +252,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     const int p0 = side * PC, shift = 31 - __clz(q.rows_each), own = row >> shift;     // its matrix
     const auto read = [&](int c, float (&t)[READ]) {
         __syncwarp();
-        if constexpr (READ == 32) tc::tmem_ld32(tmem + lanes + c, t);
-        else tc::tmem_ld16(tmem + lanes + c, t);
+        if constexpr (READ == 32) tc::tmem_ld32(tmem_slot + lanes + c, t);
+        else tc::tmem_ld16(tmem_slot + lanes + c, t);
     };
     const bool mine[2] = {p0 >> shift == own, (p0 + 16) >> shift == own};
 #pragma unroll 1
     for (int step = 0; step < q.steps; ++step) {
         // A, times 2^12
-        product(true, false, cols, rows);
+        product(step & 1, true, false, cols, rows);
         float t[READ];
 #pragma unroll
         for (int h = 0; h < PC; h += READ) {
@@ -274,7 +270,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             for (int i = 0; i < READ; i += 8) put8<PLANES>(ps, kPlaneP, row, p0 + h + i, t + i);
         }
         // B = b A + c A A, times 2^12, in A's place
-        product(false, false, rows, rows);
+        product(~step & 1, false, false, rows, rows);
 #pragma unroll
         for (int h = 0; h < PC; h += READ) {
             read(p0 + h, t);
@@ -288,7 +284,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             }
         }
         // X
-        product(false, true, rows, cols);
+        product(step & 1, false, true, rows, cols);
 #pragma unroll
         for (int h = 0; h < NC; h += READ) {
             if (c0 + h >= cols) break;
@@ -302,7 +298,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         if (step + 1 < q.steps) x_out();
     }
     // what a matrix or a product lost is seen in all of it
-    if (!ok) tc::mbar_wait(&bar, parity ^ 1, kPolls);            // what gave up may still come to its end
+    if (!ok) tc::mbar_wait(&bar, 0, kPolls), tc::mbar_wait(&bar, 1, kPolls);         // what gave up may still come to its end
     bad |= !ok || q.spoil || largest > __float_as_uint(65504.f);
     if (bad && slot < 8) lost[slot] = 1;
     __syncthreads();
