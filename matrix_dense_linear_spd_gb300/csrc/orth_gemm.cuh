@@ -15,10 +15,15 @@
 // time from the lanes side by side, block by block transposed.
 //
 // A CTA computes 128 x tile_n tiles, or a pair of CTAs 256 x tile_n tiles (each holds its 128 rows and half of B).
-// Roles, waits and registers as in xent_gemm.cuh: a producer thread for each operand, one issuing thread, eight
-// epilogue warps that work on one accumulator of tensor memory while the next tile is added up in the other. With
+// Roles, waits and registers as in xent_gemm.cuh: a producer thread for each operand, an issuing warp, eight
+// epilogue warps that work on one accumulator of tensor memory while the next tile is added up in another. With
 // PLANES = 2 the chain of K is cut into chunks that are added in registers: tensor memory's f32 sums cut where f32
 // would round, up to 2^-23.4 of the sum a step for the diagonal of A.
+//
+// What bounds it: for large matrices the operands' way into shared memory, 64 bytes a cycle and SM at full rate, and the
+// power cap (8192 x 4096 bf16: tensor pipe 86% busy in A, 66 to 70% in B X, whose addend and result take their share of L2;
+// 1,320 TFLOP/s over the call); for small ones latency, some 5 us a product: 1.4 from the end of one kernel to the start
+// of the next, 1.3 to the first operands, 2.5 from the last product to the end.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -42,7 +47,7 @@ constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
 static_assert(128 * kRegsFew + 32 * kEpilogueWarps * kRegsMany <= kThreads * kRegsLaunch, "more registers than the block has");
 constexpr uint32_t kPolls = 1u << 22;
 
-// X is kept times 2^13, A and B times 2^12: elements of X are at most 1.3 for coefficients as above, of A 1.7, and
+// X is kept times 2^13, A and B times 2^12: for (3.4445, -4.7750, 2.0315) elements of X are at most 1.3, of A 1.7, of B 3, and
 // f16 reaches 65504; typical ones, 1 / sqrt(long side), stay in f16's normal range for 22 bits up to sides of 2^16.
 constexpr float kScaleX = 8192.f, kScaleA = 4096.f;
 
@@ -63,12 +68,14 @@ __device__ __forceinline__ float2 scale_of(double sum) {
 // same lines serve both ways, a lane writing where it has read; only A and B in one plane are small enough to take
 // turns between two halves. TMA takes as long for a line of 64 bytes as for one of 128, some two cycles, and the
 // operands alone keep it busy (a 256 x 256 tile's stage 512 cycles, as long as its products), so lines are 128 bytes where
-// there is room: 12 x 1024 x 4096 bf16, five steps LINES_NOTE.
+// there is room: 8192 x 4096 bf16, five steps 1898 us with lines of 64 bytes, 1855 of 128. (Lines read and written with
+// 16 bytes a lane instead took 1705, but 12 x 1024 x 4096 971 in place of 910 and 512 x 512 no less.)
 // A stage is as small as the tile's columns allow: narrow tiles, of small matrices, wait for memory, and the more
 // of their stages are on their way the better.
 constexpr int kMostStages = 8;
 // Accumulators: tensor memory's 512 columns hold as many as the tile's width allows. Two would do for wide tiles; the
-// chunks of narrow ones, of two planes, take less time than an epilogue takes to answer (517 x 1031 f32 BUFS_NOTE).
+// chunks of narrow ones, of two planes, take less time than an epilogue takes to answer (517 x 1031 f32 208 us
+// with two, 192 so).
 constexpr int kMostAccs = 8;
 template <int PLANES, int CTAS>
 struct Ring {
@@ -89,7 +96,7 @@ struct Args {
     int per_item, total;       // tiles
     float alpha, beta;         // result = alpha * product + beta * what is added
     int stages;                // of the ring
-    __half *result;            // GRAM, SQUARE: [plane][item][rows][result_ld]
+    __half *result;            // GRAM, SQUARE: [plane][item][rows][result_ld], for what lies above the diagonal
     int64_t result_ld;
     bool last;                 // APPLY: the result is the caller's, f32 or bf16
     void *out;                 // where its lines do not start on 16-byte boundaries: stored without TMA
@@ -120,7 +127,7 @@ __device__ __forceinline__ Work work_of(int w, const Args &a) {
     } else {
         // B's side of the tiles varies first, `group` of them at a time, so that this much of B stays in L2 while X
         // goes by: with all of its 32 MB at a time one product of 8192 x 4096 reads 540 MB of memory, and the five steps take
-        // GROUP_NOTE.
+        // 1855 us; in groups of 16 MB 1820.
         const int inner = a.rows_first ? a.tiles_m : a.tiles_n, outer = a.rows_first ? a.tiles_n : a.tiles_m;
         const int g = w / (a.group * outer), size = min(a.group, inner - g * a.group);
         w -= g * a.group * outer;

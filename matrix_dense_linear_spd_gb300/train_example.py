@@ -1,6 +1,8 @@
 """A block-preconditioned training step built from this library's operators: softmax cross entropy
 and its gradients (xent, xent_grad), one SPD solve per 32-wide block of each weight's input
-(posv), and clipping of the whole step to a global norm (gclip).
+(posv), and clipping of the whole step to a global norm (gclip). With --orth the gradients are
+orthogonalised (orth) in place of the solves. After training the model is scored (score) and improved
+on its own samples by a few policy steps (score, score_grad, orth, gclip).
 
 The model is a two-layer token classifier, h = tanh(x A), logits = h W^T over a vocabulary. The
 gradient of a weight is preconditioned on its input side by the diagonal blocks of the input's
@@ -8,7 +10,7 @@ second moment, (X_b^T X_b / rows + mu I) S_b = G_b: one batch of 32 x 32 systems
 right-hand sides as the weight has outputs.
 
 Usage:
-  python -m matrix_dense_linear_spd_gb300.train_example [--steps 20] [--rows 4096] [--vocab 512]
+  python -m matrix_dense_linear_spd_gb300.train_example [--steps 20] [--rows 4096] [--vocab 512] [--orth]
 """
 from __future__ import annotations
 
@@ -34,7 +36,12 @@ def precondition(x, grad, mu=1e-2):
     return rhs.reshape(inputs, -1), info
 
 
-def step(params, x, target, lr, max_norm):
+def orthogonal(grad):
+    """The gradient with singular values of about 1, at the scale that a weight of its shape has."""
+    return bl.orth(grad) * max(1.0, grad.shape[0] / grad.shape[1]) ** 0.5
+
+
+def step(params, x, target, lr, max_norm, orth=False):
     """One training step in place. Returns (mean loss, norm of the preconditioned step, infos)."""
     A, W = params
     h = torch.tanh(x @ A)
@@ -43,12 +50,51 @@ def step(params, x, target, lr, max_norm):
     g = counted.float() / counted.sum().clamp(min=1)
     dh, dW = bl.xent_grad(h, W, target, lse, g)
     dA = x.T @ (dh * (1 - h * h))
-    step_A, info_A = precondition(x, dA)
-    step_W, info_W = precondition(h, dW.T)
+    if orth:
+        step_A, step_W = orthogonal(dA), orthogonal(dW.T)
+        info_A = info_W = torch.zeros(1, dtype=torch.int32, device=x.device)
+    else:
+        step_A, info_A = precondition(x, dA)
+        step_W, info_W = precondition(h, dW.T)
     norm = bl.gclip([step_A, step_W], max_norm)
     A.sub_(step_A, alpha=lr)
     W.sub_(step_W.T, alpha=lr)
     return (loss * g).sum(), norm, (info_A, info_W)
+
+
+def evaluate(params, x, target):
+    """(mean log probability, mean entropy, share of rows whose target is the likeliest token) of the rows that count."""
+    A, W = params
+    logp, entropy, _, _, likeliest = bl.score(torch.tanh(x @ A), W, target, top=1)
+    counted = (target >= 0) & (target < W.shape[0])
+    n = counted.sum().clamp(min=1)
+    return logp.sum() / n, entropy.sum() / n, (counted & (likeliest[:, 0] == target)).sum() / n
+
+
+def policy_gradients(params, x, action, advantage, entropy_weight):
+    """Gradients of the mean over the rows that count of advantage * logp(action) + entropy_weight * entropy:
+    (dA, dW, mean entropy)."""
+    A, W = params
+    h = torch.tanh(x @ A)
+    logp, entropy, lse, _, _ = bl.score(h, W, action)
+    counted = (action >= 0) & (action < W.shape[0])
+    share = counted.float() / counted.sum().clamp(min=1)
+    dh, dW = bl.score_grad(h, W, action, lse, entropy, share * advantage, share * entropy_weight)
+    return x.T @ (dh * (1 - h * h)), dW, (entropy * share).sum()
+
+
+def policy_step(params, x, target, lr, max_norm, entropy_weight=0.01):
+    """One step uphill in place: tokens sampled from the model, rewarded where they are the target."""
+    A, W = params
+    action = torch.multinomial(torch.softmax(torch.tanh(x @ A) @ W.T, 1), 1)[:, 0]
+    reward = (action == target).float()
+    action = torch.where(target >= 0, action, -1)
+    dA, dW, entropy = policy_gradients(params, x, action, reward - reward[target >= 0].mean(), entropy_weight)
+    step_A, step_W = orthogonal(dA), orthogonal(dW)
+    norm = bl.gclip([step_A, step_W], max_norm)
+    A.add_(step_A, alpha=lr)
+    W.add_(step_W, alpha=lr)
+    return reward[target >= 0].mean(), entropy, norm
 
 
 def problem(rows=4096, inputs=128, hidden=64, vocab=512, seed=0):
@@ -65,11 +111,11 @@ def problem(rows=4096, inputs=128, hidden=64, vocab=512, seed=0):
     return [normal(inputs, hidden, scale=inputs ** -0.5), normal(vocab, hidden, scale=0.02)], x, target
 
 
-def train(steps=20, lr=10.0, max_norm=0.25, **sizes):
-    params, x, target = problem(**sizes)
+def train(steps=20, lr=10.0, max_norm=0.25, orth=False, given=None, **sizes):
+    params, x, target = given or problem(**sizes)
     history = []
     for _ in range(steps):
-        loss, norm, infos = step(params, x, target, lr, max_norm)
+        loss, norm, infos = step(params, x, target, lr, max_norm, orth)
         history.append((loss, norm, torch.stack([i.abs().sum() for i in infos]).sum()))
     return [(float(a), float(b), int(c)) for a, b, c in history]
 
@@ -79,9 +125,16 @@ def main(argv=None):
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--rows", type=int, default=4096)
     ap.add_argument("--vocab", type=int, default=512)
+    ap.add_argument("--orth", action="store_true", help="orthogonalise the gradients in place of the solves")
     a = ap.parse_args(argv)
-    for i, (loss, norm, info) in enumerate(train(a.steps, rows=a.rows, vocab=a.vocab)):
+    params, x, target = given = problem(rows=a.rows, vocab=a.vocab)
+    for i, (loss, norm, info) in enumerate(train(a.steps, orth=a.orth, given=given)):
         print(f"step {i:3d}  loss {loss:.4f}  norm of the step before clipping {norm:8.3f}  failed pivots {info}")
+    logp, entropy, right = evaluate(params, x, target)
+    print(f"mean log probability {float(logp):.4f}  mean entropy {float(entropy):.4f}  likeliest token right {float(right):.3f}")
+    for i in range(3):
+        reward, entropy, norm = policy_step(params, x, target, lr=0.1, max_norm=1.0)
+        print(f"policy step {i}  reward {float(reward):.3f}  entropy {float(entropy):.4f}  norm {float(norm):.3f}")
 
 
 if __name__ == "__main__":
