@@ -448,7 +448,7 @@ __device__ __forceinline__ void lines_copy(const GemmArgs &a, const unsigned cha
     const int lane = threadIdx.x & 31, rows = min(32, a.m - row0), col = col0 + lane * PER;
     T *p = static_cast<T *>(a.out) + row0 * a.ldo + col;
     __syncwarp();
-#pragma unroll 1
+#pragma unroll 4
     for (int q = 0; q < rows; ++q, p += a.ldo) {
         const uint32_t x = *reinterpret_cast<const uint32_t *>(stage + q * 128 + (((lane >> 2) ^ (q & 7)) << 4) + (lane & 3) * 4);
         if constexpr (PER == 1) {
@@ -707,13 +707,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Shape sh = shape_of<MODE, CTAS>(a);
         float unit = 1.f;
         if constexpr (forms_p(MODE) || MODE == DW) unit = *a.unit;
+        // A warp's columns: half a tile's. (Parts of logits are a half of the widest tile each, whatever the tile.) With the
+        // first half alone at work on tiles of 128 columns dW of 20 rows x 1130 x 67549 in f32 took 280 us.
+        const int mine = MODE == DH || MODE == DW ? a.tile_n / 2 : kHalf, first = half * mine;
         uint32_t done = 0;
         bool ok = true;
         for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
             const Work k = work_of(w, a, sh);
             int cols = min(a.n - k.tn * a.tile_n, a.tile_n);                   // this warp's columns end there
             if (forms_p(MODE)) cols = (cols + 63) & ~63;
-            cols = min(cols, (half + 1) * kHalf);
+            cols = min(cols, first + mine);
             Row r;
             r.unit = unit;
             begin<MODE>(r, a, sh, k, (k.tm * CTAS + rank) * kTileM + quad * 32 + lane);
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (direct) {
                     if constexpr (MAY_BE_DIRECT) {
 #pragma unroll 1
-                        for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
+                        for (int c0 = first; c0 < cols; c0 += 32) {
                             __syncwarp();
                             tc::tmem_ld32(acc + c0, v[0]);
                             block<MODE, PLANES>(r, a, k, c0, cols, v[0], &map_out, stage);
@@ -743,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
 #pragma unroll
                     for (int b = 0; b < BLOCKS; ++b) {
-                        const int c0 = half * kHalf + 32 * b;
+                        const int c0 = first + 32 * b;
                         if (c0 < cols) {
                             float x[32];
                             tc::tmem_ld32(acc + c0, x);
@@ -769,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // once, and fetching is what four copies cost (P of 64 rows x 2048 x 32000 32 us instead of
                 // 28, the loss of 64 rows x 1024 x 32000 17.7 us instead of 17.0)
 #pragma unroll 1
-                for (int c0 = half * kHalf; c0 < cols; c0 += 32) {
+                for (int c0 = first; c0 < cols; c0 += 32) {
                     block<MODE, PLANES>(r, a, k, c0, cols, v[0], &map_out, stage);
 #pragma unroll
                     for (int b = 0; b + 1 < BLOCKS; ++b)
