@@ -285,7 +285,7 @@ struct Row {              // what an epilogue keeps of its row
 };
 
 template <int MODE>
-__device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s, const Work &w, int row) {
+__device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s, const Work &w, int row, unsigned char *stage) {
     r.row = row;
     r.m = s.m;
     if constexpr (MODE == DH) r.part_rows = part_rows(s.m);
@@ -299,16 +299,12 @@ __device__ __forceinline__ void begin(Row &r, const GemmArgs &a, const Shape &s,
         r.sum = r.picked = 0.f;
         if constexpr (MODE == SCORES) {
             r.t = 0.f;
-            int32_t least = kLowest;
+            r.floor = -INFINITY;
+            // the row's slots, on their way to shared memory while the products run
             if (a.top > 0 && a.slots && row < s.m) {
-                const int4 *const p = reinterpret_cast<const int4 *>(a.slots + static_cast<int64_t>(row) * a.slot_ld);
-                least = 0x7fffffff;
-                for (int j = 0; j < a.slot_ld / 4; ++j) {
-                    const int4 q = __ldcg(p + j);
-                    least = min(min(least, min(q.x, q.y)), min(q.z, q.w));
-                }
+                const int32_t *const p = a.slots + static_cast<int64_t>(row) * a.slot_ld;
+                for (int j = 0; j < a.slot_ld; j += 4) tc::copy16_async(stage + (threadIdx.x & 31) * 128 + 4 * j, p + j);
             }
-            r.floor = __int_as_float(in_order(least));
         }
         if constexpr (forms_p(MODE)) {
             r.lse = r.counted ? a.lse[src] : 0.f;
@@ -353,6 +349,7 @@ __device__ __forceinline__ void block_logits(Row &r, const GemmArgs &a, const Wo
 // As block_logits, with the entropy's sum. Where alternatives are wanted the block's largest logit is always
 // kept, the logits only where one of them reaches the row's floor: the least of the largest logits of `top`
 // groups of tiles, so that `top` logits at least are as large. What lies below is among no row's likeliest.
+// The instructions count: with K of 256 the products are done long before the epilogue.
 __device__ __forceinline__ void block_scores(Row &r, const GemmArgs &a, const Work &w, int c0, float (&v)[32]) {
     const int left = a.n - w.tn * a.tile_n - c0;
     if (left < 32) {
@@ -360,12 +357,15 @@ __device__ __forceinline__ void block_scores(Row &r, const GemmArgs &a, const Wo
         for (int i = 0; i < 32; ++i) v[i] = i < left ? v[i] : -INFINITY;
     }
     const uint32_t hit = r.at >= c0 && r.at < c0 + 32 ? 1u << (r.at - c0) : 0u;
-    float most = -INFINITY;
+    if (hit) {                                       // seldom for any of a warp's rows
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        if (hit >> i & 1) r.picked = v[i];
-        most = fmaxf(most, v[i]);
+        for (int i = 0; i < 32; ++i)
+            if (hit >> i & 1) r.picked = v[i];
     }
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmaxf(fmaxf(v[i], v[i + 8]), fmaxf(v[i + 16], v[i + 24]));
+    const float most = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7])));
     if (a.top > 0 && r.row < r.m) {
         const int64_t block = r.row * a.block_ld + (w.tn * a.tile_n + c0) / 32;
         a.block_max[block] = most;
@@ -375,27 +375,37 @@ __device__ __forceinline__ void block_scores(Row &r, const GemmArgs &a, const Wo
             for (int j = 0; j < 8; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
     }
-    const float m = fmaxf(r.top, most), ref = m == -INFINITY ? 0.f : m;
+    const float top = fmaxf(r.top, most), ref = top == -INFINITY ? 0.f : top;
     // Moving the reference by d: sum of e (x + d) = t + d sum, all times exp(d). Nothing is left of tiles whose
     // exponentials are 0, and an infinite d (no tile before) must not meet that 0.
     const float d = fmaxf(r.top - ref, -1e30f), scale = exp2f(d * kLog2e);
-    r.t = scale * fmaf(d, r.sum, r.t);
+    float t[4] = {scale * fmaf(d, r.sum, r.t), 0.f, 0.f, 0.f};         // of one sign: the order matters little
     r.sum *= scale;
-    float x[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const float at = v[i] - ref;
-        v[i] = exp2f(at * kLog2e);
-        x[i] = v[i] * fmaxf(at, -1e30f);           // a logit of minus infinity: 0 times a finite number
+        v[i] = tc::ex2(at * kLog2e);
+        t[i & 3] = fmaf(v[i], fmaxf(at, -1e30f), t[i & 3]);            // a logit of minus infinity: 0 times a finite number
     }
-    // pairwise, as in block_logits; every term of the second sum has one sign
+    // pairwise, as in block_logits
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < o; ++i) v[i] += v[i + o], x[i] += x[i + o];
+        for (int i = 0; i < o; ++i) v[i] += v[i + o];
     r.sum += v[0];
-    r.t += x[0];
-    r.top = m;
+    r.t = (t[0] + t[1]) + (t[2] + t[3]);
+    r.top = top;
+}
+// The row's floor, from the slots that begin() asked for.
+__device__ __forceinline__ void floor_of(Row &r, const GemmArgs &a, const unsigned char *stage) {
+    if (a.top == 0 || !a.slots) return;
+    tc::copies_wait();
+    int32_t least = 0x7fffffff;
+    for (int j = 0; j < a.slot_ld; j += 4) {
+        const int4 q = *reinterpret_cast<const int4 *>(stage + (threadIdx.x & 31) * 128 + 4 * j);
+        least = min(min(least, min(q.x, q.y)), min(q.z, q.w));
+    }
+    if (r.row < r.m) r.floor = __int_as_float(in_order(least));
 }
 
 template <int MODE>
@@ -719,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cols = min(cols, first + mine);
             Row r;
             r.unit = unit;
-            begin<MODE>(r, a, sh, k, (k.tm * CTAS + rank) * kTileM + quad * 32 + lane);
+            begin<MODE>(r, a, sh, k, (k.tm * CTAS + rank) * kTileM + quad * 32 + lane, stage);
             const bool direct = MAY_BE_DIRECT && k.kb1 - k.kb0 <= a.chunk;
             float v[BLOCKS][32];
             if (!direct) {
@@ -768,6 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             if (!direct) {
+                if constexpr (MODE == SCORES) floor_of(r, a, stage);
                 // One copy of the code for the four blocks, whose sums move up: a CTA with one tile fetches it
                 // once, and fetching is what four copies cost (P of 64 rows x 2048 x 32000 32 us instead of
                 // 28, the loss of 64 rows x 1024 x 32000 17.7 us instead of 17.0)
