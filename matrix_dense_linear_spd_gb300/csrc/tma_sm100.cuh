@@ -79,6 +79,13 @@ __device__ __forceinline__ void copy16_async(void *dst, const void *src) {
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
+// 32 bytes at once (32-byte aligned).
+__device__ __forceinline__ void store8(float *p, const float *v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
+                 "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 // 2^x to 2^-22, 0 below f32's normal range.
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -581,7 +581,7 @@ Plan plan_for(int dtype, const void *H, int64_t ldh, int64_t rows, int64_t dim, 
         q.picked = take(rows * 4);
         if (score) q.part_t = take(rows * q.part_ld * 4);
         if (top) {
-            q.block_ld = cdiv(std::min(q.piece, vocab), 32);
+            q.block_ld = up(cdiv(std::min(q.piece, vocab), 32), 4);
             q.block_max = take(rows * q.block_ld * 4);
             q.logits = take(rows * q.block_ld * 128);
             if (q.pieces > 1) q.best = take(rows * top * 8);

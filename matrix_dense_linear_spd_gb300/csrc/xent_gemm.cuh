@@ -279,6 +279,7 @@ struct Row {              // what an epilogue keeps of its row
     bool counted;
     float top, sum, picked;    // LOGITS
     float t, floor;            // SCORES
+    float4 blocks;             // largest logits of its blocks, the last one last
     float lse, g;              // PROBS
     float entropy, e;          // SPROBS
     float unit;                // PROBS, DW
@@ -367,14 +368,13 @@ __device__ __forceinline__ void block_scores(Row &r, const GemmArgs &a, const Wo
     for (int i = 0; i < 8; ++i) m[i] = fmaxf(fmaxf(v[i], v[i + 8]), fmaxf(v[i + 16], v[i + 24]));
     const float most = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7])));
     if (a.top > 0 && r.row < r.m) {
-        const int64_t block = r.row * a.block_ld + (w.tn * a.tile_n + c0) / 32;
-        a.block_max[block] = most;
         if (most >= r.floor) {
-            float4 *const p = reinterpret_cast<float4 *>(a.logits + block * 32);
+            float *const p = a.logits + (r.row * a.block_ld + (w.tn * a.tile_n + c0) / 32) * 32;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            for (int j = 0; j < 32; j += 8) tc::store8(p + j, v + j);
         }
     }
+    r.blocks = make_float4(r.blocks.y, r.blocks.z, r.blocks.w, most);
     const float top = fmaxf(r.top, most), ref = top == -INFINITY ? 0.f : top;
     // Moving the reference by d: sum of e (x + d) = t + d sum, all times exp(d). Nothing is left of tiles whose
     // exponentials are 0, and an infinite d (no tile before) must not meet that 0.
@@ -416,6 +416,14 @@ __device__ __forceinline__ void end(const Row &r, const GemmArgs &a, const Work 
             if (r.at >= half * kHalf && r.at < (half + 1) * kHalf) a.picked[r.row] = r.picked;
             if constexpr (MODE == SCORES) {
                 a.part_t[r.row * a.part_ld + 2 * w.tn + half] = r.t;
+                // the blocks of this part; its first one's place is a multiple of four in a row of whole fours
+                const int first = w.tn * a.tile_n + half * kHalf;
+                const int blocks = a.top > 0 ? (min(min(a.n - w.tn * a.tile_n, a.tile_n) - half * kHalf, kHalf) + 31) / 32 : 0;
+                float *const most = a.block_max + r.row * a.block_ld + first / 32;
+                if (blocks == 4) *reinterpret_cast<float4 *>(most) = r.blocks;
+                if (blocks == 3) most[0] = r.blocks.y, most[1] = r.blocks.z, most[2] = r.blocks.w;
+                if (blocks == 2) most[0] = r.blocks.z, most[1] = r.blocks.w;
+                if (blocks == 1) most[0] = r.blocks.w;
                 if (a.top > 0 && a.slots && r.top > r.floor)
                     atomicMax(a.slots + static_cast<int64_t>(r.row) * a.slot_ld + (2 * w.tn + half) % a.top,
                               in_order(__float_as_int(r.top)));
