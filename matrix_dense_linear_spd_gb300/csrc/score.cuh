@@ -81,7 +81,7 @@ struct Gather {
 template <int WARPS>
 __device__ __forceinline__ void row_sync() {
     if constexpr (WARPS == 1) __syncwarp();
-    else __syncthreads();
+    else asm volatile("bar.sync %0, %1;\n" ::"r"(1 + static_cast<int>(threadIdx.x) / (WARPS * 32)), "n"(WARPS * 32) : "memory");
 }
 // key(i) for i < n; `given`: a further key of this lane (0: none; first warp only). The result is g.chosen, 0 where there
 // are fewer. floor: what `top` keys are known to reach, or 0.
@@ -113,9 +113,9 @@ __device__ __forceinline__ void select(Gather &g, int64_t n, uint64_t given, int
         each([&](uint64_t k) { most = k > most ? k : most; });
         if constexpr (WARPS > 1) {
             if (thread < 32) g.lanes[lane] = 0;
-            __syncthreads();
+            row_sync<WARPS>();
             atomicMax(reinterpret_cast<unsigned long long *>(&g.lanes[lane]), static_cast<unsigned long long>(most));
-            __syncthreads();
+            row_sync<WARPS>();
             most = g.lanes[lane];
         }
         floor = __shfl_sync(0xffffffffu, sorted(most), top - 1);
@@ -207,8 +207,8 @@ struct Scores {
     int64_t *top_id;
 };
 
-// WARPS warps share a row: 8 where rows are few or long, else 1. (4096 rows of 3126 blocks: 1127 us in
-// all, and 1135; of 1000 blocks 283, and 248.)
+// WARPS warps share a row. With 1, 2, 4 and 8 calls of dim 256 take: 4096 rows of 250 blocks 66, 72, 85, 115 us; of 1000 blocks
+// 216, 212, 224, 252; 1000 rows of 500 blocks 50, 47, 46, 53; (dim 2048) 4096 rows of 3126 blocks 1129, 1124, 1118, 1138.
 template <int WARPS>
 __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Scores a) {
     constexpr int ROWS = 8 / WARPS, HELD = 8;
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Sco
         most = warp_max(most);
         if constexpr (WARPS > 1) {
             if (lane == 0) tops[warp] = most;
-            __syncthreads();
-            for (int w = 0; w < WARPS; ++w) most = fmaxf(most, tops[w]);
+            row_sync<WARPS>();
+            for (int w = 0; w < WARPS; ++w) most = fmaxf(most, tops[warp - share + w]);
         }
         ref = most == -INFINITY ? 0.f : most;
         const auto add = [&](float2 x, float xt) {
@@ -288,9 +288,9 @@ __global__ void __launch_bounds__(256) scores_kernel(const __grid_constant__ Sco
         }
         if constexpr (WARPS > 1) {
             if (lane == 0) sums[warp] = sum, sums_t[warp] = sum_t;
-            __syncthreads();
+            row_sync<WARPS>();
             sum = sum_t = 0.f;
-            for (int w = 0; w < WARPS; ++w) sum += sums[w], sum_t += sums_t[w];
+            for (int w = 0; w < WARPS; ++w) sum += sums[warp - share + w], sum_t += sums_t[warp - share + w];
         }
         log_sum = logf(sum);
         sound = sum > 0.f && !bad;

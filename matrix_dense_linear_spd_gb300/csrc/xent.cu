@@ -441,8 +441,6 @@ constexpr int kChunkF32 = 2, kChunkLoss = 16, kChunkFew = 1, kChunkBf16 = 256;
 // 131072 in bf16 and 1024 x 1024 x 32000 in f32 at 64, 128, 512 and 2048 MB: 11.04, 10.84, 10.66, 10.65 ms
 // and 1.22, 1.13, 1.04, 1.04 ms
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
-// Blocks or parts of a row from which on eight warps join them, whatever the number of rows.
-constexpr int64_t kLongRow = 2048;
 // Bytes of the logits that a piece's blocks may keep for the alternatives (few of them are written).
 constexpr int64_t kLogitBytes = int64_t(2) << 30;
 
@@ -761,10 +759,10 @@ bl_status run(const char *op, const Plan &q, const Call &c) {
         }
     }
     const auto join_scores = [&] {
-        // eight warps a row while all their CTAs run at once, and where a row's blocks or parts keep them busy
-        const bool eight = c.rows <= 4 * c.sms || q.block_ld >= kLongRow || q.part_ld >= kLongRow;
-        return eight ? launch_pdl(scores_kernel<8>, static_cast<unsigned>(rows), 256, 0, c.s, scores)
-                        : launch_pdl(scores_kernel<1>, static_cast<unsigned>(cdiv(rows, 8)), 256, 0, c.s, scores);
+        // as many warps a row as are at work at once, or as its blocks keep busy
+        const int warps = c.rows <= 4 * c.sms ? 8 : c.rows <= 8 * c.sms || q.block_ld >= 2048 ? 4 : q.block_ld >= 768 ? 2 : 1;
+        const auto kernel = warps == 8 ? scores_kernel<8> : warps == 4 ? scores_kernel<4> : warps == 2 ? scores_kernel<2> : scores_kernel<1>;
+        return launch_pdl(kernel, static_cast<unsigned>(cdiv(rows, 8 / warps)), 256, 0, c.s, scores);
     };
     if (q.few) {
         const bool vec = few_vec(c.W, c.ldw, c.dim, sizeof(T));
