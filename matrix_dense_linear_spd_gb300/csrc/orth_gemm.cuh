@@ -474,9 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto take = [&] {
                 if constexpr (F::kAdd > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, units & 1, kPolls)) && ok;
             };
+            if (first < cols) ask(first);              // on its way while the products run
             if constexpr (PLANES == 1) {
                 // blocks go out as they leave tensor memory
-                if (first < cols) ask(first);
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_full[done & (accs - 1)], done >> acc_bits & 1, kPolls));
                 if (!ok) {
                     if (first < cols) take();
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // one copy of the code for the blocks, whose sums move up
 #pragma unroll 1
                     for (int c0 = first; c0 < cols; c0 += UNIT) {
-                        ask(c0);
+                        if (c0 > first) ask(c0);
                         take();
                         block_out<KIND, PLANES>(a, k.item, row0, n0 + c0, 0, v[0], lines0);
                         unit_out<KIND, PLANES>(&map_out, a, k.item, row0, n0 + c0, lines0);
@@ -552,6 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 32; ++i) v[b][i] = v[b + 1][i];
                     }
                     __syncwarp();
+                } else if (first < cols) {
+                    take();
                 }
             }
             if (!ok && lane == 0) gave_up = 1;
