@@ -189,6 +189,8 @@ int stages_of(const Shape &s) {
     return std::min(kMostStages, Ring<PLANES, 1>::kBytes / (s.ctas == 1 ? Ring<PLANES, 1>::stage(s.tile_n) : Ring<PLANES, 2>::stage(s.tile_n)));
 }
 
+constexpr int64_t kMostChunks = 1216;              // CTAs that form a matrix's norm and its first X
+
 struct Plan {
     int planes;
     int64_t lines, width, small, batch;
@@ -209,7 +211,8 @@ Plan plan_for(int dtype, int64_t lines, int64_t width, int64_t batch, int sms) {
     q.ldx = up(width, 64);
     q.lda = up(q.small, 64);
     const int64_t groups = lines * cdiv(width, 8);
-    q.chunks = static_cast<int>(std::max<int64_t>(1, std::min(cdiv(groups, 1024), static_cast<int64_t>(sms) * 8 / batch)));
+    // by the matrix alone, so that its norm is the same to the last bit in any batch
+    q.chunks = static_cast<int>(std::min(cdiv(groups, 1024), kMostChunks));
     const int64_t kb_small = cdiv(q.small, kTileK), kb_long = cdiv(std::max(lines, width), kTileK);
     q.gram = shape_for(q.small, q.small, true, !q.wide, batch, kb_long, q.planes, sms);
     q.square = shape_for(q.small, q.small, true, false, batch, kb_small, q.planes, sms);
