@@ -218,7 +218,8 @@ __device__ __forceinline__ void block_out(const Args &a, int item, int row0, int
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<uint4 *>(lines + at_line<64>(lane, 4 * b + j)) = make_uint4(
-                    bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]), bf16x2(v[8 * j + 4], v[8 * j + 5]), bf16x2(v[8 * j + 6], v[8 * j + 7]));
+                    bf16x2(v[8 * j], v[8 * j + 1]), bf16x2(v[8 * j + 2], v[8 * j + 3]), bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                    bf16x2(v[8 * j + 6], v[8 * j + 7]));
         } else {
             __syncwarp();                   // lines of f32 lie across what other lanes have read
 #pragma unroll

@@ -11,7 +11,8 @@ namespace bl {
 namespace orth {
 
 template <int KIND, bool A_MN, bool B_MN, int PLANES, int CTAS>
-cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo, const Args &a, int sms, cudaStream_t s) {
+cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo, const Args &a,
+                         int sms, cudaStream_t s) {
     constexpr int kSmem = Ring<PLANES, CTAS>::kSmem;
     const auto kernel = product_kernel<KIND, A_MN, B_MN, PLANES, CTAS>;
     static std::atomic<int> groups[64];         // CTAs, or pairs of CTAs, that the device runs at once
@@ -44,8 +45,8 @@ cudaError_t launch_tiles(const CUtensorMap &ma, const CUtensorMap &mb, const CUt
 }
 
 template <int PLANES>
-cudaError_t launch(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md, const CUtensorMap &mo, const Args &a, int sms,
-                   cudaStream_t s) {
+cudaError_t launch(Layout layout, int ctas, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &md,
+                   const CUtensorMap &mo, const Args &a, int sms, cudaStream_t s) {
     switch (layout) {
         case GRAM_LINES:
             return ctas == 1 ? launch_tiles<GRAM, false, false, PLANES, 1>(ma, mb, md, mo, a, sms, s)
