@@ -67,12 +67,15 @@ __device__ __forceinline__ double block_sum(double s) {
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = s;
     __syncthreads();
-    s = 0.0;
-    for (int w = 0; w < 8; ++w) s += warps[w];
-    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0.0;
+        for (int w = 0; w < 8; ++w) s += warps[w];
+    }
     return s;
 }
 
+// (An SM adds f64 values at a sixtieth of its f32 rate: with all threads of the first X's CTAs adding up the norm and one CTA for 1024
+// groups of values, 12 x 1024 x 4096 took 994 us in place of 960.)
 // Sums of squares: eight in f32, from there on f64. Where eight leave f32's comfortable range they are formed
 // again in f64.
 template <typename T>
@@ -107,10 +110,16 @@ __global__ void __launch_bounds__(256) begin_kernel(const __grid_constant__ Sour
     pdl_wait();
     const int64_t item = blockIdx.x / q.chunks;
     const uint32_t chunk = blockIdx.x - item * q.chunks, all = q.lines * q.per_line;
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < q.chunks; i += 256) sum += q.sums[item * q.chunks + i];
-    sum = block_sum(sum);
-    const float2 factor = scale_of(sum);
+    __shared__ float2 shared_factor;
+    if (threadIdx.x < 32) {               // of the small f64 unit as little as will do: a warp, then a thread
+        double sum = 0.0;
+        for (int i = threadIdx.x; i < q.chunks; i += 32) sum += q.sums[item * q.chunks + i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (threadIdx.x == 0) shared_factor = scale_of(sum);
+    }
+    __syncthreads();
+    const float2 factor = shared_factor;
     const T *const g = static_cast<const T *>(q.g) + item * q.stride;
     __half *const to = x + item * q.lines * ldx;
     for (uint32_t i = chunk * 256 + threadIdx.x; i < all; i += q.chunks * 256) {
@@ -189,8 +198,6 @@ int stages_of(const Shape &s) {
     return std::min(kMostStages, Ring<PLANES, 1>::kBytes / (s.ctas == 1 ? Ring<PLANES, 1>::stage(s.tile_n) : Ring<PLANES, 2>::stage(s.tile_n)));
 }
 
-constexpr int64_t kMostChunks = 1216;              // CTAs that form a matrix's norm and its first X
-
 struct Plan {
     int planes;
     int64_t lines, width, small, batch;
@@ -212,7 +219,7 @@ Plan plan_for(int dtype, int64_t lines, int64_t width, int64_t batch, int sms) {
     q.lda = up(q.small, 64);
     const int64_t groups = lines * cdiv(width, 8);
     // by the matrix alone, so that its norm is the same to the last bit in any batch
-    q.chunks = static_cast<int>(std::min(cdiv(groups, 1024), kMostChunks));
+    q.chunks = static_cast<int>(std::max(std::min<int64_t>(cdiv(groups, 1024), 128), std::min<int64_t>(cdiv(groups, 4096), 1216)));
     const int64_t kb_small = cdiv(q.small, kTileK), kb_long = cdiv(std::max(lines, width), kTileK);
     q.gram = shape_for(q.small, q.small, true, !q.wide, batch, kb_long, q.planes, sms);
     q.square = shape_for(q.small, q.small, true, false, batch, kb_small, q.planes, sms);
