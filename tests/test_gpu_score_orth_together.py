@@ -100,3 +100,48 @@ def test_shared_vectors_and_views():
     assert torch.equal(dH, cH) and torch.equal(dW, cW)
     with pytest.raises(bl.BLError):
         bl.score_grad(W[100:200], W, t, a["lse"], a["entropy"], g, e, dH=W[:100])
+
+
+def spread(m, ld):
+    """m's rows ld values apart, in memory that nobody else needs."""
+    torch = torch_cuda()
+    flat = torch.empty((m.shape[0] - 1) * ld + m.shape[1], device="cuda", dtype=m.dtype)
+    return flat.as_strided(m.shape, (ld, 1)).copy_(m)
+
+
+@pytest.mark.parametrize("rows,cols", [(100, 200), (2200, 90), (300, 160)])
+def test_steps_of_matrices_whose_offsets_pass_32_bits(rows, cols):
+    torch, bl = torch_cuda(), lib()
+    G = matrix(rows, cols, "bf16", 1, seed=3)[0]
+    ld = (5 << 30) // rows // 8 * 8
+    far = spread(G, ld)
+    want = bl.orth(G)
+    assert torch.equal(bl.orth(far), want)
+    assert torch.equal(bl.orth(far.T), want.T)
+    assert torch.equal(bl.orth(far, out=far), want)
+
+
+@pytest.mark.parametrize("rows", [1, 60, 200])
+def test_scores_of_vectors_whose_offsets_pass_32_bits(rows):
+    torch, bl = torch_cuda(), lib()
+    H, W, t, _ = make(rows, 72, 2000, "bf16", seed=4)
+    g, e = weights(rows)
+    want = score_all(H, W, t, 5, g, e)
+    far = spread(W, (5 << 30) // 2000 // 8 * 8)
+    assert equal(score_all(H, far, t, 5, g, e), want)
+    if rows > 1:
+        assert equal(score_all(spread(H, (5 << 30) // rows // 8 * 8), W, t, 5, g, e), want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_a_small_matrix_that_gave_up_is_seen(kind):
+    torch, bl = torch_cuda(), lib()
+    G = matrix(60, 40, kind, 200, seed=5)
+    want = bl.orth(G)
+    switch = bl.get_lib().bl_debug_xent_gave_up
+    switch(1)
+    try:
+        got = bl.orth(G)
+    finally:
+        switch(0)
+    assert bool(got.isnan().all()) and torch.equal(bl.orth(G), want)
