@@ -672,46 +672,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
       } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        // The whole warp goes through the steps, so that what the products are issued with is known to be the same in all
+        // lanes; an elected lane issues, in 40 cycles a product. (In a branch of one lane it took 115, and a stage's
+        // four products with the look at its barrier longer than the 512 cycles that the products take.) A lane looks
+        // at one stage's barrier, 150 cycles, so that all that is there is found at once.
+        if (rank == 0) {
             const Shape sh = shape_of<MODE, CTAS>(a);
             const uint64_t da0 = A_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_a), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_a));
             const uint64_t db0 = B_MN ? tc::sdesc_mn_sw128(tc::smem_u32(tiles_b), kTileK * 128) : tc::sdesc_sw128(tc::smem_u32(tiles_b));
-            uint32_t s = 0, phase = 0, done = 0;
+            uint32_t s = 0, phase = 0, done = 0, there = 0;
             bool ok = true;
+            const auto look = [&] {                    // how many stages from s on are there
+                const uint32_t t = s + lane, wrapped = t >= kStages;
+                for (uint32_t i = 0; there == 0 && i < kPolls; ++i) {
+                    const bool now = lane < kStages && tc::mbar_wait(&full[wrapped ? t - kStages : t], phase ^ wrapped, 1);
+                    there = __ffs(~__ballot_sync(0xffffffffu, now)) - 1;
+                }
+                __syncwarp();
+                return there > 0;
+            };
             for (int w = blockIdx.x / CTAS; ok && w < sh.total; w += gridDim.x / CTAS) {
                 const Work k = work_of(w, a, sh);
                 const uint32_t idesc = tc::idesc_bf16(CTAS * kTileM, cols_of<B_MN, CTAS>(k.tn, a), A_MN, B_MN);
                 for (int c = k.kb0; ok && c < k.kb1; c += a.chunk, ++done) {
                     const uint32_t acc = tmem + (done & 1) * kTileN;
-                    if (!tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after_sync();
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&acc_empty[done & 1], (done >> 1 & 1) ^ 1, kPolls));
+                    if (!ok) break;
                     const int steps = min(c + a.chunk, k.kb1) - c;
                     for (int i = 0; i < steps; ++i) {
-                        if (!tc::mbar_wait(&full[s], phase, kPolls)) {
-                            ok = false;
-                            break;
-                        }
+                        if (there == 0) ok = look();
+                        if (!ok) break;
+                        --there;
                         tc::fence_after_sync();
                         const uint64_t da = da0 + s * (kStageA >> 4), db = db0 + s * (kStageB >> 4);
+                        if (tc::elect()) {
 #pragma unroll
-                        for (int q = 0; q < PAIRS; ++q) {
-                            const int pa = pair_a(q, PAIRS), pb = pair_b(q, PAIRS);
+                            for (int q = 0; q < PAIRS; ++q) {
+                                const int pa = pair_a(q, PAIRS), pb = pair_b(q, PAIRS);
 #pragma unroll
-                            for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
-                                tc::mma_f16<CTAS>(acc, da + pa * (kBytesA >> 4) + j * (A_MN ? 2048 / 16 : 2),
-                                                  db + pb * (kBytesB >> 4) + j * (B_MN ? 2048 / 16 : 2), idesc,
-                                                  i > 0 || q > 0 || j > 0);
+                                for (int j = 0; j < kTileK / 16; ++j)   // 16 k: 32 bytes along a line, or 16 lines
+                                    tc::mma_f16<CTAS>(acc, da + pa * (kBytesA >> 4) + j * (A_MN ? 2048 / 16 : 2),
+                                                      db + pb * (kBytesB >> 4) + j * (B_MN ? 2048 / 16 : 2), idesc,
+                                                      i > 0 || q > 0 || j > 0);
+                            }
+                            tc::mma_commit_all<CTAS>(&empty[s]);
+                            if (i + 1 == steps) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
                         }
-                        tc::mma_commit_all<CTAS>(&empty[s]);
+                        __syncwarp();
                         if (++s == kStages) s = 0, phase ^= 1;
                     }
-                    if (ok) tc::mma_commit_all<CTAS>(&acc_full[done & 1]);
                 }
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 gave_up = 1;
                 tc::mma_commit_all<CTAS>(&drained);
                 tc::mbar_wait(&drained, 0, kPolls);
