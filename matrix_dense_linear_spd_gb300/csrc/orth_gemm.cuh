@@ -15,7 +15,7 @@
 // time from the lanes side by side, block by block transposed.
 //
 // A CTA computes 128 x tile_n tiles, or a pair of CTAs 256 x tile_n tiles (each holds its 128 rows and half of B).
-// Roles, waits and registers as in xent_gemm.cuh: a producer thread for each operand, an issuing warp, eight
+// Roles, waits and registers as in xent_gemm.cuh: a producer warp for each operand, an issuing warp, eight
 // epilogue warps that work on one accumulator of tensor memory while the next tile is added up in another. With
 // PLANES = 2 the chain of K is cut into chunks that are added in registers: tensor memory's f32 sums cut where f32
 // would round, up to 2^-23.4 of the sum a step for the diagonal of A.
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
       tc::regs_dec<kRegsFew>();
       if (warp == 0 || warp == 2) {
-        if (lane == 0) {
+        {
             const bool for_a = warp == 0, announce = for_a && rank == 0;
             const uint32_t bar0 = CTAS == 1 ? tc::smem_u32(full) : tc::at_leader(full);
             uint32_t s = 0, phase = 0, issued = 0;
@@ -350,40 +350,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int groups_b = (part + 63) >> 6;
                 const uint32_t bytes = CTAS * PLANES * (kBytesA + (B_MN ? groups_b * (kTileK * 128) : a.tile_n / CTAS * 128));
                 for (int kb = 0; kb < a.kblocks; ++kb) {
-                    if (!tc::mbar_wait(&empty[s], phase ^ 1, kPolls)) {
-                        ok = false;
-                        break;
-                    }
-                    if (announce) tc::mbar_expect_tx(&full[s], bytes);
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], phase ^ 1, kPolls));
+                    if (!ok) break;
                     const uint32_t bar = bar0 + 8 * s;
+                    if (tc::elect()) {
+                        if (announce) tc::mbar_expect_tx(&full[s], bytes);
 #pragma unroll 1
-                    for (int p = 0; p < PLANES; ++p) {
-                        const int z = p * a.batch + k.item;
-                        if (for_a) {
-                            unsigned char *const d = tiles_a + s * kStageA + p * kBytesA;
-                            if constexpr (A_MN) {
+                        for (int p = 0; p < PLANES; ++p) {
+                            const int z = p * a.batch + k.item;
+                            if (for_a) {
+                                unsigned char *const d = tiles_a + s * kStageA + p * kBytesA;
+                                if constexpr (A_MN) {
 #pragma unroll
-                                for (int j = 0; j < kTileM / 64; ++j)
-                                    tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_a, bar, m0 + 64 * j, kb * kTileK, z);
+                                    for (int j = 0; j < kTileM / 64; ++j)
+                                        tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_a, bar, m0 + 64 * j, kb * kTileK, z);
+                                } else {
+                                    tc::tma_load_3d<CTAS>(d, &map_a, bar, kb * kTileK, m0, z);
+                                }
                             } else {
-                                tc::tma_load_3d<CTAS>(d, &map_a, bar, kb * kTileK, m0, z);
-                            }
-                        } else {
-                            unsigned char *const d = tiles_b + s * stage_b + p * bytes_b;
-                            if constexpr (B_MN) {
+                                unsigned char *const d = tiles_b + s * stage_b + p * bytes_b;
+                                if constexpr (B_MN) {
 #pragma unroll 1
-                                for (int j = 0; j < groups_b; ++j)
-                                    tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_b, bar, n0 + 64 * j, kb * kTileK, z);
-                            } else {
-                                tc::tma_load_3d<CTAS>(d, &map_b, bar, kb * kTileK, n0, z);
+                                    for (int j = 0; j < groups_b; ++j)
+                                        tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_b, bar, n0 + 64 * j, kb * kTileK, z);
+                                } else {
+                                    tc::tma_load_3d<CTAS>(d, &map_b, bar, kb * kTileK, n0, z);
+                                }
                             }
                         }
                     }
+                    __syncwarp();
                     issued = min(issued + 1, stages);
                     if (++s == stages) s = 0, phase ^= 1;
                 }
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 gave_up = 1;
                 // the copies in flight: the last `issued` stages before s, oldest first
                 for (uint32_t i = 0; rank == 0 && i < issued; ++i) {

@@ -609,9 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
       tc::regs_dec<kRegsFew>();
       if (warp == 0 || warp == 2) {
-        // Two producers, one for each operand: a thread needs 100 to 200 cycles to issue a copy, and
-        // a stage's products take 512. The leader's first announces the bytes of both CTAs.
-        if (lane == 0) {
+        // Two producers, one for each operand, each a warp of which an elected lane issues (in a branch of one thread a copy takes
+        // 100 to 200 cycles, and a stage's products 512: dH and dW of 4096 x 4096 x 16384 had the tensor pipe 85% busy,
+        // and 92 so). The leader's first announces the bytes of both CTAs.
+        {
             const Shape sh = shape_of<MODE, CTAS>(a);
             const bool for_a = warp == 0, announce = for_a && rank == 0;
             const uint32_t bar0 = CTAS == 1 ? tc::smem_u32(full) : tc::at_leader(full);
@@ -624,45 +625,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int groups_b = (part + 63) >> 6;
                 const uint32_t bytes = CTAS * (PA * kBytesA + PB * (B_MN ? groups_b * (kTileK * 128) : a.tile_n / CTAS * 128));
                 for (int kb = k.kb0; kb < k.kb1; ++kb) {
-                    if (!tc::mbar_wait(&empty[s], phase ^ 1, kPolls)) {
-                        ok = false;
-                        break;
-                    }
-                    if (announce) tc::mbar_expect_tx(&full[s], bytes);
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], phase ^ 1, kPolls));
+                    if (!ok) break;
                     const uint32_t bar = bar0 + 8 * s;
+                    if (tc::elect()) {
+                        if (announce) tc::mbar_expect_tx(&full[s], bytes);
 #pragma unroll 1
-                    for (int p = 0; p < (for_a ? PA : PB); ++p) {
-                        if (for_a) {
-                            unsigned char *const d = tiles_a + s * kStageA + p * kBytesA;
-                            const int z = p * a.ca.plane;
-                            if constexpr (A_MN) {
+                        for (int p = 0; p < (for_a ? PA : PB); ++p) {
+                            if (for_a) {
+                                unsigned char *const d = tiles_a + s * kStageA + p * kBytesA;
+                                const int z = p * a.ca.plane;
+                                if constexpr (A_MN) {
 #pragma unroll
-                                for (int j = 0; j < kTileM / 64; ++j) {
-                                    const int g = m0 / 64 + j;
-                                    tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_a, bar, g * a.ca.x, kb * kTileK, z + g * a.ca.z);
+                                    for (int j = 0; j < kTileM / 64; ++j) {
+                                        const int g = m0 / 64 + j;
+                                        tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_a, bar, g * a.ca.x, kb * kTileK, z + g * a.ca.z);
+                                    }
+                                } else {
+                                    tc::tma_load_3d<CTAS>(d, &map_a, bar, kb * a.ca.x, m0, z + kb * a.ca.z);
                                 }
                             } else {
-                                tc::tma_load_3d<CTAS>(d, &map_a, bar, kb * a.ca.x, m0, z + kb * a.ca.z);
-                            }
-                        } else {
-                            unsigned char *const d = tiles_b + s * kStageB + p * kBytesB;
-                            const int z = p * a.cb.plane;
-                            if constexpr (B_MN) {
+                                unsigned char *const d = tiles_b + s * kStageB + p * kBytesB;
+                                const int z = p * a.cb.plane;
+                                if constexpr (B_MN) {
 #pragma unroll 1
-                                for (int j = 0; j < groups_b; ++j) {
-                                    const int g = n0 / 64 + j;
-                                    tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_b, bar, g * a.cb.x, kb * kTileK, z + g * a.cb.z);
+                                    for (int j = 0; j < groups_b; ++j) {
+                                        const int g = n0 / 64 + j;
+                                        tc::tma_load_3d<CTAS>(d + j * kTileK * 128, &map_b, bar, g * a.cb.x, kb * kTileK, z + g * a.cb.z);
+                                    }
+                                } else {
+                                    tc::tma_load_3d<CTAS>(d, &map_b, bar, kb * a.cb.x, n0, z + kb * a.cb.z);
                                 }
-                            } else {
-                                tc::tma_load_3d<CTAS>(d, &map_b, bar, kb * a.cb.x, n0, z + kb * a.cb.z);
                             }
                         }
                     }
+                    __syncwarp();
                     issued = min(issued + 1, static_cast<uint32_t>(kStages));
                     if (++s == kStages) s = 0, phase ^= 1;
                 }
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 gave_up = 1;
                 // the copies in flight: the last `issued` stages before s, oldest first
                 for (uint32_t i = 0; rank == 0 && i < issued; ++i) {
