@@ -242,7 +242,7 @@ Plan plan_for(int dtype, int64_t lines, int64_t width, int64_t batch, int sms) {
 // ------------------------------------------------------------------ launches
 
 // Bytes of B whose tiles are worked on together. 4096 x 8192 and 8192 x 4096 bf16 at 8, 16 and 32 MB: 1868 and 1853,
-// 1812 and 1820, 1810 and 1838 us.
+// 1812 and 1820, 1810 and 1838 us (1735 to 1770 at 16 since whole warps issue products and copies).
 constexpr int64_t kGroupBytes = int64_t(16) << 20;
 // K is added in tensor memory over so many 64-deep steps at a time: two planes as in the cross entropy's f32
 // products, one plane (whose results are rounded to 11 bits, or added to a X) without end.

@@ -10,7 +10,7 @@
 //
 // A CTA computes 128 x 256 tiles, or a pair of CTAs 256 x 256 tiles (CTAS = 2: each holds its 128
 // rows of A and of the result and half of B, so B crosses shared memory once for 256 rows). One
-// thread per operand streams 64-deep tiles into a ring of shared memory by TMA, one thread (of the
+// warp per operand streams 64-deep tiles into a ring of shared memory by TMA, one warp (of the
 // pair's leader) issues tcgen05.mma (bf16 operands, f32 accumulators in tensor
 // memory), and eight warps turn finished accumulators into the mode's output while the next tile's
 // products already run: tensor memory holds two accumulators of 256 columns.
@@ -28,11 +28,11 @@
 // bf16 results are cut every 16384 of K, 1e-4 of the sum at most, where their own rounding is 4e-3.
 // Measured at rows 1024, dim 1024, vocabulary 32000, f32: dH 9.6e-6 off without chunks, 4.2e-7 with
 // chunks of 128 (9.2e-7 with 256, 2.5% faster); the bf16 loss of 4096 x 4096 x 16384 with chunks of 512,
-// 1024, 2048 and none: 317, 301, 294, 291 us.
+// 1024, 2048 and none: 317, 301, 294, 291 us (of 1024, as here, 280 since the issuing warp works as a whole).
 //
 // What bounds it: the operands' way into shared memory. A bf16 stage brings 32 KB for the 512 cycles of
-// its products, 64 bytes a cycle, and the tensor pipe is 80 to 86% busy (307 to 317 us for each of the four
-// products at 4096 x 4096 x 16384, 1,740 to 1,790 TFLOP/s; P, uncut, 303); an f32 stage brings half of that a cycle, and
+// its products, 64 bytes a cycle, and the tensor pipe is 87 to 94% busy (280 to 301 us for each of the
+// products at 4096 x 4096 x 16384, 1,820 to 1,960 TFLOP/s); an f32 stage brings half of that a cycle, and
 // the pipe is 93 to 96% busy. Then the power cap: back to back the clock falls from 1.9 to 1.65 GHz.
 //
 // P and the copies of H and W are stored in panels of 64 columns ([plane][panel][row][64]), so that
