@@ -51,7 +51,7 @@ __device__ __forceinline__ void load8(const Source &q, const T *item, uint32_t a
         __align__(16) T v[8];
 #pragma unroll
         for (int e = 0; e < static_cast<int>(sizeof(v) / 16); ++e)
-            reinterpret_cast<uint4 *>(v)[e] = __ldg(reinterpret_cast<const uint4 *>(p) + e);
+            reinterpret_cast<uint4 *>(v)[e] = reinterpret_cast<const uint4 *>(p)[e];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = static_cast<float>(v[e]);
     } else {

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 16 && sizeof(T) == 2 ? 2 
         for (int i = 0; i < NC; i += PER) {
             __align__(16) T v[PER];
             if (i + PER <= held) {
-                *reinterpret_cast<uint4 *>(v) = __ldg(reinterpret_cast<const uint4 *>(g + i));
+                *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(g + i);
             } else {
 #pragma unroll
                 for (int e = 0; e < PER; ++e) v[e] = i + e < held ? g[i + e] : T(0.f);

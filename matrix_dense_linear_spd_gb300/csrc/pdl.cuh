@@ -3,6 +3,8 @@
 // writes are visible. Every kernel launched this way calls pdl_wait() in all its threads before it
 // touches global memory, so a kernel that ends has everything before it in the stream done. Saves
 // about 2 us between two short kernels.
+// Such a kernel has no non-coherent loads (__ldg, or a __restrict__ pointer that lets the compiler make them): they are taken
+// to be of memory that nothing writes while the kernel runs, so they may be moved above the wait.
 #pragma once
 
 #include <cuda_runtime.h>
