@@ -131,7 +131,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// One lane of a converged warp.
+// One lane of a converged warp, the same one every time (which one is not said).
 __device__ __forceinline__ bool elect() {
     uint32_t r;
     asm volatile(

@@ -725,10 +725,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok && lane == 0) {
-                gave_up = 1;
-                tc::mma_commit_all<CTAS>(&drained);
-                tc::mbar_wait(&drained, 0, kPolls);
+            if (!ok) {
+                // by the lane that issued: a commit covers its own thread's products
+                if (tc::elect()) {
+                    gave_up = 1;
+                    tc::mma_commit_all<CTAS>(&drained);
+                    tc::mbar_wait(&drained, 0, kPolls);
+                }
             }
         }
       }
