@@ -300,10 +300,13 @@ bl_status run(const Plan &q, const Call &c) {
     BL_MAP(map_f16(&a_out, q.a, q.small, q.small, PLANES, q.lda, 32, LINE));
     BL_MAP(map_f16(&b_out, q.b, q.small, q.small, PLANES, q.lda, 32, LINE));
     for (int i = 0; i < 2; ++i) BL_MAP(map_f16(&x_out[i], q.x[i], q.width, q.lines, 2, q.ldx, 32, LINE));
-    const bool by_tma = for_tma(c.X, c.ldx, sizeof(T)) && (q.batch == 1 || c.stride_x * static_cast<int64_t>(sizeof(T)) % 16 == 0);
+    // A tensor map's items are whole lines apart, as many as an item has or more: items in each other's gaps, or at other
+    // distances, are stored without TMA.
+    const int64_t line_x = q.lines == 1 && q.batch > 1 ? c.stride_x : c.ldx, item_x = q.batch == 1 ? line_x * q.lines : c.stride_x;
+    const bool by_tma = for_tma(c.X, line_x, sizeof(T)) && item_x % line_x == 0 && item_x / line_x >= q.lines;
     if (by_tma)
         BL_MAP(make_map(&user_out, PLANES == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sizeof(T), c.X, q.width,
-                        q.lines, q.batch, c.ldx, q.batch == 1 ? c.ldx * q.lines : c.stride_x, 32));
+                        q.lines, q.batch, line_x, item_x, 32));
 
     const auto args = [&](const Shape &s, int64_t rows, int64_t cols, int64_t k) {
         Args r{};
