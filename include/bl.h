@@ -261,7 +261,7 @@ int64_t bl_score_workspace(bl_dtype dtype, int64_t rows, int64_t dim, int64_t vo
  * The norm is right to f32's accuracy for any finite values. A matrix of zeros gives zeros, one that holds infinity or NaN gives NaN.
  * a X is formed from 22 bits of X in f32. The products take f16 operands, of 11 bits for bf16 and of 22 bits for
  * f32 matrices, and add in f32. Between steps X must stay below 8, and A and b A + c A A below 16, in every element,
- * as the coefficients above keep them; beyond that the result is not finite. The same call gives the same bits every time, and a matrix
+ * as the coefficients above keep them; beyond that the result is not finite. (What the last step gives may be larger.) The same call gives the same bits every time, and a matrix
  * the same bits whatever else is in the batch. A kernel that gave up waiting makes all of X NaN.
  */
 bl_status bl_orth(bl_dtype dtype, int64_t rows, int64_t cols, int64_t batch, const void *G, int64_t ldg,

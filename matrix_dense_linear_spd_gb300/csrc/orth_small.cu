@@ -212,7 +212,6 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 16 && sizeof(T) == 2 ? 2 
     const int rows = q.share == 1 ? (q.m + 15) & ~15 : kRows;            // of A and B
     const int cols = (q.n + 31) & ~31;                                   // X is zero from n on
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint32_t largest = 0;
     bool ok = true;
     // One thread issues a product, all wait for it: A = X X^T (of_x), A A, or B X (apply)
     const auto product = [&](int parity, bool of_x, bool apply, int k, int n) {
@@ -287,6 +286,7 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 16 && sizeof(T) == 2 ? 2 
         }
         // X
         product(step & 1, false, true, rows, cols);
+        uint32_t largest = 0;
 #pragma unroll
         for (int h = 0; h < NC; h += READ) {
             if (c0 + h >= cols) break;
@@ -297,11 +297,14 @@ __global__ void __launch_bounds__(kSmallThreads, NC == 16 && sizeof(T) == 2 ? 2 
                 largest = max(largest, __float_as_uint(x[h + i]) & 0x7fffffffu);        // NaN is larger than infinity
             }
         }
-        if (step + 1 < q.steps) x_out();
+        // between steps X is f16, the last one is not
+        const bool last = step + 1 == q.steps;
+        bad |= largest > __float_as_uint(last ? 3.4028235e38f : 65504.f);
+        if (!last) x_out();
     }
     // what a matrix or a product lost is seen in all of it
     if (!ok) tc::mbar_wait(&bar, 0, kPolls), tc::mbar_wait(&bar, 1, kPolls);         // what gave up may still come to its end
-    bad |= !ok || q.spoil || largest > __float_as_uint(65504.f);
+    bad |= !ok || q.spoil;
     if (bad && slot < 8) lost[slot] = 1;
     __syncthreads();
     bad = slot < 8 && lost[slot];
