@@ -417,7 +417,8 @@ bl_status bl_orth(bl_dtype dtype, int64_t rows, int64_t cols, int64_t batch, con
     if (steps < 1 || steps > 64) return fail(BL_ERR_INVALID_ARGUMENT, "orth: steps=%d outside [1, 64]", steps);
     if (!coefficients || !std::isfinite(coefficients[0]) || !std::isfinite(coefficients[1]) || !std::isfinite(coefficients[2]))
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: coefficients are NULL or not finite");
-    if (!fits_small(cols, rows) && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
+    if (fits_small(cols, rows)) workspace = nullptr, workspace_bytes = 0;          // not looked at
+    else if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: workspace is NULL or not 256-byte aligned");
     Call c{G, ldg, stride_g, X, ldx, stride_x, steps, coefficients, static_cast<char *>(workspace), bl::sm_count(),
            reinterpret_cast<cudaStream_t>(stream)};
