@@ -375,7 +375,7 @@ bl_status check_matrix(const char *name, const void *p, int64_t ld, int64_t stri
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: %s is NULL or not aligned to its %lld-byte element", name, (long long)es);
     if (cols > 1 && ld < rows)
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: ld of %s is %lld < rows=%lld", name, (long long)ld, (long long)rows);
-    if (ld < 0 || ld > (int64_t(1) << 32)) return fail(BL_ERR_INVALID_ARGUMENT, "orth: ld of %s is %lld, too large", name, (long long)ld);
+    if (cols > 1 && ld > (int64_t(1) << 32)) return fail(BL_ERR_INVALID_ARGUMENT, "orth: ld of %s is %lld, too large", name, (long long)ld);
     if (batch > 1 && (stride < 0 || stride > (int64_t(1) << 36)))
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: stride of %s is %lld, negative or too large", name, (long long)stride);
     return BL_SUCCESS;

@@ -30,3 +30,16 @@ def test_a_workspace_that_is_not_needed_is_not_looked_at(rows, cols):
         X = torch.zeros_like(G)
         assert call(G, X, rows, cols, ws=ws, ws_bytes=size) == 0, (ws, size, bl.get_lib().bl_last_error())
         assert torch.equal(X, want)
+
+
+@pytest.mark.parametrize("rows", [50, 3000])
+def test_one_column_has_no_leading_dimension(rows):
+    torch, bl = torch_cuda(), lib()
+    G = torch.randn(1, rows, device="cuda")
+    want = bl.orth(G)
+    need = bl.get_lib().bl_orth_workspace(bl.BL_F32, rows, 1, 1)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    for ld in (0, 1, -7, 1 << 40):
+        X = torch.zeros_like(G)
+        assert call(G, X, rows, 1, ldg=ld, ldx=ld, ws=ws.data_ptr(), ws_bytes=need) == 0, (ld, bl.get_lib().bl_last_error())
+        assert torch.equal(X, want)
