@@ -252,9 +252,9 @@ PyObject *do_xent_grad(PyObject *const *a) {
 // ------------------------------------------------------------------ score, score_grad
 
 PyObject *do_score(PyObject *const *a) {
-    const Xent c(a[0], a[1], a[2]);
-    const int64_t top = PyLong_AsLongLong(a[3]);
+    const int64_t top = PyLong_AsLongLong(a[3]);          // may run the caller's code: before the tensors are looked at
     if (top == -1 && PyErr_Occurred()) throw Refused();
+    const Xent c(a[0], a[1], a[2]);
     On on(c.h.device(), a[4]);
     const int64_t need = bl_score_workspace(c.code, c.rows, c.dim, c.vocab, top, c.h.data_ptr(), c.ldh, c.w.data_ptr(), c.ldw);
     if (need < 0) failed(BL_ERR_INVALID_ARGUMENT);
@@ -311,21 +311,22 @@ struct Lines {
 };
 
 PyObject *do_orth(PyObject *const *a) {
+    // Reading a number may run the caller's code, which may change the list or the tensors: numbers first, from a copy.
+    const long steps = PyLong_AsLong(a[1]);
+    if (steps == -1 && PyErr_Occurred()) throw Refused();
+    Ref list(PySequence_Fast(a[2], "coefficients must be three numbers")), three(PySequence_Tuple(list.o));
+    if (PyTuple_GET_SIZE(three.o) != 3) refuse(PyExc_ValueError, "coefficients must be three numbers");
+    double coefficients[3];
+    for (int i = 0; i < 3; ++i) {
+        coefficients[i] = PyFloat_AsDouble(PyTuple_GET_ITEM(three.o, i));
+        if (PyErr_Occurred()) throw Refused();
+    }
     const at::Tensor &g = tensor(a[0], "G");
     if (g.scalar_type() != at::kFloat && g.scalar_type() != at::kBFloat16)
         refuse(PyExc_TypeError, "unsupported dtype %s", c10::toString(g.scalar_type()));
     const bl_dtype code = g.scalar_type() == at::kFloat ? BL_F32 : BL_BF16;
     if (g.dim() != 2 && g.dim() != 3) refuse(PyExc_ValueError, "G must be (rows, cols) or (batch, rows, cols)");
     if (!g.is_cuda()) refuse(PyExc_ValueError, "G must be a CUDA tensor");
-    const long steps = PyLong_AsLong(a[1]);
-    if (steps == -1 && PyErr_Occurred()) throw Refused();
-    Ref three(PySequence_Fast(a[2], "coefficients must be three numbers"));
-    if (PySequence_Fast_GET_SIZE(three.o) != 3) refuse(PyExc_ValueError, "coefficients must be three numbers");
-    double coefficients[3];
-    for (int i = 0; i < 3; ++i) {
-        coefficients[i] = PyFloat_AsDouble(PySequence_Fast_GET_ITEM(three.o, i));
-        if (PyErr_Occurred()) throw Refused();
-    }
     at::Tensor out;
     if (a[3] != Py_None) {
         out = tensor(a[3], "out");
