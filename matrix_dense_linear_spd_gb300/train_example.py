@@ -37,7 +37,8 @@ def precondition(x, grad, mu=1e-2):
 
 
 def orthogonal(grad):
-    """The gradient with singular values of about 1, at the scale that a weight of its shape has."""
+    """The gradient with singular values of about 1, at the scale that a weight of its shape has: it is given as the
+    weight is stored (turned it may have another scale)."""
     return bl.orth(grad) * max(1.0, grad.shape[0] / grad.shape[1]) ** 0.5
 
 
@@ -51,7 +52,7 @@ def step(params, x, target, lr, max_norm, orth=False):
     dh, dW = bl.xent_grad(h, W, target, lse, g)
     dA = x.T @ (dh * (1 - h * h))
     if orth:
-        step_A, step_W = orthogonal(dA), orthogonal(dW.T)
+        step_A, step_W = orthogonal(dA), orthogonal(dW).T
         info_A = info_W = torch.zeros(1, dtype=torch.int32, device=x.device)
     else:
         step_A, info_A = precondition(x, dA)
