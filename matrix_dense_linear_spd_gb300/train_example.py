@@ -21,6 +21,7 @@ import torch
 import matrix_dense_linear_spd_gb300 as bl
 
 BLOCK = 32
+SIDE = 1 << 16                # rows that one orthogonalisation takes
 
 
 def precondition(x, grad, mu=1e-2):
@@ -38,8 +39,8 @@ def precondition(x, grad, mu=1e-2):
 
 def orthogonal(grad):
     """The gradient with singular values of about 1, at the scale that a weight of its shape has: it is given as the
-    weight is stored (turned it may have another scale)."""
-    return bl.orth(grad) * max(1.0, grad.shape[0] / grad.shape[1]) ** 0.5
+    weight is stored (turned it may have another scale). Rows beyond SIDE go in blocks, each by itself."""
+    return torch.cat([bl.orth(b) * max(1.0, b.shape[0] / b.shape[1]) ** 0.5 for b in grad.split(SIDE)])
 
 
 def step(params, x, target, lr, max_norm, orth=False):
