@@ -319,7 +319,8 @@ def score(H, W, target, top=0, stream=None):
     (logp, entropy, lse, top_logp, top_id). logp, entropy and lse are f32, one value a row; top_logp (f32) and
     top_id (int64) are (rows, top): each row's `top` (0 to 32) likeliest tokens, the likeliest first and of equal
     ones the lowest first. A row whose target lies outside [0, vocab) does not count: 0, and -1 in top_id. A row
-    with a logit that is infinite or NaN has NaN, and -1 in top_id. The results carry no autograd graph; score_grad
+    with a logit of plus infinity or NaN, or of minus infinity only, has NaN, and -1 in top_id; other logits of minus
+    infinity have no share. The results carry no autograd graph; score_grad
     gives the gradients of logp and entropy."""
     return (_binding or _training()).score(H, W, target, top, _raw(stream))
 

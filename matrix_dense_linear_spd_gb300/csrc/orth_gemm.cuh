@@ -21,8 +21,8 @@
 // would round, up to 2^-23.4 of the sum a step for the diagonal of A.
 //
 // What bounds it: for large matrices the operands' way into shared memory, 64 bytes a cycle and SM at full rate, and the
-// power cap (8192 x 4096 bf16: tensor pipe 84% busy in A, 76 to 81% in B X, whose addend and result take their share of L2;
-// 1,360 TFLOP/s over the call); for small ones latency, some 5 us a product: 1.4 from the end of one kernel to the start
+// power cap (8192 x 4096 bf16: tensor pipe 84% busy in A, 76 to 82% in B X, whose addend and result take their share of L2;
+// 1,340 to 1,390 TFLOP/s over the call); for small ones latency, some 5 us a product: 1.4 from the end of one kernel to the start
 // of the next, 1.3 to the first operands, 2.5 from the last product to the end.
 #pragma once
 
@@ -69,7 +69,7 @@ __device__ __forceinline__ float2 scale_of(double sum) {
 // turns between two halves. TMA takes as long for a line of 64 bytes as for one of 128, some two cycles, and the
 // operands alone keep it busy (a 256 x 256 tile's stage 512 cycles, as long as its products), so lines are 128 bytes where
 // there is room: 8192 x 4096 bf16, five steps 1898 us with lines of 64 bytes, 1855 of 128. (These two, and those
-// at the order of tiles below, were taken with one thread issuing products and copies; 1735 to 1770 with whole warps. Lines
+// at the order of tiles below, were taken with one thread issuing products and copies; 1735 to 1795 with whole warps. Lines
 // read and written with 16 bytes a lane instead took 1705, but 12 x 1024 x 4096 971 in place of 910 and 512 x 512 no less.)
 // A stage is as small as the tile's columns allow: narrow tiles, of small matrices, wait for memory, and the more
 // of their stages are on their way the better.
@@ -100,7 +100,7 @@ struct Args {
     __half *result;            // GRAM, SQUARE: [plane][item][rows][result_ld], for what lies above the diagonal
     int64_t result_ld;
     bool last;                 // APPLY: the result is the caller's, f32 or bf16
-    void *out;                 // where its lines do not start on 16-byte boundaries: stored without TMA
+    void *out;                 // where its lines or items are not where a tensor map has them: stored without TMA
     int64_t ldo, stride_o;
     bool rows_first;           // APPLY: the order of tiles
     int group;

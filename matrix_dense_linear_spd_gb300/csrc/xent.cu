@@ -239,7 +239,7 @@ constexpr int few_smem(int R) { return 200 * 1024 / few_ctas(R); }      // H's s
 
 // With SCORE it leaves the entropy's sums too, and the logits (or null). The warp's sums then come apart over its
 // lanes, each of which goes on with one row and one of the entries (31 exchanges for eight rows, not 160, and one
-// exponential, not 32): 8 f32 rows x 128 x 100000 22 us, where the loss, whose lanes all do the same, takes 39.
+// exponential, not 32): 8 f32 rows x 128 x 100000 23 us a call, where the loss, whose lanes all do the same, takes 39.
 // Lanes that hold the same sum, where there are fewer than 32, differ in the lowest bits.
 template <int N>
 __device__ __forceinline__ float sum_apart(float (&a)[N]) {

@@ -424,8 +424,8 @@ __device__ __forceinline__ void end(const Row &r, const GemmArgs &a, const Work 
                 if (blocks == 3) most[0] = r.blocks.y, most[1] = r.blocks.z, most[2] = r.blocks.w;
                 if (blocks == 2) most[0] = r.blocks.z, most[1] = r.blocks.w;
                 if (blocks == 1) most[0] = r.blocks.w;
-                // parts in turn, those that have columns: a tile of 128 or 64 is one part (numbered as two it left every other of an
-                // even number of slots at minus infinity, and the floor with them)
+                // parts in turn, those that have columns: a tile of 128 or 64 is one part (as two it left every other of an even
+                // number of slots at minus infinity, and the floor with them: 128 f32 rows x 64 x 200000, 20 alternatives 166 us, 139 so)
                 if (a.top > 0 && a.slots && r.top > r.floor)
                     atomicMax(a.slots + static_cast<int64_t>(r.row) * a.slot_ld + (a.tile_n > kHalf ? 2 * w.tn + half : w.tn) % a.top,
                               in_order(__float_as_int(r.top)));
