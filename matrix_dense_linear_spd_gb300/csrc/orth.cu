@@ -381,6 +381,18 @@ bl_status check_matrix(const char *name, const void *p, int64_t ld, int64_t stri
     return BL_SUCCESS;
 }
 
+// Whether no two items share an element: one after the other, side by side in the gaps of each other's columns, or wherever
+// else no column of the d-th item after one meets any of its own.
+bool items_apart(int64_t rows, int64_t cols, int64_t batch, int64_t ld, int64_t stride) {
+    const int64_t extent = (cols - 1) * ld + rows;
+    if (stride >= extent || (stride >= rows && (batch - 1) * stride + rows <= ld)) return true;
+    for (int64_t d = 1; d < batch && d * stride < extent; ++d) {
+        const int64_t column = d * stride / ld, past = d * stride - column * ld;      // where that item's first column starts
+        if ((column < cols && past < rows) || (column + 1 < cols && ld - past < rows)) return false;
+    }
+    return true;
+}
+
 }  // namespace orth
 }  // namespace bl
 
@@ -410,10 +422,7 @@ bl_status bl_orth(bl_dtype dtype, int64_t rows, int64_t cols, int64_t batch, con
     if (st == BL_SUCCESS) st = check_matrix("X", X, ldx, stride_x, rows, cols, batch, es);
     if (st != BL_SUCCESS) return st;
     if (cols == 1) ldg = ldx = rows;
-    // items of X one after the other, or side by side in each other's columns' gaps
-    const int64_t extent = (cols - 1) * ldx + rows;
-    if (batch > 1 && stride_x < extent && (stride_x < rows || (batch - 1) * stride_x + rows > ldx))
-        return fail(BL_ERR_INVALID_ARGUMENT, "orth: items of X overlap");
+    if (batch > 1 && !items_apart(rows, cols, batch, ldx, stride_x)) return fail(BL_ERR_INVALID_ARGUMENT, "orth: items of X overlap");
     if (steps < 1 || steps > 64) return fail(BL_ERR_INVALID_ARGUMENT, "orth: steps=%d outside [1, 64]", steps);
     if (!coefficients || !std::isfinite(coefficients[0]) || !std::isfinite(coefficients[1]) || !std::isfinite(coefficients[2]))
         return fail(BL_ERR_INVALID_ARGUMENT, "orth: coefficients are NULL or not finite");

@@ -1,5 +1,5 @@
-"""Orthogonalised steps of matrices beyond the small kernel's, whose items lie in each other's gaps or at distances
-that are no multiple of a line's: G and results alike, the same bits as for contiguous ones, gaps as they were."""
+"""Orthogonalised steps of matrices, most of them beyond the small kernel's, whose items lie in each other's gaps or at
+distances that are no multiple of a line's: G and results alike, the same bits as for contiguous ones, gaps as they were."""
 import pytest
 
 from _gpu import lib, torch_cuda
@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 # batch, lines, width, distance of the items, of the lines (in values; both multiples of 16 bytes, but for the last)
 LAYOUTS = [(3, 300, 160, 160, 480), (3, 300, 160, 168, 504), (2, 200, 304, 304, 608), (4, 150, 264, 264, 8 * 264), (2, 300, 160, 300 * 160 + 8, 160),
            (2, 300, 160, 304 * 160, 160), (2, 300, 160, 300 * 168, 168), (2, 300, 160, 300 * 168 + 16, 168), (4, 1, 400, 400, 400), (4, 1, 400, 408, 400),
-           (4, 1, 400, 1200, 400), (3, 2, 600, 600, 1800), (3, 300, 150, 150, 450)]
+           (4, 1, 400, 1200, 400), (3, 2, 600, 600, 1800), (3, 300, 150, 150, 450),
+           (2, 3, 400, 1500, 1000), (2, 3, 40, 150, 100), (50, 4, 10, 250, 100), (2, 300, 160, 80 * 320 + 160, 320)]
 
 
 def view(flat, layout):
